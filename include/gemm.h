@@ -91,8 +91,9 @@ typedef enum { GEMM_ROW_MAJOR = 0, GEMM_COL_MAJOR = 1 } gemm_layout_t;
  * The three are multiplied with fp32 accumulation into fp32, fp16 or bf16
  * outputs (the fused epilogue of gemm_run_ep included), with A row-major
  * and B column-major (both K-contiguous; other storage orders return
- * GEMM_ERR_UNSUPPORTED).  INT8 is not offered: the sm_103a tensor cores have no
- * tcgen05.mma kind::i8 (ptxas rejects it for this target). */
+ * GEMM_ERR_UNSUPPORTED).  8-bit integers are not an input type of a plan: the
+ * sm_103a tensor cores have no tcgen05.mma kind::i8 (ptxas rejects it for this
+ * target).  gemm_run_i8 multiplies them on a GEMM_F16 plan. */
 typedef enum {
     GEMM_F16 = 0,
     GEMM_BF16 = 1,
@@ -383,6 +384,51 @@ gemm_status_t gemm_schedule_model(int sm_count, gemm_dtype_t in_dtype, int64_t M
                                   gemm_dtype_t accum_dtype, gemm_dtype_t out_dtype,
                                   gemm_division_t division, int division_splits, int unit,
                                   int32_t *items, int max_items, int *n_items, int *n_units);
+
+/* Product of 8-bit integers with a scale for each token and channel, on a
+ * GEMM_F16 plan:
+ *
+ *     D[i,j] = act(rs[i] * cs[j] * sum_k A[i,k] B[k,j] + bias[j])
+ *
+ * A is M x K row-major (tokens), B is K x N column-major (a weight matrix
+ * with one row of K codes per output channel), both int8 with lda, ldb >= K
+ * counted in elements; D is row-major, ldd >= N, GEMM_F32, GEMM_F16 or
+ * GEMM_BF16.  rs, cs, bias and act are the fields row_scale, col_scale, bias
+ * and act of `ep` (NULL: 1, 1, 0 and none).  A and B start on 16-byte
+ * boundaries and lda and ldb are multiples of 16 (K may be anything); D needs
+ * element alignment.
+ *
+ * The codes are multiplied as fp16 values with fp32 accumulation, so a sum is
+ * exact while its partial sums stay below 2^24 in magnitude (always for
+ * K <= 1040) and is rounded as an fp32 sum beyond; scales, bias and activation
+ * are applied in fp32 and D is rounded once, to nearest even.
+ *
+ * Errors, streams and the plan's rules are gemm_run's; a plan of another input
+ * type returns GEMM_ERR_UNSUPPORTED.  The plan keeps a workspace, which the
+ * first call of a larger problem grows with cudaMalloc (a stream capture has
+ * to follow a call of its size). */
+gemm_status_t gemm_run_i8(gemm_plan_t plan, const int8_t *A, const int8_t *B, void *D, int64_t M, int64_t N,
+                          int64_t K, int64_t lda, int64_t ldb, int64_t ldd, gemm_dtype_t out_dtype,
+                          const gemm_epilogue_t *ep, void *stream);
+
+/* gemm_run_i8 on rows of floating-point values X (M x K, row-major, ldx >= K,
+ * GEMM_F32, GEMM_F16 or GEMM_BF16, element alignment): the call quantises
+ * each row as gemm_quantize_rows_i8 does and uses the scales as rs, so
+ * ep->row_scale has to be NULL. */
+gemm_status_t gemm_run_i8_dynamic(gemm_plan_t plan, const void *X, gemm_dtype_t x_dtype, const int8_t *B, void *D,
+                                  int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldb, int64_t ldd,
+                                  gemm_dtype_t out_dtype, const gemm_epilogue_t *ep, void *stream);
+
+/* Symmetric 8-bit quantisation of the R rows of X (row-major, K columns,
+ * ldx >= K; GEMM_F32, GEMM_F16 or GEMM_BF16):
+ *     scale[i] = max_k |X[i,k]| / 127,   Q[i,k] = round(X[i,k] / scale[i])
+ * in fp32 (IEEE divisions, rounding half to even), codes -127..127.  A row of
+ * zeros has scale 0 and codes 0; a row with an infinity or a NaN has that as
+ * its scale.  Used on tokens, and on the rows of a weight matrix for the
+ * scales of its channels.  Q is row-major, ldq >= K; K == 0 writes scales of
+ * 0.  One kernel on `stream` of `device`; no plan and no allocation. */
+gemm_status_t gemm_quantize_rows_i8(int device, const void *X, gemm_dtype_t x_dtype, int64_t R, int64_t K,
+                                    int64_t ldx, int8_t *Q, int64_t ldq, float *scale, void *stream);
 
 /* gemm_run for callers that cannot allocate device memory.  The paper has no
  * counterpart to this entry point: its kernels need no workspace at all.

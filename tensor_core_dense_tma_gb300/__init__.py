@@ -25,6 +25,7 @@ import os
 import threading
 
 from . import build as _build_mod
+from . import logits as _logits
 
 __all__ = [
     "abi", "load", "Plan", "GemmError", "STATUS", "DTYPE", "LAYOUT",
@@ -36,6 +37,9 @@ __all__ = [
     "gemm_run_prior_art", "PRIOR_ART", "gemm_mma_fragment_map", "run_prior_art", "gemm_describe_model", "gemm_schedule_model",
     "gemm_plan_device_status_async", "gemm_plan_tensor_map_stats", "gemm_static_scratch_device_status",
     "gemm_plan_host_trace", "gemm_plan_host_trace_read",
+    "gemm_run_i8", "gemm_run_i8_dynamic", "gemm_quantize_rows_i8", "quantize_rows_i8",
+    "token_logprobs", "token_logprobs_grad", "distill_topk", "distill_topk_grad", "TokenLogprobs",
+    "TokenLogprobsGrad",
 ]
 
 STATUS = {
@@ -133,6 +137,14 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.gemm_run_static_scratch.argtypes = [i32, i32, p, p, p, p, i64, i64, i64, i64, i64, i64, i32, i32, i32,
                                             i32, f32, f32, i32, p]
     lib.gemm_run_static_scratch.restype = i32
+    lib.gemm_run_i8.argtypes = [p, p, p, p, i64, i64, i64, i64, i64, i64, i32, ctypes.POINTER(Epilogue), p]
+    lib.gemm_run_i8.restype = i32
+    lib.gemm_run_i8_dynamic.argtypes = [p, p, i32, p, p, i64, i64, i64, i64, i64, i64, i32,
+                                        ctypes.POINTER(Epilogue), p]
+    lib.gemm_run_i8_dynamic.restype = i32
+    lib.gemm_quantize_rows_i8.argtypes = [i32, p, i32, i64, i64, i64, p, i64, p, p]
+    lib.gemm_quantize_rows_i8.restype = i32
+    _logits.declare(lib)
     lib.gemm_status_string.argtypes = [i32]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_measure_mma_rate.argtypes = [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_double),
@@ -397,6 +409,21 @@ def gemm_run_static_scratch(device, in_dtype, A, B, C, D, M, N, K, lda, ldb, ldc
                                           DTYPE[out_dtype], alpha, beta, splits, stream)
 
 
+def gemm_run_i8(plan, A, B, D, M, N, K, lda, ldb, ldd, out_dtype, ep: Epilogue | None, stream) -> int:
+    return load().gemm_run_i8(plan, A, B, D, M, N, K, lda, ldb, ldd, DTYPE[out_dtype],
+                              ctypes.byref(ep) if ep is not None else None, stream)
+
+
+def gemm_run_i8_dynamic(plan, X, x_dtype, B, D, M, N, K, ldx, ldb, ldd, out_dtype, ep: Epilogue | None,
+                        stream) -> int:
+    return load().gemm_run_i8_dynamic(plan, X, DTYPE[x_dtype], B, D, M, N, K, ldx, ldb, ldd, DTYPE[out_dtype],
+                                      ctypes.byref(ep) if ep is not None else None, stream)
+
+
+def gemm_quantize_rows_i8(device, X, x_dtype, R, K, ldx, Q, ldq, scale, stream) -> int:
+    return load().gemm_quantize_rows_i8(device, X, DTYPE[x_dtype], R, K, ldx, Q, ldq, scale, stream)
+
+
 def gemm_status_string(status: int) -> str:
     return load().gemm_status_string(status).decode()
 
@@ -456,6 +483,44 @@ def _make_epilogue(M, N, bias, row_scale, col_scale, act):
             raise ValueError(f"{what} must be a contiguous fp32 device vector of length {n}")
         return v.data_ptr()
     return Epilogue(vec(bias, N, "bias"), vec(row_scale, M, "row_scale"), vec(col_scale, N, "col_scale"), ACT[act])
+
+
+def _row_stride(t, what: str) -> int:
+    """Row stride of a row-major 2-D device tensor."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D device tensor")
+    r, c = t.shape
+    s0, s1 = t.stride()
+    if (c > 1 and s1 != 1) or (r > 1 and s0 < c):
+        raise ValueError(f"{what} must be row-major (strides {t.stride()})")
+    return s0 if r > 1 else max(s0, c)
+
+
+def quantize_rows_i8(X, Q=None, scale=None, *, stream=None):
+    """Symmetric 8-bit quantisation of the rows of a row-major fp32, fp16 or
+    bf16 device matrix (see gemm_quantize_rows_i8): returns (Q, scale), the
+    int8 codes and one fp32 scale per row, X ~ Q * scale[:, None].  An
+    allocated Q has rows on 16-byte boundaries, ready for Plan.gemm_i8."""
+    import torch
+    ldx = _row_stride(X, "X")
+    dt = _dt_name(X)
+    R, K = X.shape
+    if Q is None:
+        Q = torch.empty((R, max(16, -(-K // 16) * 16)), dtype=torch.int8, device=X.device)[:, :K]
+    if scale is None:
+        scale = torch.empty((R,), dtype=torch.float32, device=X.device)
+    if Q.dtype != torch.int8 or Q.shape != (R, K) or Q.device != X.device:
+        raise ValueError("Q must be an int8 matrix of X's shape on its device")
+    if scale.dtype != torch.float32 or scale.shape != (R,) or scale.device != X.device or not scale.is_contiguous():
+        raise ValueError("scale must be a contiguous fp32 vector with one entry per row on X's device")
+    ldq = _row_stride(Q, "Q")
+    if stream is None:
+        stream = torch.cuda.current_stream(X.device).cuda_stream
+    st = gemm_quantize_rows_i8(X.device.index, X.data_ptr(), dt, R, K, ldx, Q.data_ptr(), ldq, scale.data_ptr(),
+                               stream)
+    if st != 0:
+        raise GemmError(st, "gemm_quantize_rows_i8")
+    return Q, scale
 
 
 class Plan:
@@ -557,6 +622,67 @@ class Plan:
         ep = _make_epilogue(M, N, bias, row_scale, col_scale, act)
         self.run_raw(A.data_ptr(), B.data_ptr(), C.data_ptr() if C is not None else None, D.data_ptr(),
                      M, N, K, lda, ldb, max(ldc, N), la, lb, accum_dtype, out_dtype, alpha, beta, stream, ep=ep)
+        return D
+
+    def _resolve_i8(self, A, B, D, out_dtype):
+        """Sizes and strides of an 8-bit product (D allocated if not given)."""
+        import torch
+        lda = _row_stride(A, "A")
+        M, K = A.shape
+        if B.dtype != torch.int8 or B.dim() != 2 or not B.is_cuda:
+            raise ValueError("B must be a 2-D int8 device tensor")
+        if B.shape[0] != K:
+            raise ValueError("inner dimensions differ")
+        N = B.shape[1]
+        if K > 1 and B.stride(0) != 1:
+            raise ValueError("B must be column-major: the transpose of a row-major N x K weight matrix")
+        ldb = B.stride(1) if N > 1 else -(-max(K, 1) // 16) * 16
+        if M == 1:
+            lda = -(-max(K, 1) // 16) * 16 if A.dtype == torch.int8 else K
+        if D is None:
+            D = torch.empty((M, N), dtype=getattr(torch, _TORCH_DT[out_dtype or "f32"]), device=A.device)
+        elif out_dtype is not None and _dt_name(D) != out_dtype:
+            raise ValueError("D must have the output type")
+        if D.shape != (M, N):
+            raise ValueError("D must be an M x N matrix")
+        if not (A.device == B.device == D.device):
+            raise ValueError("A, B and D must be on one device")
+        return M, N, K, lda, ldb, _row_stride(D, "D"), _dt_name(D), D
+
+    def gemm_i8(self, A, B, D=None, *, row_scale=None, col_scale=None, bias=None, act: str = "none",
+                out_dtype: str | None = None, stream=None):
+        """D = act(row_scale[i] * col_scale[j] * (A@B) + bias[j]) of int8
+        device tensors on an "f16" plan (gemm_run_i8): A row-major M x K,
+        B column-major K x N (``W.t()`` of row-major weights), the vectors
+        fp32; returns D (fp32 unless out_dtype or D says otherwise)."""
+        import torch
+        if A.dtype != torch.int8:
+            raise ValueError("A must be int8")
+        M, N, K, lda, ldb, ldd, out_dtype, D = self._resolve_i8(A, B, D, out_dtype)
+        ep = _make_epilogue(M, N, bias, row_scale, col_scale, act)
+        if stream is None:
+            stream = torch.cuda.current_stream(A.device).cuda_stream
+        st = gemm_run_i8(self.handle, A.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, lda, ldb, ldd, out_dtype, ep,
+                         stream)
+        if st != 0:
+            raise GemmError(st, "gemm_run_i8")
+        return D
+
+    def linear_i8(self, X, B, D=None, *, col_scale=None, bias=None, act: str = "none", out_dtype: str | None = None,
+                  stream=None):
+        """gemm_i8 of rows of fp32, fp16 or bf16 values: X (M x K, row-major)
+        is quantised row by row in the call (gemm_run_i8_dynamic); returns D
+        (X's type unless out_dtype or D says otherwise)."""
+        import torch
+        xt = _dt_name(X)
+        M, N, K, ldx, ldb, ldd, out_dtype, D = self._resolve_i8(X, B, D, out_dtype or (xt if D is None else None))
+        ep = _make_epilogue(M, N, bias, None, col_scale, act)
+        if stream is None:
+            stream = torch.cuda.current_stream(X.device).cuda_stream
+        st = gemm_run_i8_dynamic(self.handle, X.data_ptr(), xt, B.data_ptr(), D.data_ptr(), M, N, K, ldx, ldb, ldd,
+                                 out_dtype, ep, stream)
+        if st != 0:
+            raise GemmError(st, "gemm_run_i8_dynamic")
         return D
 
     def _resolve(self, A, B, C, D, out_dtype):
@@ -664,3 +790,9 @@ class Plan:
         if sync:
             s.synchronize()
         return D
+
+
+# operators on the rows of a logits matrix (logits.py)
+TokenLogprobs, TokenLogprobsGrad = _logits.TokenLogprobs, _logits.TokenLogprobsGrad
+token_logprobs, token_logprobs_grad = _logits.token_logprobs, _logits.token_logprobs_grad
+distill_topk, distill_topk_grad = _logits.distill_topk, _logits.distill_topk_grad

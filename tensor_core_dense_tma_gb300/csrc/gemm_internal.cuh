@@ -129,6 +129,8 @@ struct gemm_plan {
     bool attr_set[tcdt_host::kNumCfgKinds][8] = {};   // [kind][output slot + 4 * fused epilogue]
     int units[tcdt_host::kNumCfgKinds] = {};  // co-resident CTAs (single) or CTA pairs (pair)
     size_t ws_bytes = 0;          // capacity of d_ws
+    void* d_i8 = nullptr;         // gemm_run_i8's operands as fp16 codes and row scales (owned; null until used)
+    size_t i8_bytes = 0;          // capacity of d_i8
     int forced_kind = -1;         // gemm_plan_force_config
 #ifdef TCDT_FAULT_INJECTION
     int64_t fi_skip_load = -1;    // test builds only
