@@ -24,11 +24,18 @@
 #include <cstdint>
 
 #include "logits.h"
+#include "ptx_sm103.cuh"
 
 namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;               // 16-byte loads in flight per thread
+constexpr int kMaxCluster = 8;
+constexpr int kCandidates = 2048;        // kMaxCluster lists of LOGITS_MAX_TOP fit too
+constexpr int kSlack = 64;               // buckets more than wanted that are not worth telling ties apart
+constexpr int kStashVectors = 9;         // 16-byte vectors of a thread kept on chip with three CTAs an SM
+constexpr int kStashMost = 26;           // and with one
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kMaxExtent = 0x7FFFFFFF - 4096;
@@ -40,6 +47,7 @@ struct Args {
     const void* z;
     int64_t ld;
     int32_t V;
+    int cluster, stash;           // CTAs of a row; vectors of a thread kept in shared memory
     float c, inv_t, t;            // log2(e) / temperature, 1 / temperature, temperature
     const int64_t* tokens;        // [T], or teacher tokens [T][ldt]
     // log-probabilities
@@ -82,6 +90,14 @@ __device__ __forceinline__ float max_nan(float x, float lo) {
     return y;
 }
 
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t at) { return __uint_as_float(ld_cluster_u32(at)); }
+
 // Element types: kPer elements in a 16-byte vector.
 template <typename E>
 struct Ele;
@@ -89,7 +105,17 @@ struct Ele;
 template <>
 struct Ele<float> {
     static constexpr int kPer = 4;
+    static constexpr uint32_t kNegInf = 0xFF800000u;
     __device__ static float load(const float* p) { return *p; }
+    template <int N>
+    __device__ static float max_of(const uint4 (&q)[N]) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(q[k].x), __uint_as_float(q[k].y)),
+                               fmaxf(__uint_as_float(q[k].z), __uint_as_float(q[k].w))));
+        return m;
+    }
     __device__ static void unpack(const uint4& v, float (&x)[4]) {
         x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
         x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
@@ -103,6 +129,18 @@ struct Ele<float> {
 template <>
 struct Ele<__half> {
     static constexpr int kPer = 8;
+    static constexpr uint32_t kNegInf = 0xFC00FC00u;
+    template <int N>
+    __device__ static float max_of(const uint4 (&q)[N]) {
+        uint32_t none = kNegInf;
+        __half2 m = *reinterpret_cast<const __half2*>(&none);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const __half2* h = reinterpret_cast<const __half2*>(&q[k]);
+            m = __hmax2(m, __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+        }
+        return fmaxf(__half2float(__low2half(m)), __half2float(__high2half(m)));
+    }
     __device__ static float load(const __half* p) { return __half2float(*p); }
     __device__ static void unpack(const uint4& v, float (&x)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -127,6 +165,18 @@ struct Ele<__half> {
 template <>
 struct Ele<__nv_bfloat16> {
     static constexpr int kPer = 8;
+    static constexpr uint32_t kNegInf = 0xFF80FF80u;
+    template <int N>
+    __device__ static float max_of(const uint4 (&q)[N]) {
+        uint32_t none = kNegInf;
+        __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&none);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q[k]);
+            m = __hmax2(m, __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+        }
+        return fmaxf(__bfloat162float(__low2bfloat16(m)), __bfloat162float(__high2bfloat16(m)));
+    }
     __device__ static float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
     __device__ static void unpack(const uint4& v, float (&x)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -176,6 +226,17 @@ struct Row {
                      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                      : "l"(base + static_cast<int64_t>(v) * 16)
                      : "memory");
+        return r;
+    }
+    // vector v's bits, -inf outside the row and from vector `end` on
+    __device__ uint4 load_any(int v, int end) const {
+        if (v >= lo && v < hi && v < end) return load_whole(v);
+        uint4 r = make_uint4(Ele<E>::kNegInf, Ele<E>::kNegInf, Ele<E>::kNegInf, Ele<E>::kNegInf);
+        if (v < end) {
+            float x[kPer];
+            load(v, x);
+            r = Ele<E>::pack(x);     // exact: the values are of type E
+        }
         return r;
     }
     // elements of vector v as fp32, -inf outside the row
@@ -265,26 +326,168 @@ __device__ __forceinline__ float teacher_value(const void* p, int type, int64_t 
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
 }
 
-// One CTA computes one row: a pass over the row for the statistics, then
-// (GRAD) a second one that writes the gradient.
+// What a CTA of a row tells the others: its statistics, and its part of a
+// distillation loss, sum P_k (log P_k - (z_k - m) / temperature) and sum P_k
+// over the tokens in its segment.
+struct Exchange {
+    Stats s;
+    float A, P;
+};
+
+// The keys of a segment's largest logits, in descending order.
+struct TopState {
+    uint64_t list[LOGITS_MAX_TOP];
+    uint64_t cand[kCandidates];
+    int bucket[kThreads];
+    int buckets, found;
+    int count;
+};
+
+// `count` = the number of keys in list[0..n-1], the rest 0.
+//
+// Each thread's logits are a bucket, of which `key` is the largest one's
+// ordered value and `batch` the index of its first batch of vectors with it.
+// The n-th largest of the bucket maxima is no larger than the n-th largest
+// logit (n buckets hold one each that reaches it), so what reaches it is all
+// that can be among the n: only the n buckets whose maximum does have to be
+// read again, and of 512 buckets of random order few hold two.  It is found
+// bit by bit, each a count over the block.  Equal maxima (a mask of the type's
+// lowest value) are told apart by their tokens in the same way, or there would
+// be as many buckets as there are ties.
+template <typename E>
+__device__ void select_top(TopState& t, const Row<E>& row, int v0, int v1, uint32_t key, int batch, int n) {
+    constexpr int kPer = Ele<E>::kPer;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) t.buckets = t.found = 0;
+    for (int i = tid; i < n; i += kThreads) t.list[i] = 0;
+    uint32_t thr = 0;
+    int reach = kThreads;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = thr | (1u << bit);
+        const int cnt = __syncthreads_count(key >= c);
+        if (cnt >= n) {
+            thr = c;
+            reach = cnt;
+            if (cnt == n) break;
+        }
+    }
+    int limit = INT_MAX, mine = 0;     // tokens with the threshold's value count up to `limit`
+    if (thr == 0) {
+        thr = 1;                       // fewer than n buckets hold anything
+    } else if (reach > n + kSlack) {
+        mine = INT_MAX;
+        if (key == thr) {
+            for (int k = kUnroll - 1; k >= 0; --k) {
+                const int v = v0 + (batch * kUnroll + k) * kThreads + tid;
+                if (v >= v1) continue;
+                float x[kPer];
+                row.load(v, x);
+#pragma unroll
+                for (int e = kPer - 1; e >= 0; --e)
+                    if (ordered(x[e]) == thr) mine = row.first(v) + e;
+            }
+        }
+        const int need = n - __syncthreads_count(key > thr);
+        limit = 0;
+        for (int bit = 30; bit >= 0; --bit) {
+            const int c = limit | (1 << bit);
+            if (__syncthreads_count(mine < c) < need) limit = c;
+        }
+    }
+    if (key > thr || (key == thr && mine <= limit)) t.bucket[atomicAdd(&t.buckets, 1)] = tid;
+    __syncthreads();
+    for (int b = warp; b < t.buckets; b += kWarps) {
+        for (int v = v0 + t.bucket[b] + lane * kThreads; v < v1; v += 32 * kThreads) {
+            float x[kPer];
+            row.load(v, x);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const uint32_t o = ordered(x[e]);
+                const int j = row.first(v) + e;
+                if (o > thr || (o == thr && j <= limit)) {
+                    const int at = atomicAdd(&t.found, 1);
+                    if (at < kCandidates) t.cand[at] = (static_cast<uint64_t>(o) << 32) | static_cast<uint32_t>(~j);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int found = t.found;
+    if (found <= kCandidates) {
+        // a key's place is the number of larger ones
+        for (int i = tid; i < found; i += kThreads) {
+            const uint64_t k = t.cand[i];
+            int place = 0;
+            for (int o = 0; o < found; ++o) place += t.cand[o] > k;
+            if (place < n) t.list[place] = k;
+        }
+        if (tid == 0) t.count = found < n ? found : n;
+        __syncthreads();
+        return;
+    }
+    // Large logits crowded into few buckets: the largest key below the last
+    // one found, n times over the segment.
+    uint64_t last = ~0ull;
+    int count = 0;
+    for (; count < n; ++count) {
+        uint64_t best = 0;
+        for (int v = v0 + tid; v < v1; v += kThreads) {
+            float x[kPer];
+            row.load(v, x);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const uint64_t k = make_key(x[e], row.first(v) + e);
+                if (k < last && k > best) best = k;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const uint64_t k = __shfl_xor_sync(~0u, best, o);
+            if (k > best) best = k;
+        }
+        if (lane == 0) t.cand[warp] = best;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w)
+            if (t.cand[w] > best) best = t.cand[w];
+        __syncthreads();
+        if (!best) break;
+        if (tid == 0) t.list[count] = best;
+        last = best;
+    }
+    if (tid == 0) t.count = count;
+    __syncthreads();
+}
+
+// A row is computed by a cluster of a.cluster CTAs, each of which takes a
+// segment of its 16-byte vectors: one pass for the statistics, exchanged
+// through distributed shared memory, and (GRAD) a second one that writes the
+// gradient from the copy of the segment kept in shared memory (each thread
+// reads back its own vectors; what exceeds the copy is read again).
 template <typename E, int OP, bool GRAD, bool TOP>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, GRAD ? 3 : 2) rows_kernel(const Args a) {
     constexpr int kPer = Ele<E>::kPer;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
-    __shared__ uint64_t warp_key[kWarps];
-    __shared__ float shared_f[4];
+    __shared__ Exchange own, all;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t row_index = blockIdx.x;
+    const int64_t row_index = blockIdx.x / a.cluster;
+    const int rank = static_cast<int>(blockIdx.x % a.cluster);
     const Row<E> row(a.z, row_index * a.ld, a.V);
+    const int per = (row.nv + a.cluster - 1) / a.cluster;
+    const int v0 = rank * per, v1 = min(row.nv, v0 + per);
+    auto in_segment = [&](int j) {
+        const int v = static_cast<int>((static_cast<int64_t>(j) + row.head) / kPer);
+        return v >= v0 && v < v1;
+    };
 
     // the given token, or the teacher's: P_k, its log, and the student's logits there
     int token = -1;
     float z_token = 0.f;
-    float* P = reinterpret_cast<float*>(dyn);
+    uint4* stash = reinterpret_cast<uint4*>(dyn);
+    float* P = reinterpret_cast<float*>(stash + a.stash * kThreads);
     float* logP = P + a.K;
     float* zt = logP + a.K;
-    int* tok = reinterpret_cast<int*>(zt + a.K);
+    int* tok = reinterpret_cast<int*>(zt + a.K);    // -1: padding, or (for the loss) another CTA's
     if constexpr (OP == kLogprobs) {
         if (a.tokens) {
             const int64_t y = a.tokens[row_index];
@@ -312,7 +515,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
         const float log2_total = lg2(total);
         for (int k = tid; k < a.K; k += kThreads) {
             const int64_t y = a.tokens[at + k];
-            const bool real = y >= 0 && y < a.V;
+            const bool real = y >= 0 && y < a.V && in_segment(static_cast<int>(y));
             tok[k] = real ? static_cast<int>(y) : -1;
             const float l = real ? (teacher_value(a.teacher, a.teacher_type, at + k) - m) * a.c - log2_total : -INFINITY;
             P[k] = real && total != 0.f ? ex2(l) : 0.f;
@@ -324,76 +527,137 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
     // statistics
     constexpr bool kEntropy = OP == kLogprobs;
     Stats s = empty_stats();
-    for (int v = tid; v < row.nv; v += kThreads) {
-        float x[kPer];
-        row.load(v, x);
-        float m = x[0];
+    float bucket_max = -INFINITY;
+    int bucket_batch = 0;
+    const int whole_end = min(row.hi, v1);
+    for (int b = 0, v = v0 + tid; v < v1; ++b, v += kUnroll * kThreads) {
+        uint4 q[kUnroll];
+        if (v >= row.lo && v + (kUnroll - 1) * kThreads < whole_end) {
 #pragma unroll
-        for (int e = 1; e < kPer; ++e) m = fmaxf(m, x[e]);
+            for (int k = 0; k < kUnroll; ++k) q[k] = row.load_whole(v + k * kThreads);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) q[k] = row.load_any(v + k * kThreads, v1);
+        }
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (b * kUnroll + k < a.stash) stash[(b * kUnroll + k) * kThreads + tid] = q[k];
+        }
+        const float m = Ele<E>::template max_of<kUnroll>(q);
+        if constexpr (TOP) {
+            if (m > bucket_max) bucket_max = m, bucket_batch = b;
+        }
         if (m > s.m) raise_max(s, m, a.c);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) add<kEntropy>(s, x[e], a.c);
+        for (int k = 0; k < kUnroll; ++k) {
+            float x[kPer];
+            Ele<E>::unpack(q[k], x);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) add<kEntropy>(s, x[e], a.c);
+        }
     }
     s = warp_join(s, a.c);
     if (lane == 0) warp_stats[warp] = s;
     __syncthreads();
-    s = warp_stats[0];
+    if (warp == 0) {
+        s = warp_stats[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) s = join(s, warp_stats[w], a.c);
-    const bool nothing = s.S == 0.f;
-    const float log2_S = lg2(s.S);
-    const float lse = nothing ? -INFINITY : fmaf(s.m, a.inv_t, kLn2 * log2_S);
-    const float entropy = nothing ? 0.f : kLn2 * (log2_S - s.U / s.S);
-    if (tid == 0 && a.lse) a.lse[row_index] = lse;
-
-    // gradient: p_j (ga + gb log2 p_j), and the given tokens' terms added at the end
-    float ga = 0.f, gb = 0.f, g_token = 0.f;
-    if constexpr (OP == kLogprobs) {
-        if (tid == 0) {
-            if (a.logprob)
-                a.logprob[row_index] =
-                    token < 0 ? 0.f : nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
-            if (a.entropy) a.entropy[row_index] = entropy;
-        }
-        if constexpr (GRAD) {
-            const float g = token >= 0 && a.g ? a.g[row_index] : 0.f, h = a.h ? a.h[row_index] : 0.f;
-            ga = -a.inv_t * fmaf(h, entropy, g);
-            gb = -a.inv_t * h * kLn2;
-            g_token = a.inv_t * g;
-        }
-    } else {
-        // loss and the sum of P (1, or 0 without a teacher)
-        if (warp == 0) {
-            float l = 0.f, p = 0.f;
+        for (int w = 1; w < kWarps; ++w) s = join(s, warp_stats[w], a.c);
+        float A = 0.f, p = 0.f;
+        if constexpr (OP == kDistill) {
             for (int k = lane; k < a.K; k += 32)
-                if (P[k] > 0.f || P[k] != P[k]) {
-                    const float log_q = nothing ? -INFINITY : log_p(zt[k], s.m, log2_S, a.inv_t);
-                    l = fmaf(P[k], logP[k] - log_q, l);
+                if (!(P[k] <= 0.f)) {
+                    A = fmaf(P[k], logP[k] - (zt[k] - s.m) * a.inv_t, A);
                     p += P[k];
                 }
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
-                l += __shfl_xor_sync(~0u, l, o);
+                A += __shfl_xor_sync(~0u, A, o);
                 p += __shfl_xor_sync(~0u, p, o);
             }
-            if (lane == 0) {
-                shared_f[0] = p;
-                if (a.loss) a.loss[row_index] = a.t * a.t * l;
+        }
+        if (lane == 0) own = {s, A, p};
+    }
+    TopState* top = reinterpret_cast<TopState*>(dyn);
+    if constexpr (TOP) select_top(*top, row, v0, v1, ordered(bucket_max), bucket_batch, a.top);
+    float log2_S = 0.f;
+    bool nothing = false;
+    __syncwarp();
+    if (a.cluster > 1) tcdt::cluster_sync_all();
+    // the row's statistics, joined in the order of its segments by every CTA's first warp
+    if (warp == 0) {
+        Exchange x{empty_stats(), 0.f, 0.f};
+        if (a.cluster == 1) {
+            __syncwarp();
+            x = own;
+        } else if (lane < a.cluster) {
+            const uint32_t at = tcdt::map_to_cta(tcdt::smem_addr(&own), lane);
+            x.s.m = ld_cluster_f32(at), x.s.S = ld_cluster_f32(at + 4), x.s.U = ld_cluster_f32(at + 8);
+            x.A = ld_cluster_f32(at + 12), x.P = ld_cluster_f32(at + 16);
+        }
+        if (a.cluster == 1) {
+            s = x.s;
+        } else {
+            s = empty_stats();
+            for (int r = 0; r < a.cluster; ++r) {
+                Stats o;
+                o.m = __shfl_sync(~0u, x.s.m, r);
+                o.S = __shfl_sync(~0u, x.s.S, r);
+                o.U = __shfl_sync(~0u, x.s.U, r);
+                s = join(s, o, a.c);
             }
         }
-        if constexpr (GRAD) {
-            __syncthreads();
-            g_token = a.w[row_index] * a.t;
-            ga = g_token * shared_f[0];
+        nothing = s.S == 0.f;
+        log2_S = lg2(s.S);
+        float l = 0.f, p = 0.f;
+        if constexpr (OP == kDistill) {
+            for (int r = 0; r < a.cluster; ++r) {
+                const float A = a.cluster == 1 ? x.A : __shfl_sync(~0u, x.A, r);
+                const float Pr = a.cluster == 1 ? x.P : __shfl_sync(~0u, x.P, r);
+                const float mr = a.cluster == 1 ? x.s.m : __shfl_sync(~0u, x.s.m, r);
+                // a part without teacher tokens has no maximum to shift by
+                if (!(Pr <= 0.f)) l += nothing ? A : fmaf(Pr, fmaf(s.m - mr, a.inv_t, kLn2 * log2_S), A);
+                p += Pr;
+            }
+        }
+        if (lane == 0) all = {s, l, p};
+    }
+    __syncthreads();
+    s = all.s;
+    nothing = s.S == 0.f;
+    log2_S = lg2(s.S);
+    const float entropy = nothing ? 0.f : kLn2 * (log2_S - s.U / s.S);
+    if (rank == 0 && tid == 0) {
+        if (a.lse) a.lse[row_index] = nothing ? -INFINITY : fmaf(s.m, a.inv_t, kLn2 * log2_S);
+        if constexpr (OP == kLogprobs) {
+            if (a.logprob)
+                a.logprob[row_index] =
+                    token < 0 ? 0.f : nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
+            if (a.entropy) a.entropy[row_index] = entropy;
+        } else {
+            a.loss[row_index] = a.t * a.t * all.A;
         }
     }
 
     if constexpr (GRAD) {
+        // p_j (ga + gb log2 p_j), and the given tokens' terms put in at the end
+        float ga, gb = 0.f, g_token;
+        if constexpr (OP == kLogprobs) {
+            const float g = token >= 0 && a.g ? a.g[row_index] : 0.f, h = a.h ? a.h[row_index] : 0.f;
+            ga = -a.inv_t * fmaf(h, entropy, g);
+            gb = -a.inv_t * h * kLn2;
+            g_token = a.inv_t * g;
+        } else {
+            g_token = a.w[row_index] * a.t;
+            ga = g_token * all.P;
+        }
         E* out = static_cast<E*>(a.dz) + row_index * a.ldd;
         const bool whole = (reinterpret_cast<uintptr_t>(out) & 15) == static_cast<uintptr_t>(row.head) * sizeof(E);
-        for (int v = tid; v < row.nv; v += kThreads) {
+        for (int i = 0, v = v0 + tid; v < v1; ++i, v += kThreads) {
             float x[kPer];
-            row.load(v, x);
+            if (i < a.stash) Ele<E>::unpack(stash[i * kThreads + tid], x);
+            else row.load(v, x);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 const float l = max_nan((x[e] - s.m) * a.c - log2_S, -200.f);
@@ -411,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
         }
         __syncthreads();
         if constexpr (OP == kLogprobs) {
-            if (tid == 0 && token >= 0 && !nothing) {
+            if (tid == 0 && token >= 0 && !nothing && in_segment(token)) {
                 const float l = max_nan((z_token - s.m) * a.c - log2_S, -200.f);
                 out[token] = Ele<E>::round(fmaf(ex2(l), fmaf(gb, l, ga), g_token));
             }
@@ -428,38 +692,54 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
     }
 
     if constexpr (TOP) {
-        // the largest key below the last one found, `top` times over the row
-        uint64_t last = ~0ull;
-        for (int r = 0; r < a.top; ++r) {
-            uint64_t best = 0;
-            if (last)
-                for (int v = tid; v < row.nv; v += kThreads) {
-                    float x[kPer];
-                    row.load(v, x);
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) {
-                        const uint64_t key = make_key(x[e], row.first(v) + e);
-                        if (key < last && key > best) best = key;
-                    }
+        if (rank == 0) {
+            // the segments' lists side by side; a key's place is its place in its own list and the
+            // number of larger keys in each of the others
+            const int n = a.top, lists = a.cluster;
+            int total = 0;
+            for (int r = 0; r < lists; ++r)
+                total += lists == 1 ? top->count
+                                    : static_cast<int>(ld_cluster_u32(
+                                          tcdt::map_to_cta(tcdt::smem_addr(&top->count), static_cast<uint32_t>(r))));
+            const uint64_t* keys = top->list;
+            if (lists > 1) {
+                for (int i = tid; i < lists * n; i += kThreads) {
+                    const uint32_t at =
+                        tcdt::map_to_cta(tcdt::smem_addr(&top->list[i % n]), static_cast<uint32_t>(i / n));
+                    top->cand[i] = static_cast<uint64_t>(ld_cluster_u32(at + 4)) << 32 | ld_cluster_u32(at);
                 }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const uint64_t k = __shfl_xor_sync(~0u, best, o);
-                if (k > best) best = k;
+                __syncthreads();
+                keys = top->cand;
             }
-            if (lane == 0) warp_key[warp] = best;
-            __syncthreads();
-            for (int w = 0; w < kWarps; ++w)
-                if (warp_key[w] > best) best = warp_key[w];
-            __syncthreads();
-            if (tid == 0) {
-                const float z = from_ordered(static_cast<uint32_t>(best >> 32));
-                a.top_logprob[row_index * a.top + r] = best ? log_p(z, s.m, log2_S, a.inv_t) : -INFINITY;
-                a.top_token[row_index * a.top + r] = best ? static_cast<int64_t>(~static_cast<uint32_t>(best)) : -1;
+            for (int i = tid; i < lists * n; i += kThreads) {
+                const uint64_t k = keys[i];
+                if (!k) continue;
+                int place = i % n;
+                for (int r = 0; r < lists; ++r) {
+                    if (r == i / n) continue;
+                    int lo = 0, hi = n;    // keys[r * n + 0 .. lo - 1] are larger, from hi on none is
+                    while (lo < hi) {
+                        const int mid = (lo + hi) / 2;
+                        if (keys[r * n + mid] > k) lo = mid + 1;
+                        else hi = mid;
+                    }
+                    place += lo;
+                }
+                if (place < n) {
+                    const float z = from_ordered(static_cast<uint32_t>(k >> 32));
+                    a.top_logprob[row_index * n + place] = log_p(z, s.m, log2_S, a.inv_t);
+                    a.top_token[row_index * n + place] = static_cast<int64_t>(~static_cast<uint32_t>(k));
+                }
             }
-            last = best;
+            for (int i = total + tid; i < n; i += kThreads) {
+                a.top_logprob[row_index * n + i] = -INFINITY;
+                a.top_token[row_index * n + i] = -1;
+            }
         }
     }
+    // nobody leaves while its shared memory may still be read
+    __syncwarp();
+    if (a.cluster > 1) tcdt::cluster_sync_all();
 }
 
 bool float_type(gemm_dtype_t d) { return d == GEMM_F32 || d == GEMM_F16 || d == GEMM_BF16; }
@@ -513,11 +793,51 @@ struct OnDevice {
     }
 };
 
+// CTAs of a row.  A gradient keeps the row on chip: as many CTAs as it takes
+// for kStashVectors vectors a thread.  Beyond that rows are split only while
+// there are fewer CTAs than two an SM and every thread of a CTA still has
+// loads for a batch.
+int cluster_of(int64_t T, int64_t vectors, bool grad, int sms) {
+    int c = 1;
+    if (grad)
+        while (c < kMaxCluster && (vectors + c - 1) / c > static_cast<int64_t>(kStashVectors) * kThreads) c *= 2;
+    while (c < kMaxCluster && T * c * 2 <= 2 * sms && vectors / (2 * c) >= kThreads) c *= 2;
+    return c;
+}
+
 template <typename E, int OP, bool GRAD, bool TOP>
-gemm_status_t launch(const Args& a, int64_t T, cudaStream_t stream) {
-    const size_t dyn = OP == kDistill ? static_cast<size_t>(a.K) * 16 : 0;
-    rows_kernel<E, OP, GRAD, TOP><<<static_cast<unsigned>(T), kThreads, dyn, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_CUDA;
+gemm_status_t launch(Args a, int64_t T, int device, cudaStream_t stream) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return GEMM_ERR_CUDA;
+    const int64_t vectors = a.V / Ele<E>::kPer + 2;
+    a.cluster = cluster_of(T, vectors, GRAD, sms);
+    const int64_t each = ((vectors + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads;
+    a.stash = GRAD ? static_cast<int>(each < kStashMost ? each : kStashMost) : 0;
+    const size_t dyn = TOP ? sizeof(TopState)
+                           : static_cast<size_t>(a.stash) * kThreads * 16 +
+                                 (OP == kDistill ? static_cast<size_t>(a.K) * 16 : 0);
+    auto kernel = rows_kernel<E, OP, GRAD, TOP>;
+    if (T * a.cluster > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;
+    if (dyn > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dyn)) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(T * a.cluster), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
     return GEMM_OK;
 }
 
@@ -527,9 +847,9 @@ gemm_status_t launch_type(int device, gemm_dtype_t dtype, const Args& a, int64_t
     const OnDevice on(device);
     if (on.status != GEMM_OK) return on.status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == GEMM_F32) return launch<float, OP, GRAD, TOP>(a, T, s);
-    if (dtype == GEMM_F16) return launch<__half, OP, GRAD, TOP>(a, T, s);
-    return launch<__nv_bfloat16, OP, GRAD, TOP>(a, T, s);
+    if (dtype == GEMM_F32) return launch<float, OP, GRAD, TOP>(a, T, device, s);
+    if (dtype == GEMM_F16) return launch<__half, OP, GRAD, TOP>(a, T, device, s);
+    return launch<__nv_bfloat16, OP, GRAD, TOP>(a, T, device, s);
 }
 
 void fill_rows(Args& a, const void* logits, int64_t V, int64_t ld, float temperature) {
