@@ -515,7 +515,7 @@ def quantize_rows_i8(X, Q=None, scale=None, *, stream=None):
         raise ValueError("scale must be a contiguous fp32 vector with one entry per row on X's device")
     ldq = _row_stride(Q, "Q")
     if stream is None:
-        stream = torch.cuda.current_stream(X.device).cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(X.device.index)
     st = gemm_quantize_rows_i8(X.device.index, X.data_ptr(), dt, R, K, ldx, Q.data_ptr(), ldq, scale.data_ptr(),
                                stream)
     if st != 0:
@@ -661,7 +661,7 @@ class Plan:
         M, N, K, lda, ldb, ldd, out_dtype, D = self._resolve_i8(A, B, D, out_dtype)
         ep = _make_epilogue(M, N, bias, row_scale, col_scale, act)
         if stream is None:
-            stream = torch.cuda.current_stream(A.device).cuda_stream
+            stream = torch._C._cuda_getCurrentRawStream(A.device.index)
         st = gemm_run_i8(self.handle, A.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, lda, ldb, ldd, out_dtype, ep,
                          stream)
         if st != 0:
@@ -678,7 +678,7 @@ class Plan:
         M, N, K, ldx, ldb, ldd, out_dtype, D = self._resolve_i8(X, B, D, out_dtype or (xt if D is None else None))
         ep = _make_epilogue(M, N, bias, None, col_scale, act)
         if stream is None:
-            stream = torch.cuda.current_stream(X.device).cuda_stream
+            stream = torch._C._cuda_getCurrentRawStream(X.device.index)
         st = gemm_run_i8_dynamic(self.handle, X.data_ptr(), xt, B.data_ptr(), D.data_ptr(), M, N, K, ldx, ldb, ldd,
                                  out_dtype, ep, stream)
         if st != 0:

@@ -9,15 +9,19 @@
 // d = (m - m') c.  Then log2 S and m give everything else:
 //     lse = m / temperature + ln 2 log2 S,   entropy = ln 2 (log2 S - U / S),
 //     log2 p_j = (z_j - m) c - log2 S.
-// z - m is formed before the scaling, so rows of the type's lowest value
-// cancel exactly instead of overflowing.  m starts at the lowest finite
-// number, not at -inf, and u is cut off at -200 (2^-200 is 0 in fp32): a
-// masked logit of -inf then adds 0 to both sums without a test, and a NaN
-// still reaches them (max.NaN).
+// z - m is formed before the scaling: it is exact near the maximum, where p
+// is large, and rows of the type's lowest value cancel instead of overflowing
+// (z c - m c in one multiply-add saved nothing that showed).  m starts at the
+// lowest finite number, not at -inf: a masked logit of -inf then adds
+// 2^-inf = 0 without a test.  Where u or log2 p is also a factor it is cut off
+// at -200 (2^-200 is 0 in fp32, and 0 times -200 is 0, where 0 times -inf is
+// not); a NaN still reaches the sums (max.NaN).  S = 0 means that every logit
+// is -inf.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -28,14 +32,23 @@
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;            // that compute; one more warp starts the copies
+// CTAs an SM: a gradient's ring holds a whole segment, and fewer CTAs a row
+// wait for one another less (4096 x 131072 bf16 with gradient: 3 CTAs 456 us,
+// 2 CTAs 509, 4 CTAs 541; alternatives without gradient: 4 CTAs 287 us, 3 334, 5 353).
+constexpr int ctas_of(bool grad) { return grad ? 3 : 4; }
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;               // 16-byte loads in flight per thread
+constexpr int kUnroll = 1024 / kThreads; // 16-byte vectors of a thread in a chunk
+constexpr int kChunk = kUnroll * kThreads;   // vectors of an asynchronous copy: 16 KB
+constexpr int kSlotsMost = 12;           // of the ring
+constexpr int kRowsMost = 8;              // rows a cluster takes one after another
+constexpr int kBlock = kThreads + 32;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxCluster = 8;
-constexpr int kCandidates = 2048;        // kMaxCluster lists of LOGITS_MAX_TOP fit too
+constexpr int kCandidates = 1024;        // kMaxCluster lists of LOGITS_MAX_TOP fit too
 constexpr int kSlack = 64;               // buckets more than wanted that are not worth telling ties apart
-constexpr int kStashVectors = 9;         // 16-byte vectors of a thread kept on chip with three CTAs an SM
-constexpr int kStashMost = 26;           // and with one
+constexpr int64_t kSharedOfSm = 228 * 1024;
+constexpr int kDynamicMost = 225 * 1024;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kMaxExtent = 0x7FFFFFFF - 4096;
@@ -47,7 +60,10 @@ struct Args {
     const void* z;
     int64_t ld;
     int32_t V;
-    int cluster, stash;           // CTAs of a row; vectors of a thread kept in shared memory
+    int64_t T;
+    int cluster, rows, slots;     // CTAs of a row, rows of a cluster, chunks of the ring
+    int per;                      // vectors of a segment
+    int passes;                   // 2: a segment exceeds the ring, the gradient reads it again
     float c, inv_t, t;            // log2(e) / temperature, 1 / temperature, temperature
     const int64_t* tokens;        // [T], or teacher tokens [T][ldt]
     // log-probabilities
@@ -96,7 +112,52 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t at) {
     return v;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t at) { return __uint_as_float(ld_cluster_u32(at)); }
+// Asynchronous copy of whole 16-byte units into shared memory, counted on an mbarrier.
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Waits for a phase of a barrier; false once kWaitLimitNs have passed.
+__device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity) {
+    if (tcdt::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tcdt::globaltimer_ns();
+    while (!tcdt::mbar_try_wait(bar, parity))
+        if (tcdt::globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
+
+// Two 32-bit values as a register pair.
+__device__ __forceinline__ uint64_t bit_pair(uint32_t x, uint32_t y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x), "r"(y));
+    return v;
+}
+
+// Barriers of the computing threads.
+__device__ __forceinline__ void sync_threads() { tcdt::named_bar_sync(1, kThreads); }
+__device__ __forceinline__ int sync_count(bool p) {
+    int n;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, 1, %2, q;\n\t}"
+                 : "=r"(n)
+                 : "r"(p ? 1u : 0u), "n"(kThreads)
+                 : "memory");
+    return n;
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t at, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+// wait_copy for arrivals from other CTAs of the cluster.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+    if (tcdt::mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = tcdt::globaltimer_ns();
+    while (!tcdt::mbar_try_wait_cluster(bar, parity))
+        if (tcdt::globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
 
 // Element types: kPer elements in a 16-byte vector.
 template <typename E>
@@ -120,8 +181,14 @@ struct Ele<float> {
         x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
         x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     }
-    __device__ static uint4 pack(const float (&x)[4]) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    __device__ static void pairs(const uint4& v, uint64_t (&x)[2]) {
+        x[0] = bit_pair(v.x, v.y), x[1] = bit_pair(v.z, v.w);
+    }
+    __device__ static uint4 pack_pairs(const uint64_t (&x)[2]) {
+        uint4 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(x[0]));
+        asm("mov.b64 {%0, %1}, %2;" : "=r"(r.z), "=r"(r.w) : "l"(x[1]));
+        return r;
     }
     __device__ static float round(float x) { return x; }
 };
@@ -150,13 +217,20 @@ struct Ele<__half> {
             x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     }
-    __device__ static uint4 pack(const float (&x)[8]) {
+    __device__ static void pairs(const uint4& v, uint64_t (&x)[4]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("{\n\t.reg .b16 a, b;\n\t.reg .f32 l, h;\n\tmov.b32 {a, b}, %1;\n\t"
+                "cvt.f32.f16 l, a;\n\tcvt.f32.f16 h, b;\n\tmov.b64 %0, {l, h};\n\t}"
+                : "=l"(x[i])
+                : "r"(w[i]));
+    }
+    __device__ static uint4 pack_pairs(const uint64_t (&x)[4]) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        for (int i = 0; i < 4; ++i)
+            asm("{\n\t.reg .f32 l, h;\n\tmov.b64 {l, h}, %1;\n\tcvt.rn.f16x2.f32 %0, h, l;\n\t}" : "=r"(w[i]) : "l"(x[i]));
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ static __half round(float x) { return __float2half_rn(x); }
@@ -186,70 +260,59 @@ struct Ele<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
-    __device__ static uint4 pack(const float (&x)[8]) {
+    __device__ static void pairs(const uint4& v, uint64_t (&x)[4]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = bit_pair(w[i] << 16, w[i] & 0xFFFF0000u);
+    }
+    __device__ static uint4 pack_pairs(const uint64_t (&x)[4]) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        for (int i = 0; i < 4; ++i)
+            asm("{\n\t.reg .f32 l, h;\n\tmov.b64 {l, h}, %1;\n\tcvt.rn.bf16x2.f32 %0, h, l;\n\t}" : "=r"(w[i]) : "l"(x[i]));
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ static __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
 };
 
-// A row as 16-byte vectors: vector v holds the elements v * kPer - head ..
-// + kPer - 1, head the elements between the 16-byte boundary at or below the
-// row's start and the start.  Vectors lo..hi-1 lie inside the row and are
-// read whole; the (at most two) others are read element by element, so
-// nothing outside the row is touched whatever the row's alignment.
+// A CTA's part of a row: `n` of the 16-byte vectors that lie whole between
+// the 16-byte boundaries of the row, and, with the row's first and last CTA,
+// the fewer than kPer elements before the first and after the last boundary
+// (thread i has the i-th of each).  Nothing outside the row is touched,
+// whatever its alignment.
 template <typename E>
-struct Row {
+struct Segment {
     static constexpr int kPer = Ele<E>::kPer;
-    const char* base;    // 16-byte boundary at or below the row's start
-    int head, V, lo, hi, nv;
+    const E* row;
+    const uint4* vec;       // the segment's first vector
+    int head, tail;         // elements before the first and from the last boundary on, where they are this CTA's
+    int first, after;       // token of vec's first element; of the first one of the tail
+    int n;
 
-    __device__ Row(const void* z, int64_t offset, int V_) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(z) + static_cast<uintptr_t>(offset) * sizeof(E);
-        base = reinterpret_cast<const char*>(a & ~uintptr_t(15));
-        head = static_cast<int>((a & 15) / sizeof(E));
-        V = V_;
-        lo = head ? 1 : 0;
-        hi = static_cast<int>((static_cast<int64_t>(head) + V) / kPer);
-        nv = static_cast<int>((static_cast<int64_t>(head) + V + kPer - 1) / kPer);
+    __device__ __forceinline__ Segment(const void* z, int64_t offset, int V, int rank, int cluster, int per) {
+        row = static_cast<const E*>(z) + offset;
+        const int skip = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / static_cast<int>(sizeof(E));
+        const int lead = min(skip, V);
+        const int whole = static_cast<int>(static_cast<unsigned>(V - lead) / kPer);
+        const int v0 = min(rank * per, whole);
+        n = min(per, whole - v0);
+        first = lead + v0 * kPer;
+        vec = reinterpret_cast<const uint4*>(row + first);
+        after = lead + whole * kPer;
+        head = rank == 0 ? lead : 0;
+        tail = rank == cluster - 1 ? V - after : 0;
     }
-    __device__ const E* element(int j) const { return reinterpret_cast<const E*>(base) + head + j; }
-    __device__ int first(int v) const { return v * kPer - head; }    // V < 2^31 - 4096: no overflow
-    __device__ uint4 load_whole(int v) const {
+    __device__ __forceinline__ int chunks() const { return static_cast<int>(static_cast<unsigned>(n + kChunk - 1) / kChunk); }
+    __device__ __forceinline__ bool holds(int j) const {
+        return (j >= first && j < first + n * kPer) || j < head || (tail > 0 && j >= after);
+    }
+    __device__ __forceinline__ uint4 load(int v) const {
         uint4 r;
         asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                     : "l"(base + static_cast<int64_t>(v) * 16)
+                     : "l"(vec + v)
                      : "memory");
         return r;
-    }
-    // vector v's bits, -inf outside the row and from vector `end` on
-    __device__ uint4 load_any(int v, int end) const {
-        if (v >= lo && v < hi && v < end) return load_whole(v);
-        uint4 r = make_uint4(Ele<E>::kNegInf, Ele<E>::kNegInf, Ele<E>::kNegInf, Ele<E>::kNegInf);
-        if (v < end) {
-            float x[kPer];
-            load(v, x);
-            r = Ele<E>::pack(x);     // exact: the values are of type E
-        }
-        return r;
-    }
-    // elements of vector v as fp32, -inf outside the row
-    __device__ void load(int v, float (&x)[kPer]) const {
-        if (v >= lo && v < hi) {
-            Ele<E>::unpack(load_whole(v), x);
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int j = first(v) + e;
-            x[e] = (j >= 0 && j < V) ? Ele<E>::load(element(j)) : -INFINITY;
-        }
     }
 };
 
@@ -260,7 +323,7 @@ struct Stats {
 
 __device__ __forceinline__ Stats empty_stats() { return {-FLT_MAX, 0.f, 0.f}; }
 
-// d is cut off so that an empty side (m = -FLT_MAX, S = U = 0) stays 0.
+// d is cut off so that an empty side (S = U = 0) stays 0.
 __device__ __forceinline__ void raise_max(Stats& s, float m, float c) {
     const float d = max_nan((s.m - m) * c, -1e4f);
     const float f = ex2(d);
@@ -269,30 +332,66 @@ __device__ __forceinline__ void raise_max(Stats& s, float m, float c) {
     s.m = m;
 }
 
-__device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
-    const float m = fmaxf(a.m, b.m);
-    raise_max(a, m, c);
-    raise_max(b, m, c);
-    return {m, a.S + b.S, a.U + b.U};
+// Two floats in a register pair, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t ex2_2(uint64_t a) {
+    uint64_t v;
+    asm("{\n\t.reg .f32 l, h;\n\tmov.b64 {l, h}, %1;\n\tex2.approx.ftz.f32 l, l;\n\tex2.approx.ftz.f32 h, h;\n\t"
+        "mov.b64 %0, {l, h};\n\t}"
+        : "=l"(v)
+        : "l"(a));
+    return v;
+}
+// max_nan of both
+__device__ __forceinline__ uint64_t max_nan2(uint64_t a, float lo) {
+    uint64_t v;
+    asm("{\n\t.reg .f32 l, h;\n\tmov.b64 {l, h}, %1;\n\tmax.NaN.f32 l, l, %2;\n\tmax.NaN.f32 h, h, %2;\n\t"
+        "mov.b64 %0, {l, h};\n\t}"
+        : "=l"(v)
+        : "l"(a), "f"(lo));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
+// Of all lanes of a warp, for all of them: the maximum first (one
+// instruction), so that each lane's sums are scaled once and then added.
+__device__ __forceinline__ float warp_max(float x) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+
+__device__ __forceinline__ float warp_sum(float x, int width) {
+    for (int o = width / 2; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
 }
 
 template <bool ENTROPY>
-__device__ __forceinline__ void add(Stats& s, float x, float c) {
-    const float u = max_nan((x - s.m) * c, -200.f);
-    const float e = ex2(u);
-    s.S += e;
-    if constexpr (ENTROPY) s.U = fmaf(e, u, s.U);
-}
-
-__device__ __forceinline__ Stats warp_join(Stats s, float c) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        Stats r;
-        r.m = __shfl_xor_sync(~0u, s.m, o);
-        r.S = __shfl_xor_sync(~0u, s.S, o);
-        r.U = __shfl_xor_sync(~0u, s.U, o);
-        s = join(s, r, c);
-    }
+__device__ __forceinline__ Stats warp_join(Stats s, int width, float c) {
+    raise_max(s, warp_max(s.m), c);
+    s.S = warp_sum(s.S, width);
+    if constexpr (ENTROPY) s.U = warp_sum(s.U, width);
     return s;
 }
 
@@ -336,82 +435,126 @@ struct Exchange {
 
 // The keys of a segment's largest logits, in descending order.
 struct TopState {
-    uint64_t list[LOGITS_MAX_TOP];
+    uint64_t list[2][LOGITS_MAX_TOP];    // by the row's parity: the other CTAs may still read the last row's
     uint64_t cand[kCandidates];
-    int bucket[kThreads];
-    int buckets, found;
-    int count;
+    uint32_t key[kThreads];
+    int narrow[kThreads], wide[kThreads], batch[kThreads];
+    int narrows, wides, found;
+    int count[2];
+    uint32_t thr;
+    int reach;
 };
 
 // `count` = the number of keys in list[0..n-1], the rest 0.
 //
 // Each thread's logits are a bucket, of which `key` is the largest one's
-// ordered value and `batch` the index of its first batch of vectors with it.
+// ordered value and `batch` the first chunk of vectors that has it (kInHead,
+// kInTail: the thread's element before or after the vectors).
 // The n-th largest of the bucket maxima is no larger than the n-th largest
 // logit (n buckets hold one each that reaches it), so what reaches it is all
-// that can be among the n: only the n buckets whose maximum does have to be
-// read again, and of 512 buckets of random order few hold two.  It is found
-// bit by bit, each a count over the block.  Equal maxima (a mask of the type's
-// lowest value) are told apart by their tokens in the same way, or there would
-// be as many buckets as there are ties.
+// that can be among the n: only the buckets whose maximum does have to be read
+// again, and most of them (the narrow ones, whose second best chunk does not
+// reach it) in that chunk only.  It is found bit by bit, by one warp that holds
+// all the maxima.  Equal maxima (a mask of
+// the type's lowest value) are told apart by their tokens in the same way, or
+// there would be as many buckets as there are ties.
+constexpr uint32_t kOrderedLowest = 0x00800000u;     // ordered(-FLT_MAX)
+constexpr int kInHead = -1, kInTail = INT_MAX;
+
 template <typename E>
-__device__ void select_top(TopState& t, const Row<E>& row, int v0, int v1, uint32_t key, int batch, int n) {
+__device__ __forceinline__ void select_top(TopState& t, uint64_t* list, int* count_out, const Segment<E>& seg,
+                                           uint32_t key, int batch, float second, int n) {
     constexpr int kPer = Ele<E>::kPer;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) t.buckets = t.found = 0;
-    for (int i = tid; i < n; i += kThreads) t.list[i] = 0;
-    uint32_t thr = 0;
-    int reach = kThreads;
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t c = thr | (1u << bit);
-        const int cnt = __syncthreads_count(key >= c);
-        if (cnt >= n) {
-            thr = c;
-            reach = cnt;
-            if (cnt == n) break;
+    if (tid == 0) t.narrows = t.wides = t.found = 0;
+    for (int i = tid; i < n; i += kThreads) list[i] = 0;
+    t.key[tid] = key;
+    sync_threads();
+    if (warp == 0) {
+        uint32_t k[kThreads / 32];
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) k[i] = t.key[i * 32 + lane];
+        uint32_t thr = 0;
+        int reach = kThreads;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t c = thr | (1u << bit);
+            int cnt = 0;
+#pragma unroll
+            for (int i = 0; i < kThreads / 32; ++i) cnt += k[i] >= c;
+            cnt = __reduce_add_sync(~0u, cnt);
+            if (cnt >= n) {
+                thr = c;
+                reach = cnt;
+                if (cnt == n) break;
+            }
         }
+        if (lane == 0) t.thr = thr, t.reach = reach;
     }
+    sync_threads();
+    uint32_t thr = t.thr;
+    const int reach = t.reach;
     int limit = INT_MAX, mine = 0;     // tokens with the threshold's value count up to `limit`
     if (thr == 0) {
         thr = 1;                       // fewer than n buckets hold anything
     } else if (reach > n + kSlack) {
         mine = INT_MAX;
         if (key == thr) {
-            for (int k = kUnroll - 1; k >= 0; --k) {
-                const int v = v0 + (batch * kUnroll + k) * kThreads + tid;
-                if (v >= v1) continue;
-                float x[kPer];
-                row.load(v, x);
+            if (batch == kInHead) mine = tid;
+            else if (batch == kInTail) mine = seg.after + tid;
+            else
+                for (int k = kUnroll - 1; k >= 0; --k) {
+                    const int v = (batch * kUnroll + k) * kThreads + tid;
+                    if (v >= seg.n) continue;
+                    float x[kPer];
+                    Ele<E>::unpack(seg.load(v), x);
 #pragma unroll
-                for (int e = kPer - 1; e >= 0; --e)
-                    if (ordered(x[e]) == thr) mine = row.first(v) + e;
-            }
+                    for (int e = kPer - 1; e >= 0; --e)
+                        if (ordered(x[e]) == thr) mine = seg.first + v * kPer + e;
+                }
         }
-        const int need = n - __syncthreads_count(key > thr);
+        const int need = n - sync_count(key > thr);
         limit = 0;
         for (int bit = 30; bit >= 0; --bit) {
             const int c = limit | (1 << bit);
-            if (__syncthreads_count(mine < c) < need) limit = c;
+            if (sync_count(mine < c) < need) limit = c;
         }
     }
-    if (key > thr || (key == thr && mine <= limit)) t.bucket[atomicAdd(&t.buckets, 1)] = tid;
-    __syncthreads();
-    for (int b = warp; b < t.buckets; b += kWarps) {
-        for (int v = v0 + t.bucket[b] + lane * kThreads; v < v1; v += 32 * kThreads) {
-            float x[kPer];
-            row.load(v, x);
+    const float thr_value = thr < kOrderedLowest ? -INFINITY : from_ordered(thr);    // below: no number
+    if (key > thr || (key == thr && mine <= limit)) {
+        const bool beside = tid < seg.head || tid < seg.tail;
+        if (second >= thr_value || beside) t.wide[atomicAdd(&t.wides, 1)] = tid;
+        else t.narrow[atomicAdd(&t.narrows, 1)] = tid;
+        t.batch[tid] = batch;
+    }
+    sync_threads();
+    auto offer = [&](float x, int j) {
+        if (!(x >= thr_value)) return;
+        const uint32_t o = ordered(x);
+        if (o > thr || (o == thr && j <= limit)) {
+            const int at = atomicAdd(&t.found, 1);
+            if (at < kCandidates) t.cand[at] = (static_cast<uint64_t>(o) << 32) | static_cast<uint32_t>(~j);
+        }
+    };
+    auto look = [&](int v) {
+        const uint4 q[1] = {seg.load(v)};
+        if (!(Ele<E>::template max_of<1>(q) >= thr_value)) return;
+        float x[kPer];
+        Ele<E>::unpack(q[0], x);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const uint32_t o = ordered(x[e]);
-                const int j = row.first(v) + e;
-                if (o > thr || (o == thr && j <= limit)) {
-                    const int at = atomicAdd(&t.found, 1);
-                    if (at < kCandidates) t.cand[at] = (static_cast<uint64_t>(o) << 32) | static_cast<uint32_t>(~j);
-                }
-            }
-        }
+        for (int e = 0; e < kPer; ++e) offer(x[e], seg.first + v * kPer + e);
+    };
+    for (int i = tid; i < t.narrows * kUnroll; i += kThreads) {
+        const int bucket = t.narrow[i / kUnroll];
+        const int v = (t.batch[bucket] * kUnroll + i % kUnroll) * kThreads + bucket;
+        if (v < seg.n) look(v);
     }
-    __syncthreads();
+    for (int b = warp; b < t.wides; b += kWarps) {
+        const int bucket = t.wide[b];
+        for (int v = bucket + lane * kThreads; v < seg.n; v += 32 * kThreads) look(v);
+        if (lane == 0 && bucket < seg.head) offer(Ele<E>::load(seg.row + bucket), bucket);
+        if (lane == 1 && bucket < seg.tail) offer(Ele<E>::load(seg.row + seg.after + bucket), seg.after + bucket);
+    }
+    sync_threads();
     const int found = t.found;
     if (found <= kCandidates) {
         // a key's place is the number of larger ones
@@ -419,10 +562,10 @@ __device__ void select_top(TopState& t, const Row<E>& row, int v0, int v1, uint3
             const uint64_t k = t.cand[i];
             int place = 0;
             for (int o = 0; o < found; ++o) place += t.cand[o] > k;
-            if (place < n) t.list[place] = k;
+            if (place < n) list[place] = k;
         }
-        if (tid == 0) t.count = found < n ? found : n;
-        __syncthreads();
+        if (tid == 0) *count_out = found < n ? found : n;
+        sync_threads();
         return;
     }
     // Large logits crowded into few buckets: the largest key below the last
@@ -431,311 +574,469 @@ __device__ void select_top(TopState& t, const Row<E>& row, int v0, int v1, uint3
     int count = 0;
     for (; count < n; ++count) {
         uint64_t best = 0;
-        for (int v = v0 + tid; v < v1; v += kThreads) {
+        auto take = [&](float x, int j) {
+            const uint64_t k = make_key(x, j);
+            if (k < last && k > best) best = k;
+        };
+        for (int v = tid; v < seg.n; v += kThreads) {
             float x[kPer];
-            row.load(v, x);
+            Ele<E>::unpack(seg.load(v), x);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const uint64_t k = make_key(x[e], row.first(v) + e);
-                if (k < last && k > best) best = k;
-            }
+            for (int e = 0; e < kPer; ++e) take(x[e], seg.first + v * kPer + e);
         }
+        if (tid < seg.head) take(Ele<E>::load(seg.row + tid), tid);
+        if (tid < seg.tail) take(Ele<E>::load(seg.row + seg.after + tid), seg.after + tid);
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             const uint64_t k = __shfl_xor_sync(~0u, best, o);
             if (k > best) best = k;
         }
         if (lane == 0) t.cand[warp] = best;
-        __syncthreads();
+        sync_threads();
         for (int w = 0; w < kWarps; ++w)
             if (t.cand[w] > best) best = t.cand[w];
-        __syncthreads();
+        sync_threads();
         if (!best) break;
-        if (tid == 0) t.list[count] = best;
+        if (tid == 0) list[count] = best;
         last = best;
     }
-    if (tid == 0) t.count = count;
-    __syncthreads();
+    if (tid == 0) *count_out = count;
+    sync_threads();
 }
 
-// A row is computed by a cluster of a.cluster CTAs, each of which takes a
-// segment of its 16-byte vectors: one pass for the statistics, exchanged
-// through distributed shared memory, and (GRAD) a second one that writes the
-// gradient from the copy of the segment kept in shared memory (each thread
-// reads back its own vectors; what exceeds the copy is read again).
+// A cluster of a.cluster CTAs computes a row, a segment each, and a.rows rows
+// one after another.  A segment comes in chunks through a ring in shared
+// memory: one warp starts asynchronous copies, into a slot as soon as all
+// computing warps have given it back, and so runs ahead into the next row
+// while this one's sums are joined, its alternatives selected or its gradient
+// written.  The gradient reads the chunks where the statistics left them (a
+// segment fits the ring, unless the row is too long for kMaxCluster CTAs: then
+// it is copied in twice).  The segments' statistics go from each CTA into
+// every other one's shared memory, counted by an mbarrier.
+// A copy that has not arrived after kWaitLimitNs is not waited for again: its
+// vectors, and all later ones, are read from memory; statistics that have not
+// arrived make the row NaN.
 template <typename E, int OP, bool GRAD, bool TOP>
-__global__ void __launch_bounds__(kThreads, GRAD ? 3 : 2) rows_kernel(const Args a) {
+__global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args a) {
     constexpr int kPer = Ele<E>::kPer;
-    extern __shared__ __align__(16) unsigned char dyn[];
+    constexpr bool kEntropy = OP == kLogprobs;
+    extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
-    __shared__ Exchange own, all;
+    __shared__ Exchange inbox[2][kMaxCluster], all;      // by the row's parity
+    __shared__ __align__(8) uint64_t full_bar[kSlotsMost], empty_bar[kSlotsMost], inbox_bar[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t row_index = blockIdx.x / a.cluster;
     const int rank = static_cast<int>(blockIdx.x % a.cluster);
-    const Row<E> row(a.z, row_index * a.ld, a.V);
-    const int per = (row.nv + a.cluster - 1) / a.cluster;
-    const int v0 = rank * per, v1 = min(row.nv, v0 + per);
-    auto in_segment = [&](int j) {
-        const int v = static_cast<int>((static_cast<int64_t>(j) + row.head) / kPer);
-        return v >= v0 && v < v1;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / a.cluster) * a.rows;
+    const int64_t row1 = min(a.T, row0 + a.rows);
+    uint4* ring = reinterpret_cast<uint4*>(dyn);
+    const uint32_t full = tcdt::smem_addr(full_bar), empty = tcdt::smem_addr(empty_bar);
+    // the teacher's entries: tokens (-1: padding, or another CTA's; -2 up to a multiple of 4), P_k (before
+    // that its logit), log P_k, the student's logits there
+    const int K4 = (a.K + 3) & ~3;
+    int* tok = reinterpret_cast<int*>(ring + a.slots * kChunk);
+    float* P = reinterpret_cast<float*>(tok + K4);
+    float* logP = P + K4;
+    float* zt = logP + K4;
+    TopState* top = reinterpret_cast<TopState*>(ring + a.slots * kChunk);
+
+    if (tid == 0) {
+        for (int i = 0; i < a.slots; ++i) {
+            tcdt::mbar_init(full + 8 * i, 1);
+            tcdt::mbar_init(empty + 8 * i, kWarps);
+        }
+        for (int i = 0; i < 2; ++i) tcdt::mbar_init(tcdt::smem_addr(&inbox_bar[i]), static_cast<uint32_t>(a.cluster));
+        tcdt::fence_mbar_init();
+    }
+    if (OP == kDistill && tid < K4 - a.K) tok[a.K + tid] = -2;
+    __syncthreads();
+    if (a.cluster > 1) tcdt::cluster_sync_all();
+
+    if (warp == kWarps) {
+        // Chunk number q of this CTA goes to slot q % a.slots.
+        if (lane == 0) {
+            int slot = 0, started = 0;
+            uint32_t parity = 1;            // an empty ring's slots count as given back
+            bool ok = true;
+            for (int64_t r = row0; ok && r < row1; ++r) {
+                const Segment<E> seg(a.z, r * a.ld, a.V, rank, a.cluster, a.per);
+                for (int pass = 0; ok && pass < a.passes; ++pass)
+                    for (int from = 0; from < seg.n; from += kChunk) {
+                        ok = wait_copy(empty + 8 * slot, parity);
+                        if (!ok) break;
+                        const uint32_t bytes = static_cast<uint32_t>(min(kChunk, seg.n - from)) * 16u;
+                        tcdt::mbar_arrive_expect_tx(full + 8 * slot, bytes);
+                        copy_bulk(tcdt::smem_addr(ring + slot * kChunk), seg.vec + from, bytes, full + 8 * slot);
+                        ++started;
+                        if (++slot == a.slots) slot = 0, parity ^= 1u;
+                    }
+            }
+            // a copy must not land in another CTA's memory
+            for (int i = 0; i < a.slots && i < started; ++i)
+                wait_copy(full + 8 * i, static_cast<uint32_t>((started - 1 - i) / a.slots) & 1u);
+        }
+        __syncwarp();
+        if (a.cluster > 1) tcdt::cluster_sync_all();
+        return;
+    }
+
+    int slot = 0;
+    uint32_t parity = 0;
+    bool late = false;
+    // the thread's vectors of a chunk, -inf beyond the segment's end; true if all are inside
+    auto take = [&](const Segment<E>& seg, int chunk, bool give_back, uint4 (&q)[kUnroll]) {
+        if (!late && !wait_copy(full + 8 * slot, parity)) late = true;
+        const uint4* at = ring + slot * kChunk + tid;
+        const bool inside = !late && (chunk + 1) * kChunk <= seg.n;
+        if (inside) {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) q[k] = at[k * kThreads];
+        } else {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int v = chunk * kChunk + k * kThreads + tid;
+                if (v < seg.n) q[k] = late ? seg.load(v) : at[k * kThreads];
+                else q[k] = make_uint4(Ele<E>::kNegInf, Ele<E>::kNegInf, Ele<E>::kNegInf, Ele<E>::kNegInf);
+            }
+        }
+        if (give_back) {
+            __syncwarp();
+            if (lane == 0) tcdt::mbar_arrive(empty + 8 * slot);
+        }
+        if (++slot == a.slots) slot = 0, parity ^= 1u;
+        return inside;
     };
 
-    // the given token, or the teacher's: P_k, its log, and the student's logits there
-    int token = -1;
-    float z_token = 0.f;
-    uint4* stash = reinterpret_cast<uint4*>(dyn);
-    float* P = reinterpret_cast<float*>(stash + a.stash * kThreads);
-    float* logP = P + a.K;
-    float* zt = logP + a.K;
-    int* tok = reinterpret_cast<int*>(zt + a.K);    // -1: padding, or (for the loss) another CTA's
-    if constexpr (OP == kLogprobs) {
-        if (a.tokens) {
-            const int64_t y = a.tokens[row_index];
-            if (y >= 0 && y < a.V) {
-                token = static_cast<int>(y);
-                z_token = Ele<E>::load(row.element(token));
-            }
-        }
-    } else {
-        // softmax over the real entries, by every warp alike
-        const int64_t at = row_index * a.ldt;
-        float m = -FLT_MAX, total = 0.f;
-        for (int k = lane; k < a.K; k += 32) {
-            const int64_t y = a.tokens[at + k];
-            if (y >= 0 && y < a.V) m = fmaxf(m, teacher_value(a.teacher, a.teacher_type, at + k));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        for (int k = lane; k < a.K; k += 32) {
-            const int64_t y = a.tokens[at + k];
-            if (y >= 0 && y < a.V) total += ex2((teacher_value(a.teacher, a.teacher_type, at + k) - m) * a.c);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-        const float log2_total = lg2(total);
-        for (int k = tid; k < a.K; k += kThreads) {
-            const int64_t y = a.tokens[at + k];
-            const bool real = y >= 0 && y < a.V && in_segment(static_cast<int>(y));
-            tok[k] = real ? static_cast<int>(y) : -1;
-            const float l = real ? (teacher_value(a.teacher, a.teacher_type, at + k) - m) * a.c - log2_total : -INFINITY;
-            P[k] = real && total != 0.f ? ex2(l) : 0.f;
-            logP[k] = l * kLn2;
-            zt[k] = real ? Ele<E>::load(row.element(static_cast<int>(y))) : 0.f;
-        }
-    }
+    for (int64_t r = row0; r < row1; ++r) {
+        const Segment<E> seg(a.z, r * a.ld, a.V, rank, a.cluster, a.per);
+        const int chunks = seg.chunks();
+        const int turn = static_cast<int>(r - row0);
 
-    // statistics
-    constexpr bool kEntropy = OP == kLogprobs;
-    Stats s = empty_stats();
-    float bucket_max = -INFINITY;
-    int bucket_batch = 0;
-    const int whole_end = min(row.hi, v1);
-    for (int b = 0, v = v0 + tid; v < v1; ++b, v += kUnroll * kThreads) {
-        uint4 q[kUnroll];
-        if (v >= row.lo && v + (kUnroll - 1) * kThreads < whole_end) {
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) q[k] = row.load_whole(v + k * kThreads);
+        // The given token, or the teacher's entries, and the elements beside
+        // the vectors: asked for here, used once the first chunk is there.
+        constexpr int kEntries = LOGITS_MAX_TEACHER / kThreads;
+        int64_t y[kEntries] = {};
+        int token = -1;
+        float z_token = 0.f;
+        if constexpr (OP == kLogprobs) {
+            y[0] = a.tokens ? a.tokens[r] : -1;
         } else {
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k) q[k] = row.load_any(v + k * kThreads, v1);
-        }
-        if constexpr (GRAD) {
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                if (b * kUnroll + k < a.stash) stash[(b * kUnroll + k) * kThreads + tid] = q[k];
-        }
-        const float m = Ele<E>::template max_of<kUnroll>(q);
-        if constexpr (TOP) {
-            if (m > bucket_max) bucket_max = m, bucket_batch = b;
-        }
-        if (m > s.m) raise_max(s, m, a.c);
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            float x[kPer];
-            Ele<E>::unpack(q[k], x);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) add<kEntropy>(s, x[e], a.c);
-        }
-    }
-    s = warp_join(s, a.c);
-    if (lane == 0) warp_stats[warp] = s;
-    __syncthreads();
-    if (warp == 0) {
-        s = warp_stats[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) s = join(s, warp_stats[w], a.c);
-        float A = 0.f, p = 0.f;
-        if constexpr (OP == kDistill) {
-            for (int k = lane; k < a.K; k += 32)
-                if (!(P[k] <= 0.f)) {
-                    A = fmaf(P[k], logP[k] - (zt[k] - s.m) * a.inv_t, A);
-                    p += P[k];
+            for (int i = 0; i < kEntries; ++i) {
+                const int k = tid + i * kThreads;
+                if (k < a.K) {
+                    y[i] = a.tokens[r * a.ldt + k];
+                    P[k] = teacher_value(a.teacher, a.teacher_type, r * a.ldt + k);
                 }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                A += __shfl_xor_sync(~0u, A, o);
-                p += __shfl_xor_sync(~0u, p, o);
             }
         }
-        if (lane == 0) own = {s, A, p};
-    }
-    TopState* top = reinterpret_cast<TopState*>(dyn);
-    if constexpr (TOP) select_top(*top, row, v0, v1, ordered(bucket_max), bucket_batch, a.top);
-    float log2_S = 0.f;
-    bool nothing = false;
-    __syncwarp();
-    if (a.cluster > 1) tcdt::cluster_sync_all();
-    // the row's statistics, joined in the order of its segments by every CTA's first warp
-    if (warp == 0) {
-        Exchange x{empty_stats(), 0.f, 0.f};
-        if (a.cluster == 1) {
-            __syncwarp();
-            x = own;
-        } else if (lane < a.cluster) {
-            const uint32_t at = tcdt::map_to_cta(tcdt::smem_addr(&own), lane);
-            x.s.m = ld_cluster_f32(at), x.s.S = ld_cluster_f32(at + 4), x.s.U = ld_cluster_f32(at + 8);
-            x.A = ld_cluster_f32(at + 12), x.P = ld_cluster_f32(at + 16);
-        }
-        if (a.cluster == 1) {
-            s = x.s;
-        } else {
-            s = empty_stats();
-            for (int r = 0; r < a.cluster; ++r) {
-                Stats o;
-                o.m = __shfl_sync(~0u, x.s.m, r);
-                o.S = __shfl_sync(~0u, x.s.S, r);
-                o.U = __shfl_sync(~0u, x.s.U, r);
-                s = join(s, o, a.c);
-            }
-        }
-        nothing = s.S == 0.f;
-        log2_S = lg2(s.S);
-        float l = 0.f, p = 0.f;
-        if constexpr (OP == kDistill) {
-            for (int r = 0; r < a.cluster; ++r) {
-                const float A = a.cluster == 1 ? x.A : __shfl_sync(~0u, x.A, r);
-                const float Pr = a.cluster == 1 ? x.P : __shfl_sync(~0u, x.P, r);
-                const float mr = a.cluster == 1 ? x.s.m : __shfl_sync(~0u, x.s.m, r);
-                // a part without teacher tokens has no maximum to shift by
-                if (!(Pr <= 0.f)) l += nothing ? A : fmaf(Pr, fmaf(s.m - mr, a.inv_t, kLn2 * log2_S), A);
-                p += Pr;
-            }
-        }
-        if (lane == 0) all = {s, l, p};
-    }
-    __syncthreads();
-    s = all.s;
-    nothing = s.S == 0.f;
-    log2_S = lg2(s.S);
-    const float entropy = nothing ? 0.f : kLn2 * (log2_S - s.U / s.S);
-    if (rank == 0 && tid == 0) {
-        if (a.lse) a.lse[row_index] = nothing ? -INFINITY : fmaf(s.m, a.inv_t, kLn2 * log2_S);
-        if constexpr (OP == kLogprobs) {
-            if (a.logprob)
-                a.logprob[row_index] =
-                    token < 0 ? 0.f : nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
-            if (a.entropy) a.entropy[row_index] = entropy;
-        } else {
-            a.loss[row_index] = a.t * a.t * all.A;
-        }
-    }
-
-    if constexpr (GRAD) {
-        // p_j (ga + gb log2 p_j), and the given tokens' terms put in at the end
-        float ga, gb = 0.f, g_token;
-        if constexpr (OP == kLogprobs) {
-            const float g = token >= 0 && a.g ? a.g[row_index] : 0.f, h = a.h ? a.h[row_index] : 0.f;
-            ga = -a.inv_t * fmaf(h, entropy, g);
-            gb = -a.inv_t * h * kLn2;
-            g_token = a.inv_t * g;
-        } else {
-            g_token = a.w[row_index] * a.t;
-            ga = g_token * all.P;
-        }
-        E* out = static_cast<E*>(a.dz) + row_index * a.ldd;
-        const bool whole = (reinterpret_cast<uintptr_t>(out) & 15) == static_cast<uintptr_t>(row.head) * sizeof(E);
-        for (int i = 0, v = v0 + tid; v < v1; ++i, v += kThreads) {
-            float x[kPer];
-            if (i < a.stash) Ele<E>::unpack(stash[i * kThreads + tid], x);
-            else row.load(v, x);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const float l = max_nan((x[e] - s.m) * a.c - log2_S, -200.f);
-                x[e] = nothing ? 0.f : ex2(l) * fmaf(gb, l, ga);
-            }
-            if (whole && v >= row.lo && v < row.hi) {
-                *reinterpret_cast<uint4*>(out + row.first(v)) = Ele<E>::pack(x);
+        const float x_head = tid < seg.head ? Ele<E>::load(seg.row + tid) : -INFINITY;
+        const float x_tail = tid < seg.tail ? Ele<E>::load(seg.row + seg.after + tid) : -INFINITY;
+        auto given = [&] {
+            if constexpr (OP == kLogprobs) {
+                if (y[0] >= 0 && y[0] < a.V) {
+                    token = static_cast<int>(y[0]);
+                    z_token = Ele<E>::load(seg.row + token);
+                }
             } else {
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const int j = row.first(v) + e;
-                    if (j >= 0 && j < a.V) out[j] = Ele<E>::round(x[e]);
+                for (int i = 0; i < kEntries; ++i) {
+                    const int k = tid + i * kThreads;
+                    if (k >= a.K) break;
+                    const bool real = y[i] >= 0 && y[i] < a.V;
+                    const bool here = real && seg.holds(static_cast<int>(y[i]));
+                    if (!real) P[k] = -INFINITY;
+                    tok[k] = here ? static_cast<int>(y[i]) : -1;
+                    zt[k] = here ? Ele<E>::load(seg.row + y[i]) : 0.f;
                 }
             }
-        }
-        __syncthreads();
-        if constexpr (OP == kLogprobs) {
-            if (tid == 0 && token >= 0 && !nothing && in_segment(token)) {
-                const float l = max_nan((z_token - s.m) * a.c - log2_S, -200.f);
-                out[token] = Ele<E>::round(fmaf(ex2(l), fmaf(gb, l, ga), g_token));
-            }
-        } else {
-            for (int k = tid; k < a.K; k += kThreads) {
-                if (tok[k] < 0 || nothing) continue;
-                float p = 0.f;    // a token given twice: each of its entries writes the same sum
-                for (int i = 0; i < a.K; ++i)
-                    if (tok[i] == tok[k]) p += P[i];
-                const float l = max_nan((zt[k] - s.m) * a.c - log2_S, -200.f);
-                out[tok[k]] = Ele<E>::round(fmaf(ga, ex2(l), -g_token * p));
-            }
-        }
-    }
+        };
 
-    if constexpr (TOP) {
-        if (rank == 0) {
-            // the segments' lists side by side; a key's place is its place in its own list and the
-            // number of larger keys in each of the others
-            const int n = a.top, lists = a.cluster;
-            int total = 0;
-            for (int r = 0; r < lists; ++r)
-                total += lists == 1 ? top->count
-                                    : static_cast<int>(ld_cluster_u32(
-                                          tcdt::map_to_cta(tcdt::smem_addr(&top->count), static_cast<uint32_t>(r))));
-            const uint64_t* keys = top->list;
-            if (lists > 1) {
-                for (int i = tid; i < lists * n; i += kThreads) {
-                    const uint32_t at =
-                        tcdt::map_to_cta(tcdt::smem_addr(&top->list[i % n]), static_cast<uint32_t>(i / n));
-                    top->cand[i] = static_cast<uint64_t>(ld_cluster_u32(at + 4)) << 32 | ld_cluster_u32(at);
+        // statistics of the segment, and the buckets' maxima
+        float bucket_max = -INFINITY, bucket_second = -INFINITY;     // of its chunks' maxima
+        int bucket_batch = 0;
+        Stats s = empty_stats();
+        const int slot0 = slot;
+        const uint32_t parity0 = parity;
+        const uint64_t c2 = pair(a.c, a.c);
+        {
+            uint64_t m2 = pair(-s.m, -s.m), S2 = 0, U2 = 0;
+            auto raise = [&](float m) {
+                float x, y;
+                unpair(S2, x, y);
+                s.S = x + y;
+                unpair(U2, x, y);
+                s.U = x + y;
+                raise_max(s, m, a.c);
+                S2 = pair(s.S, 0.f), U2 = pair(s.U, 0.f);
+                m2 = pair(-m, -m);
+            };
+            auto add = [&](uint64_t x2) {
+                uint64_t u2 = mul2(add2(x2, m2), c2);
+                if constexpr (kEntropy) u2 = max_nan2(u2, -200.f);
+                const uint64_t e2 = ex2_2(u2);
+                S2 = add2(S2, e2);
+                if constexpr (kEntropy) U2 = fma2(e2, u2, U2);
+            };
+            if (chunks == 0) given();
+            for (int b = 0; b < chunks; ++b) {
+                uint4 q[kUnroll];
+                take(seg, b, !GRAD || a.passes == 2, q);
+                if (b == 0) given();
+                const float m = Ele<E>::template max_of<kUnroll>(q);
+                if constexpr (TOP) {
+                    bucket_second = fmaxf(bucket_second, fminf(bucket_max, m));
+                    if (m > bucket_max) bucket_max = m, bucket_batch = b;
                 }
-                __syncthreads();
-                keys = top->cand;
+                if (m > s.m) raise(m);
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) {
+                    uint64_t x[kPer / 2];
+                    Ele<E>::pairs(q[k], x);
+#pragma unroll
+                    for (int e = 0; e < kPer / 2; ++e) add(x[e]);
+                }
             }
-            for (int i = tid; i < lists * n; i += kThreads) {
-                const uint64_t k = keys[i];
-                if (!k) continue;
-                int place = i % n;
-                for (int r = 0; r < lists; ++r) {
-                    if (r == i / n) continue;
-                    int lo = 0, hi = n;    // keys[r * n + 0 .. lo - 1] are larger, from hi on none is
-                    while (lo < hi) {
-                        const int mid = (lo + hi) / 2;
-                        if (keys[r * n + mid] > k) lo = mid + 1;
-                        else hi = mid;
+            if (tid < kPer) {
+                const float m = fmaxf(x_head, x_tail);
+                if (m > s.m) raise(m);
+                add(pair(x_head, x_tail));
+                if constexpr (TOP) {
+                    if (x_head >= bucket_max) bucket_max = x_head, bucket_batch = kInHead;
+                    if (x_tail > bucket_max) bucket_max = x_tail, bucket_batch = kInTail;
+                }
+            }
+            float x, y;
+            unpair(S2, x, y);
+            s.S = x + y;
+            unpair(U2, x, y);
+            s.U = x + y;
+        }
+
+        // joined over the block by warp 0; the teacher's softmax and the
+        // segment's part of a distillation loss are warp 1's
+        s = warp_join<kEntropy>(s, 32, a.c);
+        if (lane == 0) warp_stats[warp] = s;
+        sync_threads();
+        if (warp == 0) {
+            s = lane < kWarps ? warp_stats[lane] : empty_stats();
+            s = warp_join<kEntropy>(s, kWarps, a.c);
+        }
+        float A = 0.f, p = 0.f;
+        if constexpr (OP == kDistill) {
+            if (warp == 1) {
+                const float sm = warp_max(lane < kWarps ? warp_stats[lane].m : -FLT_MAX);
+                float m = -FLT_MAX, total = 0.f;
+                for (int k = lane; k < a.K; k += 32) m = fmaxf(m, P[k]);
+                m = warp_max(m);
+                for (int k = lane; k < a.K; k += 32) total += ex2((P[k] - m) * a.c);
+                total = warp_sum(total, 32);
+                const float log2_total = lg2(total);
+                for (int k = lane; k < a.K; k += 32) {
+                    const float l = (P[k] - m) * a.c - log2_total, Pk = total != 0.f ? ex2(l) : 0.f;
+                    P[k] = Pk;
+                    logP[k] = l * kLn2;
+                    if (tok[k] >= 0 && !(Pk <= 0.f)) {
+                        A = fmaf(Pk, l * kLn2 - (zt[k] - sm) * a.inv_t, A);
+                        p += Pk;
                     }
-                    place += lo;
                 }
-                if (place < n) {
-                    const float z = from_ordered(static_cast<uint32_t>(k >> 32));
-                    a.top_logprob[row_index * n + place] = log_p(z, s.m, log2_S, a.inv_t);
-                    a.top_token[row_index * n + place] = static_cast<int64_t>(~static_cast<uint32_t>(k));
-                }
+                A = warp_sum(A, 32);
+                p = warp_sum(p, 32);
+                if (lane == 0) all.A = A, all.P = p;
             }
-            for (int i = total + tid; i < n; i += kThreads) {
-                a.top_logprob[row_index * n + i] = -INFINITY;
-                a.top_token[row_index * n + i] = -1;
+            sync_threads();
+            if (warp == 0) A = all.A, p = all.P;
+        }
+        if constexpr (TOP)
+            select_top<E>(*top, top->list[turn & 1], &top->count[turn & 1], seg, ordered(bucket_max), bucket_batch,
+                          bucket_second, a.top);
+        // The segments' statistics into every CTA's shared memory, lane i's
+        // copy to CTA i, and the row's joined from them.
+        if (warp == 0) {
+            Exchange x{s, A, p};
+            bool arrived = true;
+            if (a.cluster > 1) {
+                const uint32_t bar = tcdt::smem_addr(&inbox_bar[turn & 1]);
+                if (lane < a.cluster) {
+                    const uint32_t to = tcdt::map_to_cta(tcdt::smem_addr(&inbox[turn & 1][rank]), static_cast<uint32_t>(lane));
+                    st_cluster_f32(to, x.s.m), st_cluster_f32(to + 4, x.s.S), st_cluster_f32(to + 8, x.s.U);
+                    st_cluster_f32(to + 12, x.A), st_cluster_f32(to + 16, x.P);
+                    tcdt::mbar_arrive_cluster(tcdt::map_to_cta(bar, static_cast<uint32_t>(lane)));
+                }
+                arrived = __all_sync(~0u, wait_cluster(bar, static_cast<uint32_t>(turn >> 1) & 1u));
+                x = lane < a.cluster ? inbox[turn & 1][lane] : Exchange{empty_stats(), 0.f, 0.f};
+                s = warp_join<kEntropy>(x.s, kMaxCluster, a.c);
+            }
+            float l = 0.f, sum_P = 0.f;
+            if constexpr (OP == kDistill) {
+                // a part without teacher tokens has no maximum to shift by
+                if (!(x.P <= 0.f)) l = s.S == 0.f ? x.A : fmaf(x.P, fmaf(s.m - x.s.m, a.inv_t, kLn2 * lg2(s.S)), x.A);
+                sum_P = x.P;
+                if (a.cluster > 1) l = warp_sum(l, kMaxCluster), sum_P = warp_sum(sum_P, kMaxCluster);
+            }
+            if (!arrived) s.S = NAN, l = NAN;
+            __syncwarp();
+            if (lane == 0) all = {s, l, sum_P};
+        }
+        sync_threads();
+        s = all.s;
+        const float total_P = all.P;
+        const bool nothing = s.S == 0.f;
+        const float log2_S = lg2(s.S);
+        const float entropy = nothing ? 0.f : kLn2 * (log2_S - s.U / s.S);
+        if (rank == 0 && tid == 0) {
+            if (a.lse) a.lse[r] = nothing ? -INFINITY : fmaf(s.m, a.inv_t, kLn2 * log2_S);
+            if constexpr (OP == kLogprobs) {
+                if (a.logprob)
+                    a.logprob[r] = token < 0 ? 0.f : nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
+                if (a.entropy) a.entropy[r] = entropy;
+            } else {
+                a.loss[r] = a.t * a.t * all.A;
             }
         }
+
+        if constexpr (GRAD) {
+            // p_j (ga + gb log2 p_j), and the given tokens' terms put in at the end
+            float ga, gb = 0.f, g_token;
+            if constexpr (OP == kLogprobs) {
+                const float g = token >= 0 && a.g ? a.g[r] : 0.f, h = a.h ? a.h[r] : 0.f;
+                ga = -a.inv_t * fmaf(h, entropy, g);
+                gb = -a.inv_t * h * kLn2;
+                g_token = a.inv_t * g;
+            } else {
+                g_token = a.w[r] * a.t;
+                ga = g_token * total_P;
+            }
+            E* out = static_cast<E*>(a.dz) + r * a.ldd;
+            const bool whole = (reinterpret_cast<uintptr_t>(out + seg.first) & 15) == 0;
+            // (a row of nothing: every z - m is -inf, p and the factors are 0)
+            const float shift = nothing ? 0.f : -log2_S;
+            const uint64_t m2 = pair(-s.m, -s.m), shift2 = pair(shift, shift);
+            const uint64_t ga2 = pair(nothing ? 0.f : ga, nothing ? 0.f : ga), gb2 = pair(gb, gb);
+            auto gradient = [&](uint64_t x2) {
+                uint64_t l2 = fma2(add2(x2, m2), c2, shift2);
+                uint64_t g2 = ga2;
+                if constexpr (OP == kLogprobs) {
+                    l2 = max_nan2(l2, -200.f);
+                    g2 = fma2(gb2, l2, ga2);
+                }
+                return mul2(ex2_2(l2), g2);
+            };
+            if (a.passes == 1) slot = slot0, parity = parity0;
+            for (int b = 0; b < chunks; ++b) {
+                uint4 q[kUnroll];
+                const bool inside = take(seg, b, true, q);
+                const int v0 = b * kChunk + tid;
+                uint4* at = reinterpret_cast<uint4*>(out + seg.first) + v0;
+                if (inside && whole) {
+#pragma unroll
+                    for (int k = 0; k < kUnroll; ++k) {
+                        uint64_t x[kPer / 2];
+                        Ele<E>::pairs(q[k], x);
+#pragma unroll
+                        for (int e = 0; e < kPer / 2; ++e) x[e] = gradient(x[e]);
+                        at[k * kThreads] = Ele<E>::pack_pairs(x);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kUnroll; ++k) {
+                        const int v = v0 + k * kThreads;
+                        if (v >= seg.n) continue;
+                        uint64_t x[kPer / 2];
+                        Ele<E>::pairs(q[k], x);
+#pragma unroll
+                        for (int e = 0; e < kPer / 2; ++e) x[e] = gradient(x[e]);
+                        if (whole) {
+                            at[k * kThreads] = Ele<E>::pack_pairs(x);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < kPer / 2; ++e) {
+                                float lo, hi;
+                                unpair(x[e], lo, hi);
+                                E* to = out + seg.first + static_cast<int64_t>(v) * kPer + 2 * e;
+                                to[0] = Ele<E>::round(lo), to[1] = Ele<E>::round(hi);
+                            }
+                        }
+                    }
+                }
+            }
+            if (tid < kPer) {
+                float x0, x1;
+                unpair(gradient(pair(x_head, x_tail)), x0, x1);
+                if (tid < seg.head) out[tid] = Ele<E>::round(x0);
+                if (tid < seg.tail) out[seg.after + tid] = Ele<E>::round(x1);
+            }
+            sync_threads();
+            if constexpr (OP == kLogprobs) {
+                if (tid == 0 && token >= 0 && !nothing && seg.holds(token)) {
+                    const float l = max_nan((z_token - s.m) * a.c - log2_S, -200.f);
+                    out[token] = Ele<E>::round(fmaf(ex2(l), fmaf(gb, l, ga), g_token));
+                }
+            } else {
+                for (int k = tid; k < a.K; k += kThreads) {
+                    if (tok[k] < 0 || nothing) continue;
+                    const int t = tok[k];
+                    float p = 0.f;    // a token given twice: each of its entries writes the same sum
+                    for (int i = 0; i < a.K; i += 4) {
+                        const int4 o = *reinterpret_cast<const int4*>(tok + i);
+                        if (o.x == t) p += P[i];
+                        if (o.y == t) p += P[i + 1];
+                        if (o.z == t) p += P[i + 2];
+                        if (o.w == t) p += P[i + 3];
+                    }
+                    const float l = max_nan((zt[k] - s.m) * a.c - log2_S, -200.f);
+                    out[tok[k]] = Ele<E>::round(fmaf(ga, ex2(l), -g_token * p));
+                }
+            }
+        }
+
+        if constexpr (TOP) {
+            if (rank == 0) {
+                // the segments' lists side by side; a key's place is its place in its own list and the
+                // number of larger keys in each of the others
+                const int n = a.top, lists = a.cluster;
+                const uint64_t* keys = top->list[turn & 1];
+                const int* count = &top->count[turn & 1];
+                int total = 0;
+                for (int o = 0; o < lists; ++o)
+                    total += lists == 1 ? *count
+                                        : static_cast<int>(ld_cluster_u32(
+                                              tcdt::map_to_cta(tcdt::smem_addr(count), static_cast<uint32_t>(o))));
+                if (lists > 1) {
+                    for (int i = tid; i < lists * n; i += kThreads) {
+                        const uint32_t at = tcdt::map_to_cta(tcdt::smem_addr(keys + i % n), static_cast<uint32_t>(i / n));
+                        top->cand[i] = static_cast<uint64_t>(ld_cluster_u32(at + 4)) << 32 | ld_cluster_u32(at);
+                    }
+                    sync_threads();
+                    keys = top->cand;
+                }
+                for (int i = tid; i < lists * n; i += kThreads) {
+                    const uint64_t k = keys[i];
+                    if (!k) continue;
+                    int place = i % n;
+                    for (int o = 0; o < lists; ++o) {
+                        if (o == i / n) continue;
+                        int lo = 0, hi = n;    // keys[o * n + 0 .. lo - 1] are larger, from hi on none is
+                        while (lo < hi) {
+                            const int mid = (lo + hi) / 2;
+                            if (keys[o * n + mid] > k) lo = mid + 1;
+                            else hi = mid;
+                        }
+                        place += lo;
+                    }
+                    if (place < n) {
+                        const float z = from_ordered(static_cast<uint32_t>(k >> 32));
+                        a.top_logprob[r * n + place] = log_p(z, s.m, log2_S, a.inv_t);
+                        a.top_token[r * n + place] = static_cast<int64_t>(~static_cast<uint32_t>(k));
+                    }
+                }
+                for (int i = total + tid; i < n; i += kThreads) {
+                    a.top_logprob[r * n + i] = -INFINITY;
+                    a.top_token[r * n + i] = -1;
+                }
+            }
+        }
+        sync_threads();    // the row's entries, lists and `all` are done with
     }
     // nobody leaves while its shared memory may still be read
     __syncwarp();
@@ -763,69 +1064,94 @@ gemm_status_t check_gradient(gemm_dtype_t dtype, const void* dlogits, int64_t T,
     return aligned(dlogits, bytes_of(dtype)) ? GEMM_OK : GEMM_ERR_MISALIGNED;
 }
 
-// Makes `device` current, once checked to be the kind the kernels are built
-// for, and restores the previous one.
+// What is asked once of a device: whether it is the kind the kernels are
+// built for, and its number of SMs.
+constexpr int kDevices = 64;
+std::atomic<int> g_sms[kDevices];      // 0: not asked yet
+
+gemm_status_t sms_of(int device, int* sms) {
+    if (device < 0) return GEMM_ERR_INVALID_ARG;
+    *sms = device < kDevices ? g_sms[device].load(std::memory_order_relaxed) : 0;
+    if (*sms) return GEMM_OK;
+    int count = 0, major = 0, minor = 0;
+    gemm_status_t st = GEMM_OK;
+    if (cudaGetDeviceCount(&count) != cudaSuccess || count <= 0) st = GEMM_ERR_NO_DEVICE;
+    else if (device >= count) st = GEMM_ERR_INVALID_ARG;
+    else if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess ||
+             cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+        st = GEMM_ERR_CUDA;
+    else if (major != 10 || minor != 3) st = GEMM_ERR_NO_DEVICE;
+    if (st != GEMM_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    if (device < kDevices) g_sms[device].store(*sms, std::memory_order_relaxed);
+    return GEMM_OK;
+}
+
+// Makes `device` current and restores the previous one.
 struct OnDevice {
     int prev = -1;
-    gemm_status_t status = GEMM_OK;
+    bool ok;
     explicit OnDevice(int device) {
-        int count = 0, major = 0, minor = 0;
-        if (device < 0) {
-            status = GEMM_ERR_INVALID_ARG;
-        } else if (cudaGetDeviceCount(&count) != cudaSuccess || count <= 0) {
-            status = GEMM_ERR_NO_DEVICE;
-        } else if (device >= count) {
-            status = GEMM_ERR_INVALID_ARG;
-        } else if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
-                   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess) {
-            status = GEMM_ERR_CUDA;
-        } else if (major != 10 || minor != 3) {
-            status = GEMM_ERR_NO_DEVICE;
-        } else if (cudaGetDevice(&prev) != cudaSuccess || (prev != device && cudaSetDevice(device) != cudaSuccess)) {
-            status = GEMM_ERR_CUDA;
-        } else if (prev == device) {
-            prev = -1;
-        }
-        if (status != GEMM_OK) cudaGetLastError();
+        ok = cudaGetDevice(&prev) == cudaSuccess && (prev == device || cudaSetDevice(device) == cudaSuccess);
+        if (!ok) cudaGetLastError();
+        if (!ok || prev == device) prev = -1;
     }
     ~OnDevice() {
         if (prev >= 0) cudaSetDevice(prev);
     }
 };
 
-// CTAs of a row.  A gradient keeps the row on chip: as many CTAs as it takes
-// for kStashVectors vectors a thread.  Beyond that rows are split only while
-// there are fewer CTAs than two an SM and every thread of a CTA still has
-// loads for a batch.
-int cluster_of(int64_t T, int64_t vectors, bool grad, int sms) {
-    int c = 1;
-    if (grad)
-        while (c < kMaxCluster && (vectors + c - 1) / c > static_cast<int64_t>(kStashVectors) * kThreads) c *= 2;
-    while (c < kMaxCluster && T * c * 2 <= 2 * sms && vectors / (2 * c) >= kThreads) c *= 2;
-    return c;
-}
-
 template <typename E, int OP, bool GRAD, bool TOP>
-gemm_status_t launch(Args a, int64_t T, int device, cudaStream_t stream) {
-    int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return GEMM_ERR_CUDA;
-    const int64_t vectors = a.V / Ele<E>::kPer + 2;
-    a.cluster = cluster_of(T, vectors, GRAD, sms);
-    const int64_t each = ((vectors + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads;
-    a.stash = GRAD ? static_cast<int>(each < kStashMost ? each : kStashMost) : 0;
-    const size_t dyn = TOP ? sizeof(TopState)
-                           : static_cast<size_t>(a.stash) * kThreads * 16 +
-                                 (OP == kDistill ? static_cast<size_t>(a.K) * 16 : 0);
+gemm_status_t launch(Args a, int64_t T, int device, int sms, cudaStream_t stream) {
+    // The ring takes what shared memory is left with kCtas CTAs an SM.  A
+    // gradient wants a segment to fit it: as many CTAs as that takes, and if
+    // kMaxCluster are not enough a larger ring, with fewer CTAs an SM, and
+    // beyond that two passes.  Rows are also split while that fills idle SMs
+    // and leaves every CTA a chunk.
+    constexpr int kCtas = ctas_of(GRAD);
+    const int64_t chunks = (a.V / Ele<E>::kPer + kChunk - 1) / kChunk;
+    const int64_t beside = TOP ? static_cast<int64_t>(sizeof(TopState)) : OP == kDistill ? (a.K + 3) / 4 * 64 : 0;
+    int64_t slots = (kSharedOfSm / kCtas - 2048 - beside) / (kChunk * 16);
+    if (slots < 1) slots = 1;
+    int64_t cluster = 1;
+    if (GRAD)
+        while (cluster < kMaxCluster && (chunks + cluster - 1) / cluster > slots) ++cluster;
+    while (cluster < kMaxCluster && T * (cluster + 1) <= static_cast<int64_t>(kCtas) * sms && chunks > cluster) ++cluster;
+    const int64_t each = chunks > 0 ? (chunks + cluster - 1) / cluster : 1;
+    a.passes = 1;
+    if (GRAD && each > slots) {
+        slots = each < kSlotsMost ? each : kSlotsMost;
+        if (each > slots) a.passes = 2;
+    }
+    int64_t rows = T * cluster / (4 * kCtas * static_cast<int64_t>(sms));
+    rows = rows < 1 ? 1 : rows > kRowsMost ? kRowsMost : rows;
+    if (slots > each * rows) slots = each * rows;
+    if (slots > kSlotsMost) slots = kSlotsMost;
+    a.T = T;
+    a.cluster = static_cast<int>(cluster);
+    a.per = static_cast<int>((a.V / Ele<E>::kPer + cluster - 1) / cluster);
+    a.rows = static_cast<int>(rows);
+    a.slots = static_cast<int>(slots);
+    const size_t dyn = static_cast<size_t>(slots) * kChunk * 16 + static_cast<size_t>(beside);
+    const int64_t ctas = (T + rows - 1) / rows * cluster;
     auto kernel = rows_kernel<E, OP, GRAD, TOP>;
-    if (T * a.cluster > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;
-    if (dyn > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dyn)) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_CUDA;
+    if (ctas > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;
+    // the kernel's shared-memory opt-in, once a device
+    static std::atomic<uint64_t> prepared{0};
+    const uint64_t bit = device < kDevices ? uint64_t(1) << device : 0;
+    if (!(prepared.load(std::memory_order_relaxed) & bit) || !bit) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamicMost) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        prepared.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(T * a.cluster), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(kBlock, 1, 1);
     cfg.dynamicSmemBytes = dyn;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -844,12 +1170,15 @@ gemm_status_t launch(Args a, int64_t T, int device, cudaStream_t stream) {
 template <int OP, bool GRAD, bool TOP>
 gemm_status_t launch_type(int device, gemm_dtype_t dtype, const Args& a, int64_t T, void* stream) {
     if (T == 0) return GEMM_OK;
+    int sms = 0;
+    const gemm_status_t st = sms_of(device, &sms);
+    if (st != GEMM_OK) return st;
     const OnDevice on(device);
-    if (on.status != GEMM_OK) return on.status;
+    if (!on.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == GEMM_F32) return launch<float, OP, GRAD, TOP>(a, T, device, s);
-    if (dtype == GEMM_F16) return launch<__half, OP, GRAD, TOP>(a, T, device, s);
-    return launch<__nv_bfloat16, OP, GRAD, TOP>(a, T, device, s);
+    if (dtype == GEMM_F32) return launch<float, OP, GRAD, TOP>(a, T, device, sms, s);
+    if (dtype == GEMM_F16) return launch<__half, OP, GRAD, TOP>(a, T, device, sms, s);
+    return launch<__nv_bfloat16, OP, GRAD, TOP>(a, T, device, sms, s);
 }
 
 void fill_rows(Args& a, const void* logits, int64_t V, int64_t ld, float temperature) {

@@ -93,10 +93,17 @@ def _gradient(dlogits, logits):
     return dlogits, _matrix(dlogits, "dlogits")[2]
 
 
+_entry = {}
+
+
 def _call(name: str, *args):
-    from . import GemmError, load
-    st = getattr(load(), name)(*args)
+    f = _entry.get(name)
+    if f is None:
+        from . import load
+        f = _entry[name] = getattr(load(), name)
+    st = f(*args)
     if st != 0:
+        from . import GemmError
         raise GemmError(st, name)
 
 
@@ -104,7 +111,7 @@ def _stream(stream, device):
     if stream is not None:
         return stream
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)    # current_stream() takes 2 us to make an object
 
 
 def token_logprobs(logits, tokens=None, top: int = 0, *, temperature: float = 1.0, stream=None) -> TokenLogprobs:
@@ -120,13 +127,14 @@ def token_logprobs(logits, tokens=None, top: int = 0, *, temperature: float = 1.
     tok = _vector(tokens, T, torch.int64, dev, "tokens")
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"top must be 0..{MAX_TOP}")
+    # the launch before the views: the GPU starts while they are made
     out = torch.empty((2 + n, T), dtype=torch.float32, device=dev)
     top_lp = torch.empty((T, top), dtype=torch.float32, device=dev)
     top_tok = torch.empty((T, top), dtype=torch.int64, device=dev)
-    parts = out.unbind(0)
     at, step = out.data_ptr(), 4 * T
     _call("logits_logprobs", dev.index, code, logits.data_ptr(), T, V, ld, tok, temperature, top,
           at + 2 * step if n else None, at, at + step, top_lp.data_ptr(), top_tok.data_ptr(), _stream(stream, dev))
+    parts = out.unbind(0)
     return TokenLogprobs(parts[2] if n else None, parts[0], parts[1], top_lp, top_tok)
 
 
@@ -148,10 +156,10 @@ def token_logprobs_grad(logits, tokens=None, grad_logprob=None, grad_entropy=Non
         raise ValueError("grad_logprob needs tokens")
     dlogits, ldd = _gradient(dlogits, logits)
     out = torch.empty((2 + n, T), dtype=torch.float32, device=dev)
-    parts = out.unbind(0)
     at, step = out.data_ptr(), 4 * T
     _call("logits_logprobs_grad", dev.index, code, logits.data_ptr(), T, V, ld, tok, temperature, g, h,
           at + 2 * step if n else None, at, at + step, dlogits.data_ptr(), ldd, _stream(stream, dev))
+    parts = out.unbind(0)
     return TokenLogprobsGrad(parts[2] if n else None, parts[0], parts[1], dlogits)
 
 
