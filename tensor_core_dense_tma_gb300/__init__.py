@@ -451,10 +451,15 @@ def gemm_measure_mma_rate(device: int = 0, in_dtype: str = "f16", accum_dtype: s
 _TORCH_DT = {"f16": "float16", "bf16": "bfloat16", "f32": "float32"}
 
 
+_dt_names: dict = {}
+
+
 def _dt_name(t) -> str:
-    import torch
-    return {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.float8_e4m3fn: "e4m3",
-            torch.float8_e5m2: "e5m2"}[t.dtype]
+    if not _dt_names:
+        import torch
+        _dt_names.update({torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32",
+                          torch.float8_e4m3fn: "e4m3", torch.float8_e5m2: "e5m2"})
+    return _dt_names[t.dtype]
 
 
 def _operand_layout(t, what: str):
@@ -624,30 +629,49 @@ class Plan:
                      M, N, K, lda, ldb, max(ldc, N), la, lb, accum_dtype, out_dtype, alpha, beta, stream, ep=ep)
         return D
 
-    def _resolve_i8(self, A, B, D, out_dtype):
-        """Sizes and strides of an 8-bit product (D allocated if not given)."""
+    # A decoding step's product takes a few microseconds, so these two look at
+    # each tensor once.
+    def _run_i8(self, A, B, D, row_scale, col_scale, bias, act, out_dtype, stream):
         import torch
-        lda = _row_stride(A, "A")
-        M, K = A.shape
-        if B.dtype != torch.int8 or B.dim() != 2 or not B.is_cuda:
-            raise ValueError("B must be a 2-D int8 device tensor")
-        if B.shape[0] != K:
+        (M, K), (a0, a1) = A.shape, A.stride()
+        (KB, N), (b0, b1) = B.shape, B.stride()
+        dev = A.device
+        if B.dtype != torch.int8 or not A.is_cuda or B.device != dev:
+            raise ValueError("A and B must be on one device, B int8")
+        if KB != K:
             raise ValueError("inner dimensions differ")
-        N = B.shape[1]
-        if K > 1 and B.stride(0) != 1:
+        if (K > 1 and a1 != 1) or (M > 1 and a0 < K):
+            raise ValueError(f"A must be row-major (strides {A.stride()})")
+        if (K > 1 and b0 != 1) or (N > 1 and b1 < K):
             raise ValueError("B must be column-major: the transpose of a row-major N x K weight matrix")
-        ldb = B.stride(1) if N > 1 else -(-max(K, 1) // 16) * 16
-        if M == 1:
-            lda = -(-max(K, 1) // 16) * 16 if A.dtype == torch.int8 else K
         if D is None:
-            D = torch.empty((M, N), dtype=getattr(torch, _TORCH_DT[out_dtype or "f32"]), device=A.device)
-        elif out_dtype is not None and _dt_name(D) != out_dtype:
-            raise ValueError("D must have the output type")
-        if D.shape != (M, N):
-            raise ValueError("D must be an M x N matrix")
-        if not (A.device == B.device == D.device):
-            raise ValueError("A, B and D must be on one device")
-        return M, N, K, lda, ldb, _row_stride(D, "D"), _dt_name(D), D
+            D = torch.empty((M, N), dtype=getattr(torch, _TORCH_DT[out_dtype]), device=dev)
+            ldd = N
+        else:
+            have = _dt_name(D)
+            if out_dtype is not None and have != out_dtype:
+                raise ValueError("D must have the output type")
+            out_dtype = have
+            d0, d1 = D.stride() if D.dim() == 2 else (0, 0)
+            if D.shape != (M, N) or D.device != dev or (N > 1 and d1 != 1) or (M > 1 and d0 < N):
+                raise ValueError("D must be a row-major M x N matrix on A's device")
+            ldd = d0 if M > 1 else N
+        units = -(-K // 16) * 16 or 16            # a stride for a single row, which has none of its own
+        whole = A.dtype == torch.int8
+        lda = a0 if M > 1 else units if whole else max(K, 1)
+        ldb = b1 if N > 1 else units
+        ep = _make_epilogue(M, N, bias, row_scale, col_scale, act)
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        if whole:
+            st = gemm_run_i8(self.handle, A.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, lda, ldb, ldd, out_dtype,
+                             ep, stream)
+        else:
+            st = gemm_run_i8_dynamic(self.handle, A.data_ptr(), _dt_name(A), B.data_ptr(), D.data_ptr(), M, N, K, lda,
+                                     ldb, ldd, out_dtype, ep, stream)
+        if st != 0:
+            raise GemmError(st, "gemm_run_i8" if whole else "gemm_run_i8_dynamic")
+        return D
 
     def gemm_i8(self, A, B, D=None, *, row_scale=None, col_scale=None, bias=None, act: str = "none",
                 out_dtype: str | None = None, stream=None):
@@ -656,34 +680,21 @@ class Plan:
         B column-major K x N (``W.t()`` of row-major weights), the vectors
         fp32; returns D (fp32 unless out_dtype or D says otherwise)."""
         import torch
-        if A.dtype != torch.int8:
-            raise ValueError("A must be int8")
-        M, N, K, lda, ldb, ldd, out_dtype, D = self._resolve_i8(A, B, D, out_dtype)
-        ep = _make_epilogue(M, N, bias, row_scale, col_scale, act)
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(A.device.index)
-        st = gemm_run_i8(self.handle, A.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, lda, ldb, ldd, out_dtype, ep,
-                         stream)
-        if st != 0:
-            raise GemmError(st, "gemm_run_i8")
-        return D
+        if A.dtype != torch.int8 or A.dim() != 2 or B.dim() != 2:
+            raise ValueError("A and B must be 2-D int8 tensors")
+        return self._run_i8(A, B, D, row_scale, col_scale, bias, act,
+                            out_dtype if D is not None else out_dtype or "f32", stream)
 
     def linear_i8(self, X, B, D=None, *, col_scale=None, bias=None, act: str = "none", out_dtype: str | None = None,
                   stream=None):
         """gemm_i8 of rows of fp32, fp16 or bf16 values: X (M x K, row-major)
         is quantised row by row in the call (gemm_run_i8_dynamic); returns D
         (X's type unless out_dtype or D says otherwise)."""
-        import torch
-        xt = _dt_name(X)
-        M, N, K, ldx, ldb, ldd, out_dtype, D = self._resolve_i8(X, B, D, out_dtype or (xt if D is None else None))
-        ep = _make_epilogue(M, N, bias, None, col_scale, act)
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(X.device.index)
-        st = gemm_run_i8_dynamic(self.handle, X.data_ptr(), xt, B.data_ptr(), D.data_ptr(), M, N, K, ldx, ldb, ldd,
-                                 out_dtype, ep, stream)
-        if st != 0:
-            raise GemmError(st, "gemm_run_i8_dynamic")
-        return D
+        xt = _dt_name(X) if X.is_floating_point() else None
+        if xt not in _TORCH_DT or X.dim() != 2 or B.dim() != 2:
+            raise ValueError("X must be a 2-D fp32, fp16 or bf16 tensor, B a 2-D int8 one")
+        return self._run_i8(X, B, D, None, col_scale, bias, act, out_dtype if D is not None else out_dtype or xt,
+                            stream)
 
     def _resolve(self, A, B, C, D, out_dtype):
         """Sizes, storage orders and leading dimensions from the tensors'

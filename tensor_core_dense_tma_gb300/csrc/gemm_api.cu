@@ -986,7 +986,7 @@ gemm_status_t gemm_plan_destroy(gemm_plan_t plan) {
         if (plan->d_ws) cudaFree(plan->d_ws);
         if (plan->d_counters) cudaFree(plan->d_counters);
         if (plan->d_flags) cudaFree(plan->d_flags);
-        if (plan->d_i8) cudaFree(plan->d_i8);
+        for (int i = 0; i < plan->i8_buffers; ++i) cudaFree(plan->d_i8[i]);
         if (plan->status_stream) cudaStreamDestroy(plan->status_stream);
         destroy_host_pipeline(plan->host_pipe);
     }

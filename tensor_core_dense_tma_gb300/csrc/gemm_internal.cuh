@@ -26,6 +26,9 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 constexpr size_t kWorkspaceBytes = size_t(64) << 20;
 constexpr int kNumCounters = 8192;
 constexpr int kMaxSplits = 16;
+// Buffers of the 8-bit product, each at least twice as large as the one
+// before, the first 1 MiB or more.
+constexpr int kI8Buffers = 28;
 
 // Kernel configurations (tile rows x tile columns, CTAs per tile, stages):
 //  single16 / single64 : one CTA, 128 x 16 / 128 x 64, 8 stages -- the
@@ -129,8 +132,10 @@ struct gemm_plan {
     bool attr_set[tcdt_host::kNumCfgKinds][8] = {};   // [kind][output slot + 4 * fused epilogue]
     int units[tcdt_host::kNumCfgKinds] = {};  // co-resident CTAs (single) or CTA pairs (pair)
     size_t ws_bytes = 0;          // capacity of d_ws
-    void* d_i8 = nullptr;         // gemm_run_i8's operands as fp16 codes and row scales (owned; null until used)
-    size_t i8_bytes = 0;          // capacity of d_i8
+    void* d_i8[tcdt_host::kI8Buffers] = {};   // gemm_run_i8's codes and row scales: the last one is in use (owned)
+    int i8_buffers = 0;
+    size_t i8_bytes = 0;          // capacity of the last of them
+    bool i8_prepared[4][3] = {};  // its kernels' shared-memory opt-in done ([tile][output])
     int forced_kind = -1;         // gemm_plan_force_config
 #ifdef TCDT_FAULT_INJECTION
     int64_t fi_skip_load = -1;    // test builds only

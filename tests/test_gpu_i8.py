@@ -261,3 +261,22 @@ def test_refusals(tc, plan):
         tc.quantize_rows_i8(A.float().t())
     with pytest.raises(ValueError):
         tc.quantize_rows_i8(A.float(), scale=f)
+
+
+def test_graph_outlives_a_grown_workspace(tc):
+    """A graph captured before a larger call made the plan's workspace grow."""
+    with tc.Plan("f16", 0) as plan:
+        A, a = codes(40, 500, 1)
+        W, w = codes(300, 500, 2)
+        D = plan.gemm_i8(A, W.t())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan.gemm_i8(A, W.t(), D)
+        big, _ = codes(3000, 2000, 3)
+        plan.gemm_i8(big, big.t())
+        D.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(D.cpu().numpy().astype(np.int64), a @ w.T)
+        assert plan.device_status() == 0
