@@ -33,20 +33,19 @@
 namespace {
 
 constexpr int kThreads = 256;            // that compute; one more warp starts the copies
-// CTAs an SM: a gradient's ring holds a whole segment, and fewer CTAs a row
-// wait for one another less (4096 x 131072 bf16 with gradient: 3 CTAs 456 us,
-// 2 CTAs 509, 4 CTAs 541; alternatives without gradient: 4 CTAs 287 us, 3 334, 5 353).
+// CTAs an SM (4096 x 131072 bf16 with gradient: 3 CTAs 372 us, 4 CTAs 408, 5 CTAs
+// 531; 64 alternatives: 4 CTAs 287 us, 3 CTAs 334, 5 CTAs 353 in an earlier form).
 constexpr int ctas_of(bool grad) { return grad ? 3 : 4; }
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 1024 / kThreads; // 16-byte vectors of a thread in a chunk
 constexpr int kChunk = kUnroll * kThreads;   // vectors of an asynchronous copy: 16 KB
 constexpr int kSlotsMost = 12;           // of the ring
-constexpr int kRowsMost = 8;              // rows a cluster takes one after another
 constexpr int kBlock = kThreads + 32;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 1024;        // kMaxCluster lists of LOGITS_MAX_TOP fit too
 constexpr int kSlack = 64;               // buckets more than wanted that are not worth telling ties apart
+constexpr int64_t kInFlight = 64 << 20;  // bytes of logits that a gradient's CTAs work on at once
 constexpr int64_t kSharedOfSm = 228 * 1024;
 constexpr int kDynamicMost = 225 * 1024;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -63,7 +62,6 @@ struct Args {
     int64_t T;
     int cluster, rows, slots;     // CTAs of a row, rows of a cluster, chunks of the ring
     int per;                      // vectors of a segment
-    int passes;                   // 2: a segment exceeds the ring, the gradient reads it again
     float c, inv_t, t;            // log2(e) / temperature, 1 / temperature, temperature
     const int64_t* tokens;        // [T], or teacher tokens [T][ldt]
     // log-probabilities
@@ -609,9 +607,12 @@ __device__ __forceinline__ void select_top(TopState& t, uint64_t* list, int* cou
 // memory: one warp starts asynchronous copies, into a slot as soon as all
 // computing warps have given it back, and so runs ahead into the next row
 // while this one's sums are joined, its alternatives selected or its gradient
-// written.  The gradient reads the chunks where the statistics left them (a
-// segment fits the ring, unless the row is too long for kMaxCluster CTAs: then
-// it is copied in twice).  The segments' statistics go from each CTA into
+// written.  The gradient takes the last chunks first, where the statistics left
+// them in the ring, and the others are copied in again, from L2: the host
+// splits rows only so far that those in flight fit there, as the CTAs of a row
+// wait for one another (4096 x 131072 bf16 kept in the ring whole, in clusters of
+// four: 454 us, in clusters of two 375; gradient stores are marked streaming to
+// leave L2 to the logits).  The segments' statistics go from each CTA into
 // every other one's shared memory, counted by an mbarrier.
 // A copy that has not arrived after kWaitLimitNs is not waited for again: its
 // vectors, and all later ones, are read from memory; statistics that have not
@@ -659,16 +660,17 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             bool ok = true;
             for (int64_t r = row0; ok && r < row1; ++r) {
                 const Segment<E> seg(a.z, r * a.ld, a.V, rank, a.cluster, a.per);
-                for (int pass = 0; ok && pass < a.passes; ++pass)
-                    for (int from = 0; from < seg.n; from += kChunk) {
-                        ok = wait_copy(empty + 8 * slot, parity);
-                        if (!ok) break;
-                        const uint32_t bytes = static_cast<uint32_t>(min(kChunk, seg.n - from)) * 16u;
-                        tcdt::mbar_arrive_expect_tx(full + 8 * slot, bytes);
-                        copy_bulk(tcdt::smem_addr(ring + slot * kChunk), seg.vec + from, bytes, full + 8 * slot);
-                        ++started;
-                        if (++slot == a.slots) slot = 0, parity ^= 1u;
-                    }
+                const int chunks = seg.chunks(), again = GRAD ? chunks - min(chunks, a.slots) : 0;
+                for (int i = 0; i < chunks + again; ++i) {
+                    const int from = (i < chunks ? i : i - chunks) * kChunk;
+                    ok = wait_copy(empty + 8 * slot, parity);
+                    if (!ok) break;
+                    const uint32_t bytes = static_cast<uint32_t>(min(kChunk, seg.n - from)) * 16u;
+                    tcdt::mbar_arrive_expect_tx(full + 8 * slot, bytes);
+                    copy_bulk(tcdt::smem_addr(ring + slot * kChunk), seg.vec + from, bytes, full + 8 * slot);
+                    ++started;
+                    if (++slot == a.slots) slot = 0, parity ^= 1u;
+                }
             }
             // a copy must not land in another CTA's memory
             for (int i = 0; i < a.slots && i < started; ++i)
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
 
     for (int64_t r = row0; r < row1; ++r) {
         const Segment<E> seg(a.z, r * a.ld, a.V, rank, a.cluster, a.per);
-        const int chunks = seg.chunks();
+        const int chunks = seg.chunks(), kept = GRAD ? min(chunks, a.slots) : 0;    // kept in the ring
         const int turn = static_cast<int>(r - row0);
 
         // The given token, or the teacher's entries, and the elements beside
@@ -755,8 +757,6 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         float bucket_max = -INFINITY, bucket_second = -INFINITY;     // of its chunks' maxima
         int bucket_batch = 0;
         Stats s = empty_stats();
-        const int slot0 = slot;
-        const uint32_t parity0 = parity;
         const uint64_t c2 = pair(a.c, a.c);
         {
             uint64_t m2 = pair(-s.m, -s.m), S2 = 0, U2 = 0;
@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             if (chunks == 0) given();
             for (int b = 0; b < chunks; ++b) {
                 uint4 q[kUnroll];
-                take(seg, b, !GRAD || a.passes == 2, q);
+                take(seg, b, b < chunks - kept, q);
                 if (b == 0) given();
                 const float m = Ele<E>::template max_of<kUnroll>(q);
                 if constexpr (TOP) {
@@ -922,8 +922,9 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                 }
                 return mul2(ex2_2(l2), g2);
             };
-            if (a.passes == 1) slot = slot0, parity = parity0;
-            for (int b = 0; b < chunks; ++b) {
+            if ((slot -= kept) < 0) slot += a.slots, parity ^= 1u;
+            for (int i = 0; i < chunks; ++i) {
+                const int b = i < kept ? chunks - kept + i : i - kept;
                 uint4 q[kUnroll];
                 const bool inside = take(seg, b, true, q);
                 const int v0 = b * kChunk + tid;
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                         Ele<E>::pairs(q[k], x);
 #pragma unroll
                         for (int e = 0; e < kPer / 2; ++e) x[e] = gradient(x[e]);
-                        at[k * kThreads] = Ele<E>::pack_pairs(x);
+                        __stcs(at + k * kThreads, Ele<E>::pack_pairs(x));
                     }
                 } else {
 #pragma unroll
@@ -1106,28 +1107,25 @@ struct OnDevice {
 
 template <typename E, int OP, bool GRAD, bool TOP>
 gemm_status_t launch(Args a, int64_t T, int device, int sms, cudaStream_t stream) {
-    // The ring takes what shared memory is left with kCtas CTAs an SM.  A
-    // gradient wants a segment to fit it: as many CTAs as that takes, and if
-    // kMaxCluster are not enough a larger ring, with fewer CTAs an SM, and
-    // beyond that two passes.  Rows are also split while that fills idle SMs
-    // and leaves every CTA a chunk.
+    // The ring takes what shared memory kCtas CTAs an SM leave.  A gradient's
+    // rows in flight, which it reads twice, are to fit half of L2 (kInFlight).
+    // Rows are also split while that fills idle SMs and leaves every CTA a chunk.
     constexpr int kCtas = ctas_of(GRAD);
     const int64_t chunks = (a.V / Ele<E>::kPer + kChunk - 1) / kChunk;
     const int64_t beside = TOP ? static_cast<int64_t>(sizeof(TopState)) : OP == kDistill ? (a.K + 3) / 4 * 64 : 0;
     int64_t slots = (kSharedOfSm / kCtas - 2048 - beside) / (kChunk * 16);
-    if (slots < 1) slots = 1;
+    const int64_t ctas_at_once = static_cast<int64_t>(kCtas) * sms;
     int64_t cluster = 1;
     if (GRAD)
-        while (cluster < kMaxCluster && (chunks + cluster - 1) / cluster > slots) ++cluster;
-    while (cluster < kMaxCluster && T * (cluster + 1) <= static_cast<int64_t>(kCtas) * sms && chunks > cluster) ++cluster;
+        while (cluster < kMaxCluster && chunks > slots &&
+               (T * cluster < ctas_at_once ? T : ctas_at_once / cluster) * a.V * static_cast<int64_t>(sizeof(E)) > kInFlight)
+            ++cluster;
+    while (cluster < kMaxCluster && T * (cluster + 1) <= ctas_at_once && chunks > cluster) ++cluster;
     const int64_t each = chunks > 0 ? (chunks + cluster - 1) / cluster : 1;
-    a.passes = 1;
-    if (GRAD && each > slots) {
-        slots = each < kSlotsMost ? each : kSlotsMost;
-        if (each > slots) a.passes = 2;
-    }
-    int64_t rows = T * cluster / (4 * kCtas * static_cast<int64_t>(sms));
-    rows = rows < 1 ? 1 : rows > kRowsMost ? kRowsMost : rows;
+    // Two rows one after another save a start where a row is short and the
+    // CTAs are many (8192 x 8192 bf16 with gradient: 83 us with one, 74 with
+    // two, 77 with four; 4096 x 131072 bf16, 64 alternatives: 217, 230, 241).
+    const int64_t rows = each <= 2 && T * cluster >= 8 * ctas_at_once ? 2 : 1;
     if (slots > each * rows) slots = each * rows;
     if (slots > kSlotsMost) slots = kSlotsMost;
     a.T = T;
