@@ -475,19 +475,30 @@ def _operand_layout(t, what: str):
     raise ValueError(f"{what} must be row- or column-major (strides {t.stride()})")
 
 
+def _epilogue_vector(v, n, what):
+    import torch
+    if v is None:
+        return None
+    if v.dtype != torch.float32 or v.dim() != 1 or v.shape[0] != n or not v.is_cuda or v.stride(0) != 1:
+        raise ValueError(f"{what} must be a contiguous fp32 device vector of length {n}")
+    return v.data_ptr()
+
+
 def _make_epilogue(M, N, bias, row_scale, col_scale, act):
     """The gemm_epilogue_t of optional fp32 DEVICE vectors, or None."""
-    import torch
     if bias is None and row_scale is None and col_scale is None and act == "none":
         return None
+    return Epilogue(_epilogue_vector(bias, N, "bias"), _epilogue_vector(row_scale, M, "row_scale"),
+                    _epilogue_vector(col_scale, N, "col_scale"), ACT[act])
 
-    def vec(v, n, what):
-        if v is None:
-            return None
-        if v.dtype != torch.float32 or v.dim() != 1 or v.shape[0] != n or not v.is_cuda or v.stride(0) != 1:
-            raise ValueError(f"{what} must be a contiguous fp32 device vector of length {n}")
-        return v.data_ptr()
-    return Epilogue(vec(bias, N, "bias"), vec(row_scale, M, "row_scale"), vec(col_scale, N, "col_scale"), ACT[act])
+
+_i8_calls: dict = {}
+
+
+def _load_i8_calls():
+    import torch
+    _i8_calls.update(torch=torch, static=load().gemm_run_i8, dynamic=load().gemm_run_i8_dynamic)
+    return torch
 
 
 def _row_stride(t, what: str) -> int:
@@ -629,14 +640,14 @@ class Plan:
                      M, N, K, lda, ldb, max(ldc, N), la, lb, accum_dtype, out_dtype, alpha, beta, stream, ep=ep)
         return D
 
-    # A decoding step's product takes a few microseconds, so these two look at
-    # each tensor once.
+    # A decoding step's product takes a few microseconds of kernel, so this
+    # looks at each tensor once and calls the library's function directly.
     def _run_i8(self, A, B, D, row_scale, col_scale, bias, act, out_dtype, stream):
-        import torch
+        torch = _i8_calls.get("torch") or _load_i8_calls()
         (M, K), (a0, a1) = A.shape, A.stride()
         (KB, N), (b0, b1) = B.shape, B.stride()
         dev = A.device
-        if B.dtype != torch.int8 or not A.is_cuda or B.device != dev:
+        if B.dtype != torch.int8 or dev.type != "cuda" or B.device != dev:
             raise ValueError("A and B must be on one device, B int8")
         if KB != K:
             raise ValueError("inner dimensions differ")
@@ -661,14 +672,16 @@ class Plan:
         lda = a0 if M > 1 else units if whole else max(K, 1)
         ldb = b1 if N > 1 else units
         ep = _make_epilogue(M, N, bias, row_scale, col_scale, act)
+        if ep is not None:
+            ep = ctypes.byref(ep)
         if stream is None:
             stream = torch._C._cuda_getCurrentRawStream(dev.index)
         if whole:
-            st = gemm_run_i8(self.handle, A.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, lda, ldb, ldd, out_dtype,
-                             ep, stream)
+            st = _i8_calls["static"](self.handle, A.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, lda, ldb, ldd,
+                                     DTYPE[out_dtype], ep, stream)
         else:
-            st = gemm_run_i8_dynamic(self.handle, A.data_ptr(), _dt_name(A), B.data_ptr(), D.data_ptr(), M, N, K, lda,
-                                     ldb, ldd, out_dtype, ep, stream)
+            st = _i8_calls["dynamic"](self.handle, A.data_ptr(), DTYPE[_dt_name(A)], B.data_ptr(), D.data_ptr(), M, N,
+                                      K, lda, ldb, ldd, DTYPE[out_dtype], ep, stream)
         if st != 0:
             raise GemmError(st, "gemm_run_i8" if whole else "gemm_run_i8_dynamic")
         return D
@@ -679,7 +692,7 @@ class Plan:
         device tensors on an "f16" plan (gemm_run_i8): A row-major M x K,
         B column-major K x N (``W.t()`` of row-major weights), the vectors
         fp32; returns D (fp32 unless out_dtype or D says otherwise)."""
-        import torch
+        torch = _i8_calls.get("torch") or _load_i8_calls()
         if A.dtype != torch.int8 or A.dim() != 2 or B.dim() != 2:
             raise ValueError("A and B must be 2-D int8 tensors")
         return self._run_i8(A, B, D, row_scale, col_scale, bias, act,

@@ -258,16 +258,15 @@ gemm_status_t check_product(gemm_plan* plan, const void* B, const void* D, int64
 // Kernels of the product, by the number of tokens M.
 enum Path { kDot, kTile, kWide };
 
-Path path_of(int64_t M, int64_t N, int64_t K, bool quantised_here, int sms) {
+Path path_of(int64_t M, int64_t N, int64_t K, int sms) {
     // Whole-number sums: K products of up to 2^14 stay within 31 bits.
-    // Measured against the tile kernel (us, 1 / 3 / 8 tokens): 2048 x 2048
-    // weights 4.3 / 3.5 / 5.2 to 6.1 / 6.2 / 6.4, 4096 x 4096 6.4 / 7.9 / 12.6
-    // to 9.2 / 9.2 / 9.3, 8192 x 8192 14.0 / 16.6 / 26.6 to 15.9 / 16.1 / 16.1;
-    // where the tokens are quantised in the call the tile kernel has more of
-    // the weights under way meanwhile (8192 x 8192, 1 token: 19.5 to 17.0).
+    // Measured against the tile kernel (us, 1 / 4 / 8 tokens): 2048 x 2048
+    // weights 3.4 / 3.4 / 4.6 to 6.1 / 6.2 / 6.4, 4096 x 4096 4.9 / 6.9 / 11.3 to
+    // 9.2 / 9.2 / 9.3, 8192 x 8192 12.6 / 18.7 / 26.2 to 15.9 / 16.1 / 16.1, and
+    // with 1 token quantised in the call 14.2 to 17.0.
     if (K < (1 << 17)) {
         const int64_t weights = N * K;
-        if (M <= 2 && !quantised_here) return kDot;
+        if (M <= 2) return kDot;
         if (M <= 4 && weights <= (1 << 24)) return kDot;
         if (M <= 8 && weights <= (1 << 22)) return kDot;
     }
@@ -386,7 +385,7 @@ gemm_status_t run_product(gemm_plan* plan, const int8_t* A, const void* X, gemm_
                           const gemm_epilogue_t* ep_in, cudaStream_t s) {
     gemm_epilogue_t ep{};
     if (ep_in) ep = *ep_in;
-    const Path path = path_of(M, N, K, X != nullptr, plan->sm_count);
+    const Path path = path_of(M, N, K, plan->sm_count);
     const int64_t ldh = round_up(K, path == kDot ? 16 : 8);
     const size_t a_bytes = static_cast<size_t>(round_up(M * ldh * (path == kDot ? 1 : 2), 256));
     const size_t b_bytes = path == kWide ? static_cast<size_t>(round_up(N * ldh * 2, 256)) : 0;

@@ -48,14 +48,13 @@ def declare(lib: ctypes.CDLL) -> None:
         f.restype = i32
 
 
-_types = None
+_types: dict = {}      # filled on the first use, with the library's entry points
 
 
 def _dtype(t) -> int:
-    global _types
-    if _types is None:
+    if not _types:
         import torch
-        _types = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+        _types.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
     code = _types.get(t.dtype)
     if code is None:
         raise ValueError(f"fp32, fp16 or bf16 wanted, got {t.dtype}")
