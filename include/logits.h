@@ -28,7 +28,10 @@
  * ordinal, made current while the call runs and then restored) and
  * synchronises nothing, so it may be captured in a graph.  Calls are
  * independent: any number may run at once, from any threads and streams.
- * Results do not depend on timing: the same inputs give the same bits.
+ * Results do not depend on timing: the same inputs give the same bits.  Every
+ * wait inside a kernel is bounded: a copy that has not arrived after 2 s is
+ * made up for by plain loads, a row whose CTAs then still wait for one another's
+ * statistics becomes NaN.
  *
  * Errors.  Arguments are checked on the host before anything is launched:
  * GEMM_ERR_INVALID_ARG (null pointer, negative size, stride below its row

@@ -8,6 +8,9 @@ computation is one CUDA kernel per call on the given (or current) stream.
 ``logits`` is a T x V device tensor of fp32, fp16 or bf16 with unit column
 stride; rows may be padded (the product that feeds on a gradient wants row
 strides of whole 16 bytes, and an allocated gradient has them).
+
+What a call allocates belongs to torch's current stream; with another
+``stream`` order the two, as for any tensor used on a second stream.
 """
 from __future__ import annotations
 
@@ -92,6 +95,15 @@ def _gradient(dlogits, logits):
     return dlogits, _matrix(dlogits, "dlogits")[2]
 
 
+def _outputs(T: int, dev, first: bool):
+    """Three fp32 vectors of length T (the first one only if asked for).
+    Allocated one by one: views of a common buffer take twice as long to make."""
+    import torch
+    f32 = torch.float32
+    return (torch.empty((T,), dtype=f32, device=dev) if first else None,
+            torch.empty((T,), dtype=f32, device=dev), torch.empty((T,), dtype=f32, device=dev))
+
+
 _entry = {}
 
 
@@ -122,19 +134,16 @@ def token_logprobs(logits, tokens=None, top: int = 0, *, temperature: float = 1.
     T, V, ld = _matrix(logits, "logits")
     dev = logits.device
     code = _dtype(logits)
-    n = 0 if tokens is None else 1
     tok = _vector(tokens, T, torch.int64, dev, "tokens")
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"top must be 0..{MAX_TOP}")
-    # the launch before the views: the GPU starts while they are made
-    out = torch.empty((2 + n, T), dtype=torch.float32, device=dev)
+    lp, entropy, lse = _outputs(T, dev, tokens is not None)
     top_lp = torch.empty((T, top), dtype=torch.float32, device=dev)
     top_tok = torch.empty((T, top), dtype=torch.int64, device=dev)
-    at, step = out.data_ptr(), 4 * T
     _call("logits_logprobs", dev.index, code, logits.data_ptr(), T, V, ld, tok, temperature, top,
-          at + 2 * step if n else None, at, at + step, top_lp.data_ptr(), top_tok.data_ptr(), _stream(stream, dev))
-    parts = out.unbind(0)
-    return TokenLogprobs(parts[2] if n else None, parts[0], parts[1], top_lp, top_tok)
+          lp.data_ptr() if lp is not None else None, entropy.data_ptr(), lse.data_ptr(), top_lp.data_ptr(),
+          top_tok.data_ptr(), _stream(stream, dev))
+    return TokenLogprobs(lp, entropy, lse, top_lp, top_tok)
 
 
 def token_logprobs_grad(logits, tokens=None, grad_logprob=None, grad_entropy=None, *, temperature: float = 1.0,
@@ -147,19 +156,17 @@ def token_logprobs_grad(logits, tokens=None, grad_logprob=None, grad_entropy=Non
     T, V, ld = _matrix(logits, "logits")
     dev = logits.device
     code = _dtype(logits)
-    n = 0 if tokens is None else 1
     tok = _vector(tokens, T, torch.int64, dev, "tokens")
     g = _vector(grad_logprob, T, torch.float32, dev, "grad_logprob")
     h = _vector(grad_entropy, T, torch.float32, dev, "grad_entropy")
     if grad_logprob is not None and tokens is None:
         raise ValueError("grad_logprob needs tokens")
     dlogits, ldd = _gradient(dlogits, logits)
-    out = torch.empty((2 + n, T), dtype=torch.float32, device=dev)
-    at, step = out.data_ptr(), 4 * T
+    lp, entropy, lse = _outputs(T, dev, tokens is not None)
     _call("logits_logprobs_grad", dev.index, code, logits.data_ptr(), T, V, ld, tok, temperature, g, h,
-          at + 2 * step if n else None, at, at + step, dlogits.data_ptr(), ldd, _stream(stream, dev))
-    parts = out.unbind(0)
-    return TokenLogprobsGrad(parts[2] if n else None, parts[0], parts[1], dlogits)
+          lp.data_ptr() if lp is not None else None, entropy.data_ptr(), lse.data_ptr(), dlogits.data_ptr(), ldd,
+          _stream(stream, dev))
+    return TokenLogprobsGrad(lp, entropy, lse, dlogits)
 
 
 def _teacher(teacher_tokens, teacher_logits, T, dev):
@@ -184,16 +191,13 @@ def distill_topk(logits, teacher_tokens, teacher_logits, *, temperature: float =
     the teacher's top logits (T x K with their int64 tokens; a token outside
     0..V-1 is padding) at `temperature`, Q the student's over the vocabulary.
     Returns (loss, lse), lse that of logits / temperature (logits_distill)."""
-    import torch
     T, V, ld = _matrix(logits, "logits")
     dev = logits.device
     code = _dtype(logits)
     teacher = _teacher(teacher_tokens, teacher_logits, T, dev)
-    out = torch.empty((2, T), dtype=torch.float32, device=dev)
-    at = out.data_ptr()
-    _call("logits_distill", dev.index, code, logits.data_ptr(), T, V, ld, *teacher, temperature, at, at + 4 * T,
-          _stream(stream, dev))
-    loss, lse = out.unbind(0)
+    _, loss, lse = _outputs(T, dev, False)
+    _call("logits_distill", dev.index, code, logits.data_ptr(), T, V, ld, *teacher, temperature, loss.data_ptr(),
+          lse.data_ptr(), _stream(stream, dev))
     return loss, lse
 
 
