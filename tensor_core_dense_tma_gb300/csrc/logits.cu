@@ -45,7 +45,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 1024;        // kMaxCluster lists of LOGITS_MAX_TOP fit too
 constexpr int kSlack = 64;               // buckets more than wanted that are not worth telling ties apart
-constexpr int64_t kInFlight = 64 << 20;  // bytes of logits that a gradient's CTAs work on at once
+constexpr int64_t kInFlight = 64 << 20, kInFlightWhole = 80 << 20;   // bytes of logits that a gradient works on at once
 constexpr int64_t kSharedOfSm = 228 * 1024;
 constexpr int kDynamicMost = 225 * 1024;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -1107,20 +1107,27 @@ struct OnDevice {
 
 template <typename E, int OP, bool GRAD, bool TOP>
 gemm_status_t launch(Args a, int64_t T, int device, int sms, cudaStream_t stream) {
-    // The ring takes what shared memory kCtas CTAs an SM leave.  A gradient's
-    // rows in flight, which it reads twice, are to fit half of L2 (kInFlight).
-    // Rows are also split while that fills idle SMs and leaves every CTA a chunk.
+    // The ring takes what shared memory kCtas CTAs an SM leave.
     constexpr int kCtas = ctas_of(GRAD);
     const int64_t chunks = (a.V / Ele<E>::kPer + kChunk - 1) / kChunk;
     const int64_t beside = TOP ? static_cast<int64_t>(sizeof(TopState)) : OP == kDistill ? (a.K + 3) / 4 * 64 : 0;
     int64_t slots = (kSharedOfSm / kCtas - 2048 - beside) / (kChunk * 16);
     const int64_t ctas_at_once = static_cast<int64_t>(kCtas) * sms;
+    // CTAs of a row.  A gradient's rows in flight, which it reads twice, are to
+    // fit L2 beside what it writes (4096 x 131072 bf16: 1 CTA a row 426 us, 2 375,
+    // 3 478; 600 x 131072 fp32: 143, 131, 130 and 4 117; 300 x 131072 bf16, 79 MB
+    // in all: 36 and 42).
     int64_t cluster = 1;
     if (GRAD)
         while (cluster < kMaxCluster && chunks > slots &&
-               (T * cluster < ctas_at_once ? T : ctas_at_once / cluster) * a.V * static_cast<int64_t>(sizeof(E)) > kInFlight)
+               (T * cluster < ctas_at_once ? T : ctas_at_once / cluster) * a.V * static_cast<int64_t>(sizeof(E)) >
+                   (cluster == 1 ? kInFlightWhole : kInFlight))
             ++cluster;
-    while (cluster < kMaxCluster && T * (cluster + 1) <= ctas_at_once && chunks > cluster) ++cluster;
+    // Few rows are split over up to two CTAs an SM (64 x 131072 bf16 with
+    // gradient: 1 CTA a row 21 us, 2 15, 4 14, 8 19), in halves, as long as every
+    // CTA has a chunk, or four where it selects alternatives of its own first
+    // (1 x 131072 bf16: 1 CTA 16.4 us, 4 13.0, 8 13.6; 64 x 50001: 13.4, 14.0, 15.8).
+    while (cluster * 2 <= kMaxCluster && T * cluster * 2 <= 2 * sms && chunks >= cluster * 2 * (TOP ? 4 : 1)) cluster *= 2;
     const int64_t each = chunks > 0 ? (chunks + cluster - 1) / cluster : 1;
     // Two rows one after another save a start where a row is short and the
     // CTAs are many (8192 x 8192 bf16 with gradient: 83 us with one, 74 with
