@@ -329,6 +329,9 @@ gemm_status_t launch_tile(gemm_plan* plan, tcdt_i8::Params p, const __half* x, i
     p.idesc = make_idesc(true, 0, false, false, 128, BN);
     p.status = plan->d_status;
     p.timeout_ns = plan->timeout_ns;
+#ifdef TCDT_FAULT_INJECTION
+    p.fi_skip_load = plan->fi_skip_load;
+#endif
     const int64_t tiles_n = (p.N + 127) / 128, tiles_m = (p.M + BN - 1) / BN;
     const int64_t blocks = (p.K + Cfg::KS - 1) / Cfg::KS;
     // CTAs that share a tile's K.  Four while all run at once (2048 x 2048

@@ -36,6 +36,9 @@ struct Params {
     uint32_t idesc;
     int* status;
     uint64_t timeout_ns;
+#ifdef TCDT_FAULT_INJECTION
+    int64_t fi_skip_load;    // test builds only: this stage (counted per CTA) gets no tokens
+#endif
 };
 
 // Programmatic dependent launch: grid_wait returns once the kernel before in
@@ -305,6 +308,12 @@ tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
         int issued = 0;
         // the first weights are on their way before the tokens' codes are there
         const int ahead = min(Cfg::STAGES, kb1 - kb0);
+        auto load_tokens = [&](int kb, int to) {
+            const uint32_t sx = base + to * Cfg::STAGE_BYTES + Cfg::W_BYTES;
+#pragma unroll
+            for (int c = 0; c < KS / 64; ++c)
+                tcdt::tma_load_2d(sx + c * Cfg::X_CHUNK, &tmX, full_bar(to), kb * KS + 64 * c, m0);
+        };
         if (tcdt::elect_one_sync())
             for (int i = 0; i < ahead; ++i) {
                 tcdt::mbar_arrive_expect_tx(full_bar(i), Cfg::STAGE_BYTES);
@@ -317,25 +326,32 @@ tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                 ok = false;
                 break;
             }
-            const uint32_t sw = base + stage * Cfg::STAGE_BYTES, sx = sw + Cfg::W_BYTES;
             if (tcdt::elect_one_sync()) {
                 if (kb - kb0 >= ahead) {
                     tcdt::mbar_arrive_expect_tx(full_bar(stage), Cfg::STAGE_BYTES);
-                    tcdt::tma_load_2d(sw, &tmW, full_bar(stage), kb * KS, n0);
+                    tcdt::tma_load_2d(base + stage * Cfg::STAGE_BYTES, &tmW, full_bar(stage), kb * KS, n0);
                 }
-#pragma unroll
-                for (int c = 0; c < KS / 64; ++c)
-                    tcdt::tma_load_2d(sx + c * Cfg::X_CHUNK, &tmX, full_bar(stage), kb * KS + 64 * c, m0);
+#ifdef TCDT_FAULT_INJECTION
+                // the barrier expects bytes that never come: a wait downstream must run out
+                if (issued != p.fi_skip_load)
+#endif
+                    load_tokens(kb, stage);
             }
             __syncwarp();
             ++issued;
             if (++stage == Cfg::STAGES) stage = 0, phase ^= 1u;
         }
-        if (!ok) {      // let the copies already issued land
-            for (int i = 0; i < Cfg::STAGES && i < issued; ++i) {
-                if (--stage < 0) stage = Cfg::STAGES - 1, phase ^= 1u;
-                tcdt::wait_phase_drain(full_bar(stage), phase, 100000000ull);
-            }
+        // The copies started land before this CTA ends, whoever gave up.
+        // Stages whose weights alone were asked for get their tokens first,
+        // so that their barriers complete.
+        for (; issued < ahead; ++issued) {
+            if (tcdt::elect_one_sync()) load_tokens(kb0 + issued, stage);
+            __syncwarp();
+            if (++stage == Cfg::STAGES) stage = 0, phase ^= 1u;
+        }
+        for (int i = 0; i < Cfg::STAGES && i < issued; ++i) {
+            if (--stage < 0) stage = Cfg::STAGES - 1, phase ^= 1u;
+            tcdt::wait_phase_drain(full_bar(stage), phase, 100000000ull);
         }
     } else if (warp == Cfg::WORKERS + 1) {
         int stage = 0, slot = 0;
@@ -433,16 +449,18 @@ tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                 for (int i = 0; i < 16; ++i)
                     v[i] = __uint_as_float(acc[i]) * (__shfl_sync(~0u, rs, i) * cs) + bias;
                 tcdt::ep_act_w<16>(p.act, v);
-                if (n >= p.N) continue;
                 const int64_t at = static_cast<int64_t>(m0 + c) * p.ldd + n;
-                if (c + 16 <= cols) {
+                if (n < p.N) {
+                    if (c + 16 <= cols) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
-                } else {
+                        for (int i = 0; i < 16; ++i) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c + i < cols) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < cols) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
+                    }
                 }
+                __syncwarp();      // the next read of tensor memory is the whole warp's
             }
         } else if (p.splits > 1) {
             // partial sums [token][row]; the ring is free, every copy and MMA has finished
