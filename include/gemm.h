@@ -408,9 +408,9 @@ gemm_status_t gemm_schedule_model(int sm_count, gemm_dtype_t in_dtype, int64_t M
  * first call of a larger problem grows with cudaMalloc: a stream capture has
  * to follow a call of its size, and captured calls stay valid when a later
  * call grows it (until the plan is destroyed).  A call launches one to three
- * kernels.  Weights are read as they are, 8 bits each, by calls of up to about
- * 1500 tokens; beyond, a copy of 16 bits each is made in the workspace by
- * every call. */
+ * kernels.  Weights are read as they are, 8 bits each, unless a call of many
+ * tokens (beyond 256, mostly some 2000 and more) is faster with a copy of 16
+ * bits each that it makes in the workspace. */
 gemm_status_t gemm_run_i8(gemm_plan_t plan, const int8_t *A, const int8_t *B, void *D, int64_t M, int64_t N,
                           int64_t K, int64_t lda, int64_t ldb, int64_t ldd, gemm_dtype_t out_dtype,
                           const gemm_epilogue_t *ep, void *stream);

@@ -13,6 +13,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "gemm.h"
@@ -256,7 +258,7 @@ gemm_status_t check_product(gemm_plan* plan, const void* B, const void* D, int64
 }
 
 // Kernels of the product, by the number of tokens M.
-enum Path { kDot, kTile, kWide };
+enum Path { kDot, kTile, kPair, kWide };
 
 Path path_of(int64_t M, int64_t N, int64_t K, int sms) {
     // Whole-number sums: K products of up to 2^14 stay within 31 bits.
@@ -270,12 +272,26 @@ Path path_of(int64_t M, int64_t N, int64_t K, int sms) {
         if (M <= 4 && weights <= (1 << 24)) return kDot;
         if (M <= 8 && weights <= (1 << 22)) return kDot;
     }
-    // Widening the weights first pays once every one of them is used by more
-    // than about 1500 tokens and the tiles take more than two waves of two CTAs
-    // an SM (8192 x 8192 weights: 1024 tokens 106 us to 120, 1536 tokens 158 to
-    // 152; 2055 x 1000: 2048 tokens 18 us to 22, 4097 tokens with scales and
-    // bias in 17 x 33 tiles 34 to 39).
-    return M <= 1024 || (M + 127) / 128 * ((N + 127) / 128) <= 4LL * sms ? kTile : kWide;
+    // Few tokens or few tiles of 128 x 128: those, which then share K in clusters or
+    // have an SM of their own (1024 x 8192 weights, 1024 tokens: 25 us, pairs 45,
+    // widened first 74; 640 x 16000, 3500 tokens, 140 tiles: 91, 105, 109).
+    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
+    if (M <= 256 || tiles <= sms) return kTile;
+    // Otherwise the least of three estimates in us, fitted to 97 measured sizes from
+    // 8192 x 300 to 640 x 16000 weights and 512 to 10000 tokens with bf16 results;
+    // the choice cost 1.2 % over the best of the three on average, 15 % at most.
+    // 128 x 128 tiles run two an SM, whose starts and epilogues fill each other's
+    // gaps but whose MMAs do not overlap the last wave; 256 x 256 tiles on CTA pairs
+    // run one an SM; the fp16 kernel divides its last wave, after both operands were
+    // widened.  8192 x 8192 weights, 512 / 1024 / 1536 / 4097 tokens: 56 / 109 / 165 /
+    // - us, 46 / 92 / 138 / 363 and 91 / 123 / 158 / 344; 4096 x 512, 4097 tokens: 31,
+    // 38, 35; 1024 x 8192, 4097 tokens: 72, 62, 72.
+    const double k = K / 1000.0, pairs = (M + 255) / 256 * ((N + 255) / 256), wave = sms / 2;
+    const double round_tiles = std::ceil(tiles / (2.0 * sms));
+    const double tile = 3.4 + 4.6 * std::max(1.0, tiles / (2.0 * sms)) + 6.3 * k * round_tiles;
+    const double pair = 2.5 + std::ceil(pairs / wave) * (6.2 + 5.3 * k);
+    const double wide = 12.5 + 0.75e-3 * (static_cast<double>(N) + M) * k + pairs / wave * (3.9 + 3.45 * k);
+    return tile <= std::min(pair, wide) ? kTile : pair <= wide ? kPair : kWide;
 }
 
 // The kernel may start before the one that makes the tokens' codes has
@@ -380,6 +396,48 @@ gemm_status_t launch_tile_out(gemm_plan* plan, const tcdt_i8::Params& p, const _
     return launch_tile<BN, tcdt::kOutBF16>(plan, p, x, ldx, s);
 }
 
+template <int OUT>
+gemm_status_t launch_pair(gemm_plan* plan, tcdt_i8::Params p, const __half* x, int64_t ldx, cudaStream_t s) {
+    using Cfg = tcdt_i8::PairConfig;
+    CUtensorMap tmW, tmX;
+    gemm_status_t st = encode_map(plan, &tmW, p.B, static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.N),
+                                  static_cast<uint64_t>(p.ldb), Cfg::KS, 128, GEMM_E4M3, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (st == GEMM_OK)
+        st = encode_map(plan, &tmX, x, static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.M),
+                        static_cast<uint64_t>(ldx), 64, Cfg::BN / 2, GEMM_F16);
+    if (st != GEMM_OK) return st;
+    p.idesc = make_idesc(true, 0, false, false, 256, Cfg::BN);
+    p.status = plan->d_status;
+    p.timeout_ns = plan->timeout_ns;
+#ifdef TCDT_FAULT_INJECTION
+    p.fi_skip_load = plan->fi_skip_load;
+#endif
+    auto kernel = tcdt_i8::pair_kernel<OUT>;
+    bool& prepared = plan->i8_prepared[4][OUT];
+    if (!prepared && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    prepared = true;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.N + 255) / 256 * 2), static_cast<unsigned>((p.M + Cfg::BN - 1) / Cfg::BN), 1);
+    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    cfg.numAttrs = 1 + dependent(attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, p) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    ++plan->launches;
+    return GEMM_OK;
+}
+
 // The product once arguments are checked: A's codes as given, or made from X
 // in the plan's buffer, where the tokens (and on the wide path the weights)
 // also become fp16.
@@ -426,6 +484,11 @@ gemm_status_t run_product(gemm_plan* plan, const int8_t* A, const void* X, gemm_
         if (M == 2) return launch_dot<2, 2>(plan, p, X != nullptr, out, s);
         if (M <= 4) return launch_dot<4, 4>(plan, p, X != nullptr, out, s);
         return launch_dot<8, 4>(plan, p, X != nullptr, out, s);
+    }
+    if (path == kPair) {
+        if (out == GEMM_F32) return launch_pair<tcdt::kOutF32>(plan, p, a, ldh, s);
+        if (out == GEMM_F16) return launch_pair<tcdt::kOutF16>(plan, p, a, ldh, s);
+        return launch_pair<tcdt::kOutBF16>(plan, p, a, ldh, s);
     }
     if (M <= 16) return launch_tile_out<16>(plan, p, a, ldh, out, s);
     if (M <= 32) return launch_tile_out<32>(plan, p, a, ldh, out, s);

@@ -243,6 +243,40 @@ __device__ __forceinline__ void finish_store4(const Params& p, const float4& sum
         if (n + i < p.N) tcdt::store_elem<OUT>(p.D, at + i, v[i]);
 }
 
+// Tokens first, first + step, ... below `cols` of an accumulator, finished and
+// stored, a channel a lane: 16 tokens at a time, of which lane i brings token
+// i's scale; the activation is chosen once, a warp stores 32 channels of a
+// token.  All lanes of the warp take part.
+template <int OUT>
+__device__ __forceinline__ void store_tokens(const Params& p, uint32_t taddr, int cols, int first, int step, int m0,
+                                             int64_t n, float cs, float bias) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll 1
+    for (int c = first; c < cols; c += step) {
+        uint32_t acc[16];
+        tcdt::tmem_ld_32x32b_x16(taddr + c, acc);
+        const int mine = m0 + c + lane % 16;
+        const float rs = p.rs && mine < p.M ? p.rs[mine] : 1.f;
+        tcdt::tmem_ld_wait();
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(acc[i]) * (__shfl_sync(~0u, rs, i) * cs) + bias;
+        tcdt::ep_act_w<16>(p.act, v);
+        const int64_t at = static_cast<int64_t>(m0 + c) * p.ldd + n;
+        if (n < p.N) {
+            if (c + 16 <= cols) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < cols) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
+            }
+        }
+        __syncwarp();      // the next read of tensor memory is the whole warp's
+    }
+}
+
 // A cluster of p.splits CTAs computes one tile, each a range of the K blocks;
 // their partial sums meet in shared memory, and each CTA finishes its share
 // of the tokens, adding the partials in the order of their ranges.
@@ -434,34 +468,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
         const int64_t n = n0 + r;
         const float cs = p.cs && n < p.N ? p.cs[n] : 1.f, bias = p.bias && n < p.N ? p.bias[n] : tcdt::kNoBias;
         if (ok && p.splits == 1) {
-            // 16 tokens at a time: lane i brings token i's scale, the
-            // activation is chosen once, a warp stores 32 channels of a token
-            const int cols = min(BN, p.M - m0);
-#pragma unroll 1
-            for (int c = 16 * group; c < cols; c += 16 * Cfg::GROUPS) {
-                uint32_t acc[16];
-                tcdt::tmem_ld_32x32b_x16(tmem + lanes + c, acc);
-                const int mine = m0 + c + lane % 16;
-                const float rs = p.rs && mine < p.M ? p.rs[mine] : 1.f;
-                tcdt::tmem_ld_wait();
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[i] = __uint_as_float(acc[i]) * (__shfl_sync(~0u, rs, i) * cs) + bias;
-                tcdt::ep_act_w<16>(p.act, v);
-                const int64_t at = static_cast<int64_t>(m0 + c) * p.ldd + n;
-                if (n < p.N) {
-                    if (c + 16 <= cols) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < cols) tcdt::store_elem<OUT>(p.D, at + i * p.ldd, v[i]);
-                    }
-                }
-                __syncwarp();      // the next read of tensor memory is the whole warp's
-            }
+            store_tokens<OUT>(p, tmem + lanes, min(BN, p.M - m0), 16 * group, 16 * Cfg::GROUPS, m0, n, cs, bias);
         } else if (p.splits > 1) {
             // partial sums [token][row]; the ring is free, every copy and MMA has finished
             const int cols = min(BN, p.M - m0);
@@ -514,6 +521,219 @@ tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
     if (warp == Cfg::WORKERS + 1) {
         tcdt::tc_fence_after_sync();
         tcdt::tmem_dealloc<1>(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// pair_kernel: 256 channels x 256 tokens on a CTA pair
+// ---------------------------------------------------------------------------
+// What bounds the tile kernel with many tokens is what an SM can take in from
+// L2, about 51 bytes a cycle: 128 channels (8 bits) and 128 tokens (fp16) of 64
+// codes are 24 KB for MMAs of 256 cycles.  With cta_group::2 the two CTAs of a
+// pair hold half of the tokens each, so that the same 24 KB feed 512 cycles.
+// Each CTA widens its own 128 channels into its own tensor memory; the first
+// one's MMAs read both.  A stage's shared memory and its columns of tensor
+// memory are freed together, by the commit of its MMAs.  8192 x 8192 weights, 512
+// tokens: 46 us (640 cycles a stage) to 56 with tiles of 128 x 128 on one CTA.
+struct PairConfig {
+    static constexpr int BN = 256, KS = 64;
+    static constexpr int W_BYTES = 128 * KS, X_BYTES = (BN / 2) * 128;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+    static constexpr int STAGES = 8;
+    static constexpr int SLOT_COLS = KS / 2;
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 512;
+    static constexpr int GROUPS = 2, WORKERS = 8, THREADS = 32 * (WORKERS + 2);
+    static_assert(BN + STAGES * SLOT_COLS <= TMEM_COLS, "TMEM");
+};
+
+// Arrival on a barrier of either CTA of the pair.  What it announces is in
+// tensor memory, ordered by tcgen05.fence on both sides; no other memory has to
+// be released at cluster scope (which takes several hundred cycles a stage).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(PairConfig::THREADS, 1)
+pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
+    using Cfg = PairConfig;
+    constexpr int KS = Cfg::KS;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = tcdt::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t bar_base = base + Cfg::STAGES * Cfg::STAGE_BYTES;
+    auto w_bar = [&](int s) { return bar_base + 8u * s; };                          // weights landed (each CTA's own)
+    auto x_bar = [&](int s) { return bar_base + 8u * (Cfg::STAGES + s); };          // both halves of the tokens (first CTA)
+    auto slot_bar = [&](int s) { return bar_base + 8u * (2 * Cfg::STAGES + s); };   // both CTAs' channels widened (first CTA)
+    auto empty_bar = [&](int s) { return bar_base + 8u * (3 * Cfg::STAGES + s); };  // MMAs done (both)
+    const uint32_t acc_bar = bar_base + 8u * 4 * Cfg::STAGES;
+    const uint32_t drain_bar = acc_bar + 8u;
+    static_assert(8 * (4 * Cfg::STAGES + 2) + 8 <= 512, "barriers");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = static_cast<int>(tcdt::cluster_ctarank());
+    const bool leader = rank == 0;
+    const int n0 = static_cast<int>(blockIdx.x) * 128;       // the pair's channels lie side by side
+    const int m0 = static_cast<int>(blockIdx.y) * Cfg::BN;
+    const int blocks = (p.K + KS - 1) / KS;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+            tcdt::mbar_init(w_bar(s), 1);
+            tcdt::mbar_init(x_bar(s), 1);
+            tcdt::mbar_init(slot_bar(s), 8);                 // four warps of each CTA
+            tcdt::mbar_init(empty_bar(s), 1);
+        }
+        tcdt::mbar_init(acc_bar, 1);
+        tcdt::mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        tcdt::fence_mbar_init();
+    }
+    if (warp == Cfg::WORKERS && lane == 0) {
+        tcdt::tma_prefetch_desc(&tmW);
+        tcdt::tma_prefetch_desc(&tmX);
+    }
+    if (warp == Cfg::WORKERS + 1) {
+        tcdt::tmem_alloc<2>(tcdt::smem_addr(tmem_slot), Cfg::TMEM_COLS);
+        tcdt::tmem_relinquish_alloc_permit<2>();
+    }
+    tcdt::tc_fence_before_sync();
+    tcdt::cluster_sync_all();               // the peer's barriers are there before anything arrives on them
+    tcdt::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wctx{p.status, p.timeout_ns, abort_flag};
+    bool ok = true;
+
+    if (warp == Cfg::WORKERS) {
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        const int ahead = min(Cfg::STAGES, blocks);
+        auto load_weights = [&](int kb, int to) {
+            tcdt::mbar_arrive_expect_tx(w_bar(to), Cfg::W_BYTES);
+            tcdt::tma_load_2d(base + to * Cfg::STAGE_BYTES, &tmW, w_bar(to), kb * KS, n0);
+        };
+        if (tcdt::elect_one_sync())
+            for (int i = 0; i < ahead; ++i) load_weights(i, i);
+        __syncwarp();
+        grid_wait();
+        for (int kb = 0; kb < blocks; ++kb) {
+            if (!tcdt::warp_wait_phase(empty_bar(stage), phase ^ 1u, wctx, kSiteProducer)) break;
+            if (tcdt::elect_one_sync()) {
+                if (kb >= ahead) load_weights(kb, stage);
+                if (leader) tcdt::mbar_arrive_expect_tx(x_bar(stage), 2 * Cfg::X_BYTES);
+#ifdef TCDT_FAULT_INJECTION
+                if (issued != p.fi_skip_load)
+#endif
+                    tcdt::tma_load_2d_pair(base + stage * Cfg::STAGE_BYTES + Cfg::W_BYTES, &tmX,
+                                           tcdt::map_to_cta(x_bar(stage), 0), kb * KS, m0 + rank * (Cfg::BN / 2));
+            }
+            __syncwarp();
+            ++issued;
+            if (++stage == Cfg::STAGES) stage = 0, phase ^= 1u;
+        }
+        // the copies started land before the pair ends, whoever gave up
+        int s = stage;
+        uint32_t ph = phase;
+        for (int i = 0; leader && i < Cfg::STAGES && i < issued; ++i) {
+            if (--s < 0) s = Cfg::STAGES - 1, ph ^= 1u;
+            tcdt::wait_phase_drain(x_bar(s), ph, 100000000ull);
+        }
+        for (; issued < ahead; ++issued)
+            if (++stage == Cfg::STAGES) stage = 0, phase ^= 1u;
+        for (int i = 0; i < Cfg::STAGES && i < issued; ++i) {
+            if (--stage < 0) stage = Cfg::STAGES - 1, phase ^= 1u;
+            tcdt::wait_phase_drain(w_bar(stage), phase, 100000000ull);
+        }
+    } else if (warp == Cfg::WORKERS + 1) {
+        if (leader) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = 0; kb < blocks; ++kb) {
+                if (!tcdt::warp_wait_phase(x_bar(stage), phase, wctx, kSiteMmaTokens) ||
+                    !tcdt::warp_wait_phase(slot_bar(stage), phase, wctx, kSiteMmaSlot)) {
+                    ok = false;
+                    break;
+                }
+                tcdt::tc_fence_after_sync();
+                const uint32_t sx = base + stage * Cfg::STAGE_BYTES + Cfg::W_BYTES;
+                const uint32_t a = tmem + Cfg::BN + stage * Cfg::SLOT_COLS;
+                if (tcdt::elect_one_sync()) {
+#pragma unroll
+                    for (int k = 0; k < KS / 16; ++k)
+                        umma_f16_ts_pair(tmem, a + 8 * k, tcdt::smem_desc_sw128(sx + k * 32, 16u, 1024u), p.idesc,
+                                         (kb != 0 || k != 0) ? 1u : 0u);
+                    tcdt::umma_commit<2>(empty_bar(stage), 3);
+                    if (kb + 1 == blocks) tcdt::umma_commit<2>(acc_bar, 3);
+                }
+                __syncwarp();
+                if (++stage == Cfg::STAGES) stage = 0, phase ^= 1u;
+            }
+            if (!ok) {
+                if (tcdt::elect_one_sync()) tcdt::umma_commit<2>(drain_bar, 1);
+                __syncwarp();
+                tcdt::wait_phase_drain(drain_bar, 0, 100000000ull);
+            }
+        }
+    } else {
+        const int r = threadIdx.x % 128, group = warp / 4;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;
+        int stage = group;
+        uint32_t phase = 0;
+        for (int kb = group; kb < blocks; kb += Cfg::GROUPS) {
+            // (the weights come into a stage whose MMAs are done, so its columns are free too)
+            if (!tcdt::warp_wait_phase(w_bar(stage), phase, wctx, kSiteConvertFull)) {
+                ok = false;
+                break;
+            }
+            const uint32_t sw = base + stage * Cfg::STAGE_BYTES + r * 64u;
+            uint4 q[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) q[c] = ld_shared_v4u(sw + ((c ^ ((r >> 1) & 3)) << 4));
+            tcdt::tc_fence_after_sync();
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                widen4(q[c].x, w[8 * c + 0], w[8 * c + 1]);
+                widen4(q[c].y, w[8 * c + 2], w[8 * c + 3]);
+                widen4(q[c].z, w[8 * c + 4], w[8 * c + 5]);
+                widen4(q[c].w, w[8 * c + 6], w[8 * c + 7]);
+            }
+            tcdt::tmem_st_32x32b_x32(tmem + lanes + Cfg::BN + stage * Cfg::SLOT_COLS, w);
+            tcdt::tmem_st_wait();
+            tcdt::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(tcdt::map_to_cta(slot_bar(stage), 0));
+            if ((stage += Cfg::GROUPS) >= Cfg::STAGES) stage -= Cfg::STAGES, phase ^= 1u;
+        }
+        if (ok) {
+            ok = tcdt::warp_wait_phase(acc_bar, 0, wctx, kSiteAccumulator);
+            tcdt::tc_fence_after_sync();
+        }
+        grid_wait();     // for the row scales
+        const int64_t n = n0 + r;
+        const float cs = p.cs && n < p.N ? p.cs[n] : 1.f, bias = p.bias && n < p.N ? p.bias[n] : tcdt::kNoBias;
+        const int cols = min(Cfg::BN, p.M - m0);
+        if (ok) store_tokens<OUT>(p, tmem + lanes, cols, 16 * group, 16 * Cfg::GROUPS, m0, n, cs, bias);
+    }
+    tcdt::tc_fence_before_sync();
+    __syncwarp();
+    tcdt::cluster_sync_all();               // the MMAs into the peer's tensor memory are finished
+    if (warp == Cfg::WORKERS + 1) {
+        tcdt::tc_fence_after_sync();
+        tcdt::tmem_dealloc<2>(tmem, Cfg::TMEM_COLS);
     }
 }
 

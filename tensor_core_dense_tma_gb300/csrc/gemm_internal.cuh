@@ -135,7 +135,7 @@ struct gemm_plan {
     void* d_i8[tcdt_host::kI8Buffers] = {};   // gemm_run_i8's codes and row scales: the last one is in use (owned)
     int i8_buffers = 0;
     size_t i8_bytes = 0;          // capacity of the last of them
-    bool i8_prepared[4][3] = {};  // its kernels' shared-memory opt-in done ([tile][output])
+    bool i8_prepared[5][3] = {};  // its kernels' shared-memory opt-in done ([tile][output])
     int forced_kind = -1;         // gemm_plan_force_config
 #ifdef TCDT_FAULT_INJECTION
     int64_t fi_skip_load = -1;    // test builds only

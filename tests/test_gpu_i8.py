@@ -263,6 +263,29 @@ def test_refusals(tc, plan):
         tc.quantize_rows_i8(A.float(), scale=f)
 
 
+# CTA pairs: one wave and two, the second CTA's channels cut off or absent; few codes and many tokens
+@pytest.mark.parametrize("M,N,K", [(1500, 2049, 2100), (1025, 3300, 70), (2100, 300, 130), (3000, 129, 64),
+                                   (777, 4230, 2500), (5000, 1000, 1), (1025, 3300, 1000), (1300, 5633, 2100),
+                                   (4100, 1000, 900), (9000, 300, 1101)], ids=lambda v: str(v))
+@pytest.mark.parametrize("out", list(TYPES))
+def test_many_tokens(plan, M, N, K, out):
+    g = np.random.default_rng(K)
+    A, a = codes(M, K, 1, top=60)
+    W, w = codes(N, K, 2, top=60)
+    rs = (g.random(M) * 0.1 / np.sqrt(K)).astype(np.float32)
+    bias = g.normal(size=N).astype(np.float32)
+    D = torch.full((M, N + 3), float("nan"), dtype=TYPES[out], device="cuda")
+    plan.gemm_i8(A, W.t(), D[:, 1:N + 1], row_scale=torch.from_numpy(rs).cuda(), bias=torch.from_numpy(bias).cuda(),
+                 act="relu")
+    s = (a.astype(np.float64) @ w.T.astype(np.float64)) * rs.astype(np.float64)[:, None]
+    u = s + bias.astype(np.float64)
+    got = D.double().cpu().numpy()
+    assert np.isnan(got[:, 0]).all() and np.isnan(got[:, N + 1:]).all()
+    want = np.maximum(u, 0)
+    tol = 2.0 ** -22 * (np.abs(s) + np.abs(u)) + HALF_ULP[out] * want + (2.0 ** -25 if out == "f16" else 0.0)
+    assert np.all(np.abs(got[:, 1:N + 1] - want) <= tol * (1 + 1e-6))
+
+
 def test_graph_outlives_a_grown_workspace(tc):
     """A graph captured before a larger call made the plan's workspace grow."""
     with tc.Plan("f16", 0) as plan:

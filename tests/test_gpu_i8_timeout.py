@@ -31,9 +31,9 @@ def fi_lib():
     return lib
 
 
-# one range of K a tile; ranges shared by a cluster; wide tiles; a stage within the first ones and a later one
+# one range of K a tile; ranges shared by a cluster; wide tiles; CTA pairs; a stage within the first ones and a later one
 @pytest.mark.parametrize("M,N,K,stage", [(16, 20000, 2048, 1), (16, 512, 4096, 0), (60, 512, 4096, 3),
-                                         (1000, 2048, 1024, 7)], ids=lambda v: str(v))
+                                         (1000, 2048, 1024, 7), (1024, 4096, 4096, 9)], ids=lambda v: str(v))
 def test_stalled_tokens_report_timeout_and_recover(fi_lib, M, N, K, stage):
     lib = fi_lib
     h = ctypes.c_void_p()
