@@ -428,7 +428,8 @@ gemm_status_t gemm_run_i8_dynamic(gemm_plan_t plan, const void *X, gemm_dtype_t 
  *     scale[i] = max_k |X[i,k]| / 127,   Q[i,k] = round(X[i,k] / scale[i])
  * in fp32 (IEEE divisions, rounding half to even), codes -127..127.  A row of
  * zeros has scale 0 and codes 0; a row with an infinity or a NaN has that as
- * its scale.  Used on tokens, and on the rows of a weight matrix for the
+ * its scale and codes 0, so that what is scaled back, and every product of the
+ * row, is NaN.  Used on tokens, and on the rows of a weight matrix for the
  * scales of its channels.  Q is row-major, ldq >= K; K == 0 writes scales of
  * 0.  One kernel on `stream` of `device`; no plan and no allocation. */
 gemm_status_t gemm_quantize_rows_i8(int device, const void *X, gemm_dtype_t x_dtype, int64_t R, int64_t K,

@@ -70,10 +70,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
-// Both divisions are IEEE, so that the codes are those of the definition.
+// Both divisions are IEEE, so that the codes are those of the definition.  A
+// quotient that is no number (a row with an infinity or a NaN) has code 0: the
+// row's other codes are 0 as well, and 0 times its scale makes results NaN.
 __device__ __forceinline__ int code_of(float x, float scale) {
     const float c = scale != 0.f ? __fdiv_rn(x, scale) : 0.f;
-    return __float2int_rn(fminf(fmaxf(c, -127.f), 127.f));
+    return c == c ? __float2int_rn(fminf(fmaxf(c, -127.f), 127.f)) : 0;
 }
 
 __device__ __forceinline__ void store_code(int8_t* p, int q) { *p = static_cast<int8_t>(q); }
