@@ -394,7 +394,8 @@ gemm_status_t gemm_schedule_model(int sm_count, gemm_dtype_t in_dtype, int64_t M
  * with one row of K codes per output channel), both int8 with lda, ldb >= K
  * counted in elements; D is row-major, ldd >= N, GEMM_F32, GEMM_F16 or
  * GEMM_BF16.  rs, cs, bias and act are the fields row_scale, col_scale, bias
- * and act of `ep` (NULL: 1, 1, 0 and none).  A and B start on 16-byte
+ * and act of `ep` (NULL: 1, 1, 0 and none); a NaN stays one through every
+ * activation, GEMM_ACT_RELU too.  A and B start on 16-byte
  * boundaries and lda and ldb are multiples of 16 (K may be anything); D needs
  * element alignment.
  *

@@ -356,7 +356,7 @@ gemm_status_t prepare_all(gemm_plan* plan) {
 
 gemm_status_t launch_scale(gemm_plan* plan, const void* C, void* D, int64_t M, int64_t N, int64_t ldc,
                            gemm_dtype_t out, float alpha, float beta, cudaStream_t stream,
-                           const gemm_epilogue_t* ep = nullptr) {
+                           const gemm_epilogue_t* ep = nullptr, bool keep_nan = false) {
     const int64_t total = M * N;
     int64_t blocks = (total + 255) / 256;
     if (blocks > 4LL * plan->sm_count) blocks = 4LL * plan->sm_count;
@@ -366,12 +366,14 @@ gemm_status_t launch_scale(gemm_plan* plan, const void* C, void* D, int64_t M, i
     const float* bias = ep ? ep->bias : nullptr;
     const uint32_t act = ep ? static_cast<uint32_t>(ep->act) : 0u;
     if (out == GEMM_F32)
-        tcdt::scale_c_kernel<tcdt::kOutF32><<<blocks, 256, 0, stream>>>(m, n, C, D, ldc, alpha, beta, rs, cs, bias, act);
+        tcdt::scale_c_kernel<tcdt::kOutF32><<<blocks, 256, 0, stream>>>(m, n, C, D, ldc, alpha, beta, rs, cs, bias, act,
+                                                                        keep_nan);
     else if (out == GEMM_F16)
-        tcdt::scale_c_kernel<tcdt::kOutF16><<<blocks, 256, 0, stream>>>(m, n, C, D, ldc, alpha, beta, rs, cs, bias, act);
+        tcdt::scale_c_kernel<tcdt::kOutF16><<<blocks, 256, 0, stream>>>(m, n, C, D, ldc, alpha, beta, rs, cs, bias, act,
+                                                                        keep_nan);
     else
         tcdt::scale_c_kernel<tcdt::kOutBF16><<<blocks, 256, 0, stream>>>(m, n, C, D, ldc, alpha, beta, rs, cs, bias,
-                                                                         act);
+                                                                         act, keep_nan);
     if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_CUDA;
     ++plan->launches;
     return GEMM_OK;
@@ -473,6 +475,37 @@ gemm_status_t run_choice(gemm_plan* plan, const Choice& ch, const void* A, const
 }
 
 }  // namespace
+
+namespace tcdt_host {
+
+gemm_status_t run_keep_nan(gemm_plan* plan, const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
+                           int64_t lda, int64_t ldb, int64_t ldd, gemm_dtype_t out, const gemm_epilogue_t* ep,
+                           cudaStream_t s) {
+    if (K == 0) return launch_scale(plan, nullptr, D, M, N, ldd, out, 1.0f, 0.0f, s, ep, true);
+    bool valid = true;
+    Choice ch = select_choice(plan, M, N, K, GEMM_ROW_MAJOR, GEMM_COL_MAJOR, GEMM_F32, out, &valid, nullptr);
+    if (!valid) return GEMM_ERR_UNSUPPORTED;
+    if (ep->act != GEMM_ACT_RELU) {
+        const bool plain = !ep->bias && !ep->row_scale && !ep->col_scale && ep->act == GEMM_ACT_NONE;
+        return run_choice(plan, ch, A, B, nullptr, D, M, N, K, lda, ldb, ldd, GEMM_ROW_MAJOR, GEMM_COL_MAJOR, GEMM_F32,
+                          out, 1.0f, 0.0f, plain ? nullptr : ep, s);
+    }
+    if (ch.kind != kCfgPair256) {
+        // ReLU that keeps a NaN is built for this configuration, the choice of nine
+        // in ten of the sizes that come here
+        const int kind = plan->forced_kind, splits = plan->forced_splits;
+        plan->forced_kind = kCfgPair256;
+        plan->forced_splits = 0;
+        ch = choose(plan, M, N, K, GEMM_F32, false, &valid);
+        plan->forced_kind = kind;
+        plan->forced_splits = splits;
+        if (!valid) return GEMM_ERR_UNSUPPORTED;
+    }
+    const Problem pr = make_problem(ch.swap, A, B, M, N, K, lda, ldb, GEMM_ROW_MAJOR, GEMM_COL_MAJOR, ep);
+    return launch_pair256_ep_nan(plan, out_slot(GEMM_F32, out), ch, pr, D, ldd, s);
+}
+
+}  // namespace tcdt_host
 
 extern "C" {
 

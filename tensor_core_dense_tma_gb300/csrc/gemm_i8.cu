@@ -252,6 +252,7 @@ gemm_status_t check_product(gemm_plan* plan, const void* B, const void* D, int64
     if (M == 0 || N == 0) return GEMM_OK;
     if (!D || ldd < N) return GEMM_ERR_INVALID_ARG;
     if (ldd > (int64_t(1) << 40) || ldb > (int64_t(1) << 40)) return GEMM_ERR_UNSUPPORTED;
+    if (((M + 15) / 16) * ((N + 15) / 16) > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;    // gemm_run's limit
     if (!aligned(D, out == GEMM_F32 ? 4 : 2)) return GEMM_ERR_MISALIGNED;
     if (K == 0) return GEMM_OK;
     if (!B || ldb < K) return GEMM_ERR_INVALID_ARG;
@@ -448,6 +449,7 @@ gemm_status_t run_product(gemm_plan* plan, const int8_t* A, const void* X, gemm_
                           const gemm_epilogue_t* ep_in, cudaStream_t s) {
     gemm_epilogue_t ep{};
     if (ep_in) ep = *ep_in;
+    if (K == 0) return run_keep_nan(plan, nullptr, nullptr, D, M, N, 0, 8, 8, ldd, out, &ep, s);
     const Path path = path_of(M, N, K, plan->sm_count);
     const int64_t ldh = round_up(K, path == kDot ? 16 : 8);
     const size_t a_bytes = static_cast<size_t>(round_up(M * ldh * (path == kDot ? 1 : 2), 256));
@@ -470,8 +472,7 @@ gemm_status_t run_product(gemm_plan* plan, const int8_t* A, const void* X, gemm_
     if (path == kWide) {
         st = launch_widen(plan, B, ldb, b, ldh, N, K, s);
         if (st != GEMM_OK) return st;
-        return gemm_run_ep(plan, a, b, nullptr, D, M, N, K, ldh, ldh, ldd, GEMM_ROW_MAJOR, GEMM_COL_MAJOR, GEMM_F32,
-                           out, 1.0f, 0.0f, &ep, s);
+        return run_keep_nan(plan, a, b, D, M, N, K, ldh, ldh, ldd, out, &ep, s);
     }
     tcdt_i8::Params p{};
     p.M = static_cast<int32_t>(M), p.N = static_cast<int32_t>(N), p.K = static_cast<int32_t>(K);
@@ -510,12 +511,11 @@ gemm_status_t gemm_run_i8(gemm_plan_t plan, const int8_t* A, const int8_t* B, vo
                           const gemm_epilogue_t* ep, void* stream) {
     const gemm_status_t st = check_product(plan, B, D, M, N, K, ldb, ldd, out_dtype, ep);
     if (st != GEMM_OK || M == 0 || N == 0) return st;
-    if (K == 0)
-        return gemm_run_ep(plan, nullptr, nullptr, nullptr, D, M, N, 0, 8, 8, ldd, GEMM_ROW_MAJOR, GEMM_COL_MAJOR,
-                           GEMM_F32, out_dtype, 1.0f, 0.0f, ep, stream);
-    if (!A || lda < K) return GEMM_ERR_INVALID_ARG;
-    if (lda > (int64_t(1) << 40)) return GEMM_ERR_UNSUPPORTED;
-    if (!aligned(A, 16) || lda % 16) return GEMM_ERR_MISALIGNED;
+    if (K > 0) {
+        if (!A || lda < K) return GEMM_ERR_INVALID_ARG;
+        if (lda > (int64_t(1) << 40)) return GEMM_ERR_UNSUPPORTED;
+        if (!aligned(A, 16) || lda % 16) return GEMM_ERR_MISALIGNED;
+    }
     const OnDevice on(plan->device);
     if (!on.ok) return GEMM_ERR_CUDA;
     return run_product(plan, A, nullptr, GEMM_F32, B, D, M, N, K, lda, ldb, ldd, out_dtype, ep,
@@ -528,12 +528,11 @@ gemm_status_t gemm_run_i8_dynamic(gemm_plan_t plan, const void* X, gemm_dtype_t 
     if (!float_type(x_dtype) || (ep && ep->row_scale)) return GEMM_ERR_INVALID_ARG;
     const gemm_status_t st = check_product(plan, B, D, M, N, K, ldb, ldd, out_dtype, ep);
     if (st != GEMM_OK || M == 0 || N == 0) return st;
-    if (K == 0)
-        return gemm_run_ep(plan, nullptr, nullptr, nullptr, D, M, N, 0, 8, 8, ldd, GEMM_ROW_MAJOR, GEMM_COL_MAJOR,
-                           GEMM_F32, out_dtype, 1.0f, 0.0f, ep, stream);
-    if (!X || ldx < K) return GEMM_ERR_INVALID_ARG;
-    if (ldx > (int64_t(1) << 40)) return GEMM_ERR_UNSUPPORTED;
-    if (!aligned(X, x_dtype == GEMM_F32 ? 4 : 2)) return GEMM_ERR_MISALIGNED;
+    if (K > 0) {
+        if (!X || ldx < K) return GEMM_ERR_INVALID_ARG;
+        if (ldx > (int64_t(1) << 40)) return GEMM_ERR_UNSUPPORTED;
+        if (!aligned(X, x_dtype == GEMM_F32 ? 4 : 2)) return GEMM_ERR_MISALIGNED;
+    }
     const OnDevice on(plan->device);
     if (!on.ok) return GEMM_ERR_CUDA;
     return run_product(plan, nullptr, X, x_dtype, B, D, M, N, K, ldx, ldb, ldd, out_dtype, ep,

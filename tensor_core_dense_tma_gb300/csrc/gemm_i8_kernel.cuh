@@ -51,7 +51,7 @@ template <int OUT>
 __device__ __forceinline__ void finish_store(const Params& p, float sum, float rs, float cs, float bias, int64_t m,
                                              int64_t n) {
     float v[1] = {sum * (rs * cs) + bias};
-    tcdt::ep_act_w<1>(p.act, v);
+    tcdt::ep_act_w<1, tcdt::kEpKeepNan>(p.act, v);
     tcdt::store_elem<OUT>(p.D, m * p.ldd + n, v[0]);
 }
 
@@ -229,7 +229,7 @@ __device__ __forceinline__ void finish_store4(const Params& p, const float4& sum
                                               const float (&bias)[4], int64_t m, int64_t n) {
     float v[4] = {sum.x * (rs * cs[0]) + bias[0], sum.y * (rs * cs[1]) + bias[1], sum.z * (rs * cs[2]) + bias[2],
                   sum.w * (rs * cs[3]) + bias[3]};
-    tcdt::ep_act_w<4>(p.act, v);
+    tcdt::ep_act_w<4, tcdt::kEpKeepNan>(p.act, v);
     const int64_t at = m * p.ldd + n;
     constexpr int kBytes = OUT == tcdt::kOutF32 ? 16 : 8;
     char* to = static_cast<char*>(p.D) + at * (kBytes / 4);
@@ -261,7 +261,7 @@ __device__ __forceinline__ void store_tokens(const Params& p, uint32_t taddr, in
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(acc[i]) * (__shfl_sync(~0u, rs, i) * cs) + bias;
-        tcdt::ep_act_w<16>(p.act, v);
+        tcdt::ep_act_w<16, tcdt::kEpKeepNan>(p.act, v);
         const int64_t at = static_cast<int64_t>(m0 + c) * p.ldd + n;
         if (n < p.N) {
             if (c + 16 <= cols) {

@@ -129,7 +129,7 @@ struct gemm_plan {
     uint64_t timeout_ns = 2000000000ull;
     uint64_t launches = 0;
     tcdt_host::EncodeTiledFn encode = nullptr;
-    bool attr_set[tcdt_host::kNumCfgKinds][8] = {};   // [kind][output slot + 4 * fused epilogue]
+    bool attr_set[tcdt_host::kNumCfgKinds][12] = {};  // [kind][output slot + 4 * epilogue form]
     int units[tcdt_host::kNumCfgKinds] = {};  // co-resident CTAs (single) or CTA pairs (pair)
     size_t ws_bytes = 0;          // capacity of d_ws
     void* d_i8[tcdt_host::kI8Buffers] = {};   // gemm_run_i8's codes and row scales: the last one is in use (owned)
@@ -211,6 +211,15 @@ TCDT_DECLARE_KIND_IN(single64, tf32)
 TCDT_DECLARE_KIND_IN(single256, tf32)
 TCDT_DECLARE_KIND_IN(pair256, tf32)
 #undef TCDT_DECLARE_KIND_IN
+// pair256 whose ReLU keeps a NaN (the 8-bit product's)
+gemm_status_t launch_pair256_ep_nan(gemm_plan* plan, int slot, const Choice& ch, const Problem& pr, void* D,
+                                    int64_t ldd, cudaStream_t s);
+
+// gemm_run_ep's D = act(rs cs A B + bias) of checked arguments, fp32 accumulation, A
+// row-major and B column-major, whose ReLU keeps a NaN.
+gemm_status_t run_keep_nan(gemm_plan* plan, const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
+                           int64_t lda, int64_t ldb, int64_t ldd, gemm_dtype_t out, const gemm_epilogue_t* ep,
+                           cudaStream_t s);
 
 // 2-D tensor map over a matrix whose contiguous dimension has `inner`
 // elements (rows of `ld` elements), 128-byte swizzle, zero fill outside.
@@ -281,9 +290,9 @@ void fill_launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, cuda
 }
 
 // Shared-memory opt-in and co-residency of one kernel instantiation.
-template <class Cfg, bool EP = false>
+template <class Cfg, int EP = tcdt::kEpNone>
 gemm_status_t prepare(gemm_plan* plan, int kind, int slot) {
-    if (plan->attr_set[kind][slot + (EP ? 4 : 0)]) return GEMM_OK;
+    if (plan->attr_set[kind][slot + 4 * EP]) return GEMM_OK;
     auto kern = tcdt::gemm_sm103_kernel<Cfg, EP>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess) {
         cudaGetLastError();
@@ -305,7 +314,7 @@ gemm_status_t prepare(gemm_plan* plan, int kind, int slot) {
     cudaGetLastError();
     if (units <= 0) units = plan->sm_count / Cfg::CG;
     if (plan->units[kind] == 0 || units < plan->units[kind]) plan->units[kind] = units;
-    plan->attr_set[kind][slot + (EP ? 4 : 0)] = true;
+    plan->attr_set[kind][slot + 4 * EP] = true;
     return GEMM_OK;
 }
 
@@ -350,7 +359,7 @@ inline int fill_schedule(KernelParams& p, const Choice& ch, int64_t M, int64_t N
     return work < ch.units ? static_cast<int>(work) : ch.units;
 }
 
-template <class Cfg, bool EP = false>
+template <class Cfg, int EP = tcdt::kEpNone>
 gemm_status_t launch_tc(gemm_plan* plan, const Choice& ch, const Problem& pr, const void* C, void* D,
                         int64_t ldc, float alpha, float beta, gemm_dtype_t out_dtype, cudaStream_t stream) {
     const bool a_mn = pr.la == GEMM_COL_MAJOR;   // column-major A is M-contiguous
@@ -461,7 +470,7 @@ gemm_status_t launch_tc(gemm_plan* plan, const Choice& ch, const Problem& pr, co
 
 // Output slots: 0 fp32, 1 fp16, 2 bf16 (fp32 accumulation), 3 fp16 with fp16
 // accumulation (16-bit operands only).
-template <template <bool, int, int> class CfgT, int IN = tcdt::kInF16, bool EP = false>
+template <template <bool, int, int> class CfgT, int IN = tcdt::kInF16, int EP = tcdt::kEpNone>
 gemm_status_t prepare_kind(gemm_plan* plan, int kind, int slot) {
     switch (slot) {
         case 0: return prepare<CfgT<false, tcdt::kOutF32, IN>, EP>(plan, kind, slot);
@@ -473,7 +482,7 @@ gemm_status_t prepare_kind(gemm_plan* plan, int kind, int slot) {
     }
 }
 
-template <template <bool, int, int> class CfgT, int IN = tcdt::kInF16, bool EP = false>
+template <template <bool, int, int> class CfgT, int IN = tcdt::kInF16, int EP = tcdt::kEpNone>
 gemm_status_t launch_kind(gemm_plan* plan, int slot, const Choice& ch, const Problem& pr, const void* C, void* D,
                           int64_t ldc, float alpha, float beta, cudaStream_t s) {
     gemm_status_t st = prepare_kind<CfgT, IN, EP>(plan, ch.kind, slot);
@@ -504,7 +513,7 @@ gemm_status_t launch_kind(gemm_plan* plan, int slot, const Choice& ch, const Pro
     gemm_status_t launch_##name##_ep(gemm_plan* plan, int slot, const Choice& ch, const Problem& pr,     \
                                      const void* C, void* D, int64_t ldc, float alpha, float beta,       \
                                      cudaStream_t s) {                                                    \
-        return launch_kind<CfgT, tcdt::kInF16, true>(plan, slot, ch, pr, C, D, ldc, alpha, beta, s);    \
+        return launch_kind<CfgT, tcdt::kInF16, tcdt::kEpFused>(plan, slot, ch, pr, C, D, ldc, alpha, beta, s);    \
     }
 
 #define TCDT_DEFINE_KIND_IN(name, CfgT, suffix, IN)                                                      \
@@ -518,7 +527,7 @@ gemm_status_t launch_kind(gemm_plan* plan, int slot, const Choice& ch, const Pro
     gemm_status_t launch_##name##_##suffix##_ep(gemm_plan* plan, int slot, const Choice& ch,            \
                                                 const Problem& pr, const void* C, void* D, int64_t ldc,  \
                                                 float alpha, float beta, cudaStream_t s) {               \
-        return launch_kind<CfgT, IN, true>(plan, slot, ch, pr, C, D, ldc, alpha, beta, s);              \
+        return launch_kind<CfgT, IN, tcdt::kEpFused>(plan, slot, ch, pr, C, D, ldc, alpha, beta, s);              \
     }
 
 }  // namespace tcdt_host

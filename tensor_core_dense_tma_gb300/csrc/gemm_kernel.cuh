@@ -465,6 +465,10 @@ struct Vec {
     static constexpr int ESZ = OUT == kOutF32 ? 4 : 2;
 };
 
+// EP of the kernels: without the fused epilogue, with it, and with it and a
+// ReLU that keeps a NaN.
+constexpr int kEpNone = 0, kEpFused = 1, kEpKeepNan = 2;
+
 // Fused epilogue ("矩阵乘法优化可视化学习文档", section 6, epilogue fusion:
 // bias, activation and scale applied before the write-back):
 //     x = alpha * (s_row[r] * s_col[c] * acc) + beta * C + bias
@@ -504,12 +508,18 @@ __device__ __forceinline__ float ep_gelu(float x) {
 // The activation over a whole segment: the test on `act` stays outside the
 // element loops, so each activation is one straight run of code (a test per
 // element interleaved the three bodies and the epilogue warps then missed in
-// the instruction cache they share with the producer and MMA warps).
-template <int W>
+// the instruction cache they share with the producer and MMA warps).  fmaxf
+// makes a NaN 0; the ReLU of kEpKeepNan, for the 8-bit product, keeps it (in
+// instantiations of their own: a second ReLU beside this one cost 4096^3 with a
+// bias 0.7 % and with GELU 1.5 %).
+template <int W, int EP = kEpFused>
 __device__ __forceinline__ void ep_act_w(uint32_t act, float (&v)[W]) {
     if (act == 1u) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = fmaxf(v[i], 0.0f);
+        for (int i = 0; i < W; ++i) {
+            if constexpr (EP == kEpKeepNan) asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(v[i]) : "f"(v[i]));
+            else v[i] = fmaxf(v[i], 0.0f);
+        }
     } else if (act == 2u) {
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = ep_gelu(v[i]);
@@ -530,7 +540,7 @@ __device__ __forceinline__ void ep_scale(const KernelParams& p, float (&a)[W], i
     }
 }
 
-template <int W>
+template <int W, int EP>
 __device__ __forceinline__ void ep_finish(const KernelParams& p, float (&v)[W], int row, int col0) {
     const float br = (p.bias_row && row < p.M) ? __ldg(p.bias_row + row) : kNoBias;
     if (p.bias_col) {
@@ -543,7 +553,7 @@ __device__ __forceinline__ void ep_finish(const KernelParams& p, float (&v)[W], 
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += br;
     }
-    ep_act_w<W>(p.act, v);
+    ep_act_w<W, EP>(p.act, v);
 }
 
 // Warp form, for the paths where the 32 lanes of a warp hold 32 rows of the
@@ -582,7 +592,7 @@ __device__ __forceinline__ void ep_scale_w(const KernelParams& p, const EpLane& 
     }
 }
 
-template <int W>
+template <int W, int EP>
 __device__ __forceinline__ void ep_finish_w(const KernelParams& p, const EpLane& e, float (&v)[W]) {
     if (p.bias_col) {
 #pragma unroll
@@ -591,7 +601,7 @@ __device__ __forceinline__ void ep_finish_w(const KernelParams& p, const EpLane&
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += e.br;
     }
-    ep_act_w<W>(p.act, v);
+    ep_act_w<W, EP>(p.act, v);
 }
 
 // 16 bytes of C (one aligned group) into c[i0 .. i0+VEC).
@@ -763,7 +773,7 @@ __device__ __forceinline__ void store_d_block(const KernelParams& p, int row0, i
 
 // alpha * acc (+ beta * C) for W consecutive accumulator columns of one
 // accumulator row, written to D (row-major, or transposed with trans_out).
-template <class Cfg, bool EP>
+template <class Cfg, int EP>
 __device__ __forceinline__ void epilogue_chunk(const KernelParams& p, const float (&acc)[Cfg::W], int row,
                                                int col0, bool row_ok = true, int lane = 0) {
     if constexpr (!EP) {
@@ -821,7 +831,7 @@ __device__ __forceinline__ void epilogue_chunk(const KernelParams& p, const floa
                         v[i] = fmaf(p.alpha, a[i],
                                     p.beta * load_elem<Cfg::OUT>(p.C, static_cast<int64_t>(col0 + i) * p.ldc + row));
             }
-            if (p.ep) ep_finish_w<W>(p, ec, v);
+            if (p.ep) ep_finish_w<W, EP>(p, ec, v);
     #pragma unroll
             for (int i = 0; i < W; ++i)
                 if (i < n) store_elem<Cfg::OUT>(p.D, static_cast<int64_t>(col0 + i) * p.ldc + row, v[i]);
@@ -838,7 +848,7 @@ __device__ __forceinline__ void epilogue_chunk(const KernelParams& p, const floa
     #pragma unroll
             for (int i = 0; i < W; ++i) v[i] = fmaf(p.alpha, a[i], p.beta * c[i]);
         }
-        if (p.ep) ep_finish_w<W>(p, ec, v);
+        if (p.ep) ep_finish_w<W, EP>(p, ec, v);
         if (row_ok) row_segment_dispatch<Cfg::OUT, W, true>(static_cast<char*>(p.D) + off * ESZ, v, n);
     
     }
@@ -846,7 +856,7 @@ __device__ __forceinline__ void epilogue_chunk(const KernelParams& p, const floa
 
 // alpha * acc (+ beta * C) for 4 consecutive columns of one row (used by the
 // split-K reduction, whose threads own consecutive column quads of a row).
-template <class Cfg, bool EP>
+template <class Cfg, int EP>
 __device__ __forceinline__ void epilogue_quad(const KernelParams& p, const float4& a, int row, int col) {
     if constexpr (!EP) {
         constexpr int ESZ = Vec<Cfg::OUT>::ESZ;
@@ -901,7 +911,7 @@ __device__ __forceinline__ void epilogue_quad(const KernelParams& p, const float
                         v[i] = fmaf(p.alpha, acc[i],
                                     p.beta * load_elem<Cfg::OUT>(p.C, static_cast<int64_t>(col + i) * p.ldc + row));
             }
-            if (p.ep) ep_finish<4>(p, v, row, col);
+            if (p.ep) ep_finish<4, EP>(p, v, row, col);
     #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < n) store_elem<Cfg::OUT>(p.D, static_cast<int64_t>(col + i) * p.ldc + row, v[i]);
@@ -913,7 +923,7 @@ __device__ __forceinline__ void epilogue_quad(const KernelParams& p, const float
             for (int i = 0; i < 4; ++i)
                 if (i < n) v[i] = fmaf(p.alpha, acc[i], p.beta * load_elem<Cfg::OUT>(p.C, off + i));
         }
-        if (p.ep) ep_finish<4>(p, v, row, col);
+        if (p.ep) ep_finish<4, EP>(p, v, row, col);
         char* dp = static_cast<char*>(p.D) + off * ESZ;
         if (n == 4 && (reinterpret_cast<uintptr_t>(dp) & (4 * ESZ - 1)) == 0) {
             if constexpr (Cfg::OUT == kOutF32) {
@@ -979,7 +989,7 @@ __device__ __forceinline__ void stage_row_and_store(const void* tmap, const uint
 
 // Epilogue values of one segment -> D through the staging buffer.  `ec`:
 // the segment's epilogue vectors (EP), loaded a segment ahead by the caller.
-template <class Cfg, bool EP>
+template <class Cfg, int EP>
 __device__ __forceinline__ void stage_and_store(const KernelParams& p, const void* tmap, float (&v)[32], int row,
                                                 int col0, int row0w, int lane, uint32_t stg, int& sbuf,
                                                 bool row_ok, const EpLane& ec) {
@@ -1007,7 +1017,7 @@ __device__ __forceinline__ void stage_and_store(const KernelParams& p, const voi
         for (int i = 0; i < 32; ++i) v[i] = fmaf(p.alpha, acc[i], p.beta * c[i]);
     }
     if constexpr (EP) {
-        if (p.ep) ep_finish_w<32>(p, ec, v);
+        if (p.ep) ep_finish_w<32, EP>(p, ec, v);
     }
     if constexpr (Cfg::OUT == kOutF32) {
         uint32_t words[32];
@@ -1031,7 +1041,7 @@ __device__ __forceinline__ void stage_and_store_f32(const void* tmap, const uint
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <class Cfg, bool EP = false>
+template <class Cfg, int EP = kEpNone>
 __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
 gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmD,
@@ -1626,7 +1636,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                                 for (int i = 0; i < W; ++i) v[i] = fmaf(p.alpha, a[i], p.beta * cv[i]);
                             }
                             if constexpr (EP) {
-                                if (p.ep) ep_finish_w<W>(p, ec, v);
+                                if (p.ep) ep_finish_w<W, EP>(p, ec, v);
                             }
                             store_d_block<Cfg::OUT>(p, row0w, col0, lane, cur, v);
                         }
@@ -1777,7 +1787,8 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 // epilogue gives it for a sum that comes to zero.
 template <int OUT>
 __global__ void scale_c_kernel(int32_t M, int32_t N, const void* C, void* D, int64_t ldc, float alpha, float beta,
-                               const float* row_scale, const float* col_scale, const float* bias, uint32_t act) {
+                               const float* row_scale, const float* col_scale, const float* bias, uint32_t act,
+                               bool keep_nan) {
     const int64_t total = static_cast<int64_t>(M) * N;
     for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < total;
          e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -1788,7 +1799,8 @@ __global__ void scale_c_kernel(int32_t M, int32_t N, const void* C, void* D, int
         float v = beta != 0.0f ? fmaf(alpha, a0, beta * load_elem<OUT>(C, off)) : alpha * a0;
         if (bias) v += bias[j];
         float a[1] = {v};
-        ep_act_w<1>(act, a);
+        if (keep_nan) ep_act_w<1, kEpKeepNan>(act, a);
+        else ep_act_w<1>(act, a);
         store_elem<OUT>(D, off, a[0]);
     }
 }

@@ -2,8 +2,9 @@
 
 A row with one has it as its scale (max |x| / 127), and x / scale is then no
 number or 0: the row's codes are 0 and its results, 0 times the scale, NaN.
-No tolerance is needed there; the rows beside are compared as in
-test_gpu_i8.py (exact codes and sums, two scalings and the bias in fp32).
+A NaN stays one through every activation.  No tolerance is needed there; the
+rows beside are compared as in test_gpu_i8.py (exact codes and sums, two
+scalings and the bias in fp32).
 """
 import math
 
@@ -87,3 +88,28 @@ def test_scales_of_given_codes(plan, M, N, K, launches):
     bad = torch.zeros((M, N), dtype=torch.bool, device="cuda")
     bad[M // 2], bad[:, 5], bad[:, N - 1] = True, True, True
     assert torch.equal(torch.isnan(D), bad)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu"])
+@pytest.mark.parametrize("M,N,K,launches", SIZES, ids=lambda v: str(v))
+def test_activations_keep_a_nan(plan, M, N, K, launches, act):
+    """A NaN sum is no negative number: it does not become 0."""
+    x = torch.randn((M, K), device="cuda")
+    x[M // 2, 3] = NAN
+    W, _ = codes(N, K, 4)
+    bias = torch.randn(N, device="cuda")
+    bias[N // 2] = NAN
+    cs = torch.full((N,), 1.0 / K, device="cuda")
+    for out in TYPES:
+        D = plan.linear_i8(x, W.t(), col_scale=cs, bias=bias, act=act, out_dtype=out)
+        bad = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+        bad[M // 2], bad[:, N // 2] = True, True
+        assert torch.equal(torch.isnan(D), bad)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu"])
+def test_activation_of_an_empty_sum_keeps_a_nan(plan, act):
+    bias = torch.tensor([1.0, NAN, -1.0], device="cuda")
+    A, W = torch.zeros((5, 0), dtype=torch.int8, device="cuda"), torch.zeros((3, 0), dtype=torch.int8, device="cuda")
+    D = plan.gemm_i8(A, W.t(), bias=bias, act=act)
+    assert torch.isnan(D[:, 1]).all() and not torch.isnan(D[:, [0, 2]]).any()
