@@ -305,6 +305,12 @@ unsigned dependent(cudaLaunchAttribute& attr) {
     return 1;
 }
 
+// Channels over x, tiles of tokens over y and z (token_tile).
+dim3 tile_grid(int64_t x, int64_t token_tiles) {
+    const int64_t z = (token_tiles + 65534) / 65535;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>((token_tiles + z - 1) / z), static_cast<unsigned>(z));
+}
+
 template <int MT, int R>
 gemm_status_t launch_dot(gemm_plan* plan, const tcdt_i8::Params& p, bool after_tokens, gemm_dtype_t out,
                          cudaStream_t s) {
@@ -370,7 +376,7 @@ gemm_status_t launch_tile(gemm_plan* plan, tcdt_i8::Params p, const __half* x, i
     }
     prepared = true;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles_n * p.splits), static_cast<unsigned>(tiles_m), 1);
+    cfg.gridDim = tile_grid(tiles_n * p.splits, tiles_m);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = s;
@@ -423,7 +429,7 @@ gemm_status_t launch_pair(gemm_plan* plan, tcdt_i8::Params p, const __half* x, i
     }
     prepared = true;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.N + 255) / 256 * 2), static_cast<unsigned>((p.M + Cfg::BN - 1) / Cfg::BN), 1);
+    cfg.gridDim = tile_grid((p.N + int64_t{255}) / 256 * 2, (p.M + int64_t{Cfg::BN - 1}) / Cfg::BN);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = s;

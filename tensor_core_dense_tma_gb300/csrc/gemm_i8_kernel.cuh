@@ -47,6 +47,10 @@ struct Params {
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// This CTA's tile of tokens: they go over y and z of the grid, as y ends at
+// 65535 (8.4 million tokens); the last ones of z may be beyond the last tile.
+__device__ __forceinline__ uint32_t token_tile() { return blockIdx.z * gridDim.y + blockIdx.y; }
+
 template <int OUT>
 __device__ __forceinline__ void finish_store(const Params& p, float sum, float rs, float cs, float bias, int64_t m,
                                              int64_t n) {
@@ -302,7 +306,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = p.splits > 1 ? static_cast<int>(tcdt::cluster_ctarank()) : 0;
     const int n0 = static_cast<int>(blockIdx.x / p.splits) * 128;
-    const int m0 = static_cast<int>(blockIdx.y) * BN;
+    if (token_tile() * BN >= static_cast<uint32_t>(p.M)) return;     // the whole cluster's
+    const int m0 = static_cast<int>(token_tile()) * BN;
     const int blocks = (p.K + KS - 1) / KS;
     const int kb0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / p.splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / p.splits);
@@ -587,7 +592,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
     const int rank = static_cast<int>(tcdt::cluster_ctarank());
     const bool leader = rank == 0;
     const int n0 = static_cast<int>(blockIdx.x) * 128;       // the pair's channels lie side by side
-    const int m0 = static_cast<int>(blockIdx.y) * Cfg::BN;
+    if (token_tile() * Cfg::BN >= static_cast<uint32_t>(p.M)) return;     // the whole pair's
+    const int m0 = static_cast<int>(token_tile()) * Cfg::BN;
     const int blocks = (p.K + KS - 1) / KS;
 
     if (threadIdx.x == 0) {
