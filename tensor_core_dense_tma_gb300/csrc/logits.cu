@@ -41,6 +41,8 @@ constexpr int kUnroll = 1024 / kThreads; // 16-byte vectors of a thread in a chu
 constexpr int kChunk = kUnroll * kThreads;   // vectors of an asynchronous copy: 16 KB
 constexpr int kSlotsMost = 12;           // of the ring
 constexpr int kBlock = kThreads + 32;
+// A copy is waited for this long, other CTAs' statistics twice as long (a CTA that
+// gave up on a copy still brings its own), a slot of the ring three times.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 1024;        // kMaxCluster lists of LOGITS_MAX_TOP fit too
@@ -83,6 +85,18 @@ struct Args {
     float* lse;
     void* dz;
     int64_t ldd;
+#ifdef TCDT_FAULT_INJECTION
+    // test builds only: the limit above; in CTAs of rank fi_rank of a row (-1: all) the copy that is not
+    // started, the chunk that the warps of a mask do not wait for, and whether statistics are kept back
+    uint64_t fi_limit_ns;
+    int64_t fi_skip_copy, fi_late_chunk;
+    uint32_t fi_late_warps;
+    int fi_silent, fi_rank;
+    __device__ bool fi_here(int rank) const { return fi_rank < 0 || fi_rank == rank; }
+    __device__ uint64_t limit_ns() const { return fi_limit_ns; }
+#else
+    __device__ static constexpr uint64_t limit_ns() { return kWaitLimitNs; }
+#endif
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -117,12 +131,27 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// Waits for a phase of a barrier; false once kWaitLimitNs have passed.
-__device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity) {
+// Waits for a phase of a barrier; false once the limit has passed.
+__device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     if (tcdt::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = tcdt::globaltimer_ns();
     while (!tcdt::mbar_try_wait(bar, parity))
-        if (tcdt::globaltimer_ns() - t0 > kWaitLimitNs) return false;
+        if (tcdt::globaltimer_ns() - t0 > limit_ns) return false;
+    return true;
+}
+
+// The same while nobody of the CTA has given up: the first one to do so says it
+// to the others, so that they do not wait out the limit one after another.
+__device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* gave_up) {
+    if (tcdt::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tcdt::globaltimer_ns();
+    while (!tcdt::mbar_try_wait(bar, parity)) {
+        if (*gave_up) return false;
+        if (tcdt::globaltimer_ns() - t0 > limit_ns) {
+            *gave_up = 1;
+            return false;
+        }
+    }
     return true;
 }
 
@@ -148,12 +177,12 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t at, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
-// wait_copy for arrivals from other CTAs of the cluster.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+// wait_limited for arrivals from other CTAs of the cluster.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     if (tcdt::mbar_try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = tcdt::globaltimer_ns();
     while (!tcdt::mbar_try_wait_cluster(bar, parity))
-        if (tcdt::globaltimer_ns() - t0 > kWaitLimitNs) return false;
+        if (tcdt::globaltimer_ns() - t0 > limit_ns) return false;
     return true;
 }
 
@@ -614,9 +643,12 @@ __device__ __forceinline__ void select_top(TopState& t, uint64_t* list, int* cou
 // four: 454 us, in clusters of two 375; gradient stores are marked streaming to
 // leave L2 to the logits).  The segments' statistics go from each CTA into
 // every other one's shared memory, counted by an mbarrier.
-// A copy that has not arrived after kWaitLimitNs is not waited for again: its
-// vectors, and all later ones, are read from memory; statistics that have not
-// arrived make the row NaN.
+// A thread whose copy has not arrived in time waits for none again: it reads
+// its vectors of that chunk and all later ones from memory.  Its warp, if it is
+// lane 0, gives no slot back any more, as it no longer knows that one was filled:
+// what is in the ring then stays there for the threads that did see it arrive,
+// and the warp that copies, which waits for every warp, starts no more copies.
+// Statistics that have not arrived make the row NaN.
 template <typename E, int OP, bool GRAD, bool TOP>
 __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args a) {
     constexpr int kPer = Ele<E>::kPer;
@@ -624,6 +656,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
     __shared__ Exchange inbox[2][kMaxCluster], all;      // by the row's parity
+    __shared__ volatile int gave_up;                     // on a copy or a slot of the ring
     __shared__ __align__(8) uint64_t full_bar[kSlotsMost], empty_bar[kSlotsMost], inbox_bar[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x % a.cluster);
@@ -646,6 +679,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             tcdt::mbar_init(empty + 8 * i, kWarps);
         }
         for (int i = 0; i < 2; ++i) tcdt::mbar_init(tcdt::smem_addr(&inbox_bar[i]), static_cast<uint32_t>(a.cluster));
+        gave_up = 0;
         tcdt::fence_mbar_init();
     }
     if (OP == kDistill && tid < K4 - a.K) tok[a.K + tid] = -2;
@@ -663,18 +697,21 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                 const int chunks = seg.chunks(), again = GRAD ? chunks - min(chunks, a.slots) : 0;
                 for (int i = 0; i < chunks + again; ++i) {
                     const int from = (i < chunks ? i : i - chunks) * kChunk;
-                    ok = wait_copy(empty + 8 * slot, parity);
+                    ok = wait_copy(empty + 8 * slot, parity, 3 * a.limit_ns(), &gave_up);
                     if (!ok) break;
                     const uint32_t bytes = static_cast<uint32_t>(min(kChunk, seg.n - from)) * 16u;
                     tcdt::mbar_arrive_expect_tx(full + 8 * slot, bytes);
-                    copy_bulk(tcdt::smem_addr(ring + slot * kChunk), seg.vec + from, bytes, full + 8 * slot);
+#ifdef TCDT_FAULT_INJECTION
+                    if (!(started == a.fi_skip_copy && a.fi_here(rank)))
+#endif
+                        copy_bulk(tcdt::smem_addr(ring + slot * kChunk), seg.vec + from, bytes, full + 8 * slot);
                     ++started;
                     if (++slot == a.slots) slot = 0, parity ^= 1u;
                 }
             }
             // a copy must not land in another CTA's memory
             for (int i = 0; i < a.slots && i < started; ++i)
-                wait_copy(full + 8 * i, static_cast<uint32_t>((started - 1 - i) / a.slots) & 1u);
+                wait_limited(full + 8 * i, static_cast<uint32_t>((started - 1 - i) / a.slots) & 1u, a.limit_ns());
         }
         __syncwarp();
         if (a.cluster > 1) tcdt::cluster_sync_all();
@@ -684,9 +721,15 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     int slot = 0;
     uint32_t parity = 0;
     bool late = false;
+#ifdef TCDT_FAULT_INJECTION
+    int64_t taken = 0;
+#endif
     // the thread's vectors of a chunk, -inf beyond the segment's end; true if all are inside
     auto take = [&](const Segment<E>& seg, int chunk, bool give_back, uint4 (&q)[kUnroll]) {
-        if (!late && !wait_copy(full + 8 * slot, parity)) late = true;
+#ifdef TCDT_FAULT_INJECTION
+        if (taken++ == a.fi_late_chunk && a.fi_here(rank) && (a.fi_late_warps >> warp & 1u)) late = true;
+#endif
+        if (!late && !wait_copy(full + 8 * slot, parity, a.limit_ns(), &gave_up)) late = true;
         const uint4* at = ring + slot * kChunk + tid;
         const bool inside = !late && (chunk + 1) * kChunk <= seg.n;
         if (inside) {
@@ -702,7 +745,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         }
         if (give_back) {
             __syncwarp();
-            if (lane == 0) tcdt::mbar_arrive(empty + 8 * slot);
+            if (lane == 0 && !late) tcdt::mbar_arrive(empty + 8 * slot);
         }
         if (++slot == a.slots) slot = 0, parity ^= 1u;
         return inside;
@@ -857,13 +900,17 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             bool arrived = true;
             if (a.cluster > 1) {
                 const uint32_t bar = tcdt::smem_addr(&inbox_bar[turn & 1]);
+#ifdef TCDT_FAULT_INJECTION
+                if (a.fi_silent && a.fi_here(rank)) {
+                } else
+#endif
                 if (lane < a.cluster) {
                     const uint32_t to = tcdt::map_to_cta(tcdt::smem_addr(&inbox[turn & 1][rank]), static_cast<uint32_t>(lane));
                     st_cluster_f32(to, x.s.m), st_cluster_f32(to + 4, x.s.S), st_cluster_f32(to + 8, x.s.U);
                     st_cluster_f32(to + 12, x.A), st_cluster_f32(to + 16, x.P);
                     tcdt::mbar_arrive_cluster(tcdt::map_to_cta(bar, static_cast<uint32_t>(lane)));
                 }
-                arrived = __all_sync(~0u, wait_cluster(bar, static_cast<uint32_t>(turn >> 1) & 1u));
+                arrived = __all_sync(~0u, wait_cluster(bar, static_cast<uint32_t>(turn >> 1) & 1u, 2 * a.limit_ns()));
                 x = lane < a.cluster ? inbox[turn & 1][lane] : Exchange{empty_stats(), 0.f, 0.f};
                 s = warp_join<kEntropy>(x.s, kMaxCluster, a.c);
             }
@@ -1065,6 +1112,15 @@ gemm_status_t check_gradient(gemm_dtype_t dtype, const void* dlogits, int64_t T,
     return aligned(dlogits, bytes_of(dtype)) ? GEMM_OK : GEMM_ERR_MISALIGNED;
 }
 
+#ifdef TCDT_FAULT_INJECTION
+struct {
+    uint64_t limit_ns = kWaitLimitNs;
+    int64_t skip_copy = -1, late_chunk = -1;
+    uint32_t late_warps = 0;
+    int silent = 0, rank = -1;
+} g_fi;
+#endif
+
 // What is asked once of a device: whether it is the kind the kernels are
 // built for, and its number of SMs.
 constexpr int kDevices = 64;
@@ -1140,6 +1196,14 @@ gemm_status_t launch(Args a, int64_t T, int device, int sms, cudaStream_t stream
     a.per = static_cast<int>((a.V / Ele<E>::kPer + cluster - 1) / cluster);
     a.rows = static_cast<int>(rows);
     a.slots = static_cast<int>(slots);
+#ifdef TCDT_FAULT_INJECTION
+    a.fi_limit_ns = g_fi.limit_ns;
+    a.fi_skip_copy = g_fi.skip_copy;
+    a.fi_late_chunk = g_fi.late_chunk;
+    a.fi_late_warps = g_fi.late_warps;
+    a.fi_silent = g_fi.silent;
+    a.fi_rank = g_fi.rank;
+#endif
     const size_t dyn = static_cast<size_t>(slots) * kChunk * 16 + static_cast<size_t>(beside);
     const int64_t ctas = (T + rows - 1) / rows * cluster;
     auto kernel = rows_kernel<E, OP, GRAD, TOP>;
@@ -1302,5 +1366,15 @@ gemm_status_t logits_distill_grad(int device, gemm_dtype_t dtype, const void* lo
     a.ldd = ldd;
     return launch_type<kDistill, true, false>(device, dtype, a, T, stream);
 }
+
+#ifdef TCDT_FAULT_INJECTION
+// Test builds only (not part of the product library or of include/logits.h), for
+// the calls that follow: see Args.
+gemm_status_t logits_test_inject(uint64_t limit_ns, int64_t skip_copy, int64_t late_chunk, uint32_t late_warps,
+                                 int silent, int rank) {
+    g_fi = {limit_ns, skip_copy, late_chunk, late_warps, silent, rank};
+    return GEMM_OK;
+}
+#endif
 
 }  // extern "C"
