@@ -31,7 +31,7 @@
  * Results do not depend on timing: the same inputs give the same bits.  Every
  * wait inside a kernel is bounded: a copy that has not arrived after 2 s is
  * made up for by plain loads, a row whose CTAs then still wait for one another's
- * statistics becomes NaN.
+ * statistics becomes NaN, its alternatives NaN and -1.
  *
  * Errors.  Arguments are checked on the host before anything is launched:
  * GEMM_ERR_INVALID_ARG (null pointer, negative size, stride below its row

@@ -648,7 +648,7 @@ __device__ __forceinline__ void select_top(TopState& t, uint64_t* list, int* cou
 // lane 0, gives no slot back any more, as it no longer knows that one was filled:
 // what is in the ring then stays there for the threads that did see it arrive,
 // and the warp that copies, which waits for every warp, starts no more copies.
-// Statistics that have not arrived make the row NaN.
+// Statistics that have not arrived make the row NaN, and its alternatives none.
 template <typename E, int OP, bool GRAD, bool TOP>
 __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args a) {
     constexpr int kPer = Ele<E>::kPer;
@@ -656,6 +656,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
     __shared__ Exchange inbox[2][kMaxCluster], all;      // by the row's parity
+    __shared__ bool heard;                               // of every CTA of the row
     __shared__ volatile int gave_up;                     // on a copy or a slot of the ring
     __shared__ __align__(8) uint64_t full_bar[kSlotsMost], empty_bar[kSlotsMost], inbox_bar[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             }
             if (!arrived) s.S = NAN, l = NAN;
             __syncwarp();
-            if (lane == 0) all = {s, l, sum_P};
+            if (lane == 0) all = {s, l, sum_P}, heard = arrived;
         }
         sync_threads();
         s = all.s;
@@ -1039,7 +1040,13 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         }
 
         if constexpr (TOP) {
-            if (rank == 0) {
+            if (rank == 0 && !heard) {
+                // no CTA's list is known to be whole: none is read
+                for (int i = tid; i < a.top; i += kThreads) {
+                    a.top_logprob[r * a.top + i] = NAN;
+                    a.top_token[r * a.top + i] = -1;
+                }
+            } else if (rank == 0) {
                 // the segments' lists side by side; a key's place is its place in its own list and the
                 // number of larger keys in each of the others
                 const int n = a.top, lists = a.cluster;

@@ -1,11 +1,12 @@
-"""The operators on logits when a copy into the ring of shared memory does not
-arrive, without a GPU fault: bounded waits run out.
+"""The operators on logits when a copy into the ring of shared memory or another
+CTA's statistics do not arrive, without a GPU fault: bounded waits run out.
 
 A test build of the library (-DTCDT_FAULT_INJECTION, a separate .so) lets the
 warp that copies arm a chunk's barrier and start no copy, or lets some of the
 computing warps give up on a chunk at once while the others see it arrive, in
 every CTA or in one CTA of a row.  The kernel makes up for it by plain loads, so
-the results are those without the fault, bit for bit.
+the results are those without the fault, bit for bit.  A CTA that keeps back its
+statistics makes the rows that it shares NaN.
 """
 import ctypes
 import os
@@ -106,5 +107,27 @@ def test_late_copies_are_made_up_for(fi, T, V, kind, op):
         if fault == dict(skip_copy=0):
             assert waited > LIMIT_NS * 1e-9       # a wait did run out
         assert same(got, want), fault
+    inject(fi)
+    assert same(case.run(fi, op), want)
+
+
+@pytest.mark.parametrize("rank", [0, 1, 7])
+@pytest.mark.parametrize("op", OPS)
+def test_statistics_that_do_not_arrive(fi, op, rank):
+    """Rows split over eight CTAs, one of which tells the others nothing."""
+    T, V = 3, 131072
+    case = Case(T, V, "f32")
+    inject(fi)
+    want = case.run(fi, op)
+    inject(fi, silent=1, rank=rank)
+    t0 = time.monotonic()
+    *f, tv, ti, d = case.run(fi, op)
+    assert LIMIT_NS * 2e-9 < time.monotonic() - t0 < 10.0
+    for x in f[:2] if op.startswith("distill") else f:
+        assert torch.isnan(x).all()
+    if op == "top":
+        assert torch.isnan(tv).all() and bool((ti == -1).all())
+    if "grad" in op:
+        assert torch.isnan(d).all()
     inject(fi)
     assert same(case.run(fi, op), want)
