@@ -62,7 +62,7 @@ struct Args {
     int64_t ld;
     int32_t V;
     int64_t T;
-    int cluster, rows, slots;     // CTAs of a row, rows of a cluster, chunks of the ring
+    int cluster, rows, slots;     // CTAs of a row, rows of a CTA, chunks of the ring
     int per;                      // vectors of a segment
     float c, inv_t, t;            // log2(e) / temperature, 1 / temperature, temperature
     const int64_t* tokens;        // [T], or teacher tokens [T][ldt]
@@ -140,18 +140,13 @@ __device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, uint
     return true;
 }
 
-// The same while nobody of the CTA has given up: the first one to do so says it
-// to the others, so that they do not wait out the limit one after another.
-__device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* gave_up) {
+// The same for a slot of the ring, given up as soon as a computing thread has
+// given up on a copy (the slot may then never be given back).
+__device__ __forceinline__ bool wait_slot(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* gave_up) {
     if (tcdt::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = tcdt::globaltimer_ns();
-    while (!tcdt::mbar_try_wait(bar, parity)) {
-        if (*gave_up) return false;
-        if (tcdt::globaltimer_ns() - t0 > limit_ns) {
-            *gave_up = 1;
-            return false;
-        }
-    }
+    while (!tcdt::mbar_try_wait(bar, parity))
+        if (*gave_up || tcdt::globaltimer_ns() - t0 > limit_ns) return false;
     return true;
 }
 
@@ -462,17 +457,17 @@ struct Exchange {
 
 // The keys of a segment's largest logits, in descending order.
 struct TopState {
-    uint64_t list[2][LOGITS_MAX_TOP];    // by the row's parity: the other CTAs may still read the last row's
+    uint64_t list[LOGITS_MAX_TOP];
     uint64_t cand[kCandidates];
     uint32_t key[kThreads];
     int narrow[kThreads], wide[kThreads], batch[kThreads];
     int narrows, wides, found;
-    int count[2];
+    int count;                           // of keys in the list
     uint32_t thr;
     int reach;
 };
 
-// `count` = the number of keys in list[0..n-1], the rest 0.
+// Into t.list[0..n-1] and t.count; the rest of the list is 0.
 //
 // Each thread's logits are a bucket, of which `key` is the largest one's
 // ordered value and `batch` the first chunk of vectors that has it (kInHead,
@@ -489,9 +484,10 @@ constexpr uint32_t kOrderedLowest = 0x00800000u;     // ordered(-FLT_MAX)
 constexpr int kInHead = -1, kInTail = INT_MAX;
 
 template <typename E>
-__device__ __forceinline__ void select_top(TopState& t, uint64_t* list, int* count_out, const Segment<E>& seg,
-                                           uint32_t key, int batch, float second, int n) {
+__device__ __forceinline__ void select_top(TopState& t, const Segment<E>& seg, uint32_t key, int batch, float second,
+                                           int n) {
     constexpr int kPer = Ele<E>::kPer;
+    uint64_t* list = t.list;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) t.narrows = t.wides = t.found = 0;
     for (int i = tid; i < n; i += kThreads) list[i] = 0;
@@ -591,7 +587,7 @@ __device__ __forceinline__ void select_top(TopState& t, uint64_t* list, int* cou
             for (int o = 0; o < found; ++o) place += t.cand[o] > k;
             if (place < n) list[place] = k;
         }
-        if (tid == 0) *count_out = found < n ? found : n;
+        if (tid == 0) t.count = found < n ? found : n;
         sync_threads();
         return;
     }
@@ -627,12 +623,12 @@ __device__ __forceinline__ void select_top(TopState& t, uint64_t* list, int* cou
         if (tid == 0) list[count] = best;
         last = best;
     }
-    if (tid == 0) *count_out = count;
+    if (tid == 0) t.count = count;
     sync_threads();
 }
 
-// A cluster of a.cluster CTAs computes a row, a segment each, and a.rows rows
-// one after another.  A segment comes in chunks through a ring in shared
+// A cluster of a.cluster CTAs computes a row, a segment each, or one CTA a.rows
+// rows one after another (a.rows is 1 in clusters).  A segment comes in chunks through a ring in shared
 // memory: one warp starts asynchronous copies, into a slot as soon as all
 // computing warps have given it back, and so runs ahead into the next row
 // while this one's sums are joined, its alternatives selected or its gradient
@@ -655,10 +651,10 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     constexpr bool kEntropy = OP == kLogprobs;
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
-    __shared__ Exchange inbox[2][kMaxCluster], all;      // by the row's parity
+    __shared__ Exchange inbox[kMaxCluster], all;
     __shared__ bool heard;                               // of every CTA of the row
-    __shared__ volatile int gave_up;                     // on a copy or a slot of the ring
-    __shared__ __align__(8) uint64_t full_bar[kSlotsMost], empty_bar[kSlotsMost], inbox_bar[2];
+    __shared__ volatile int gave_up;                     // on a copy
+    __shared__ __align__(8) uint64_t full_bar[kSlotsMost], empty_bar[kSlotsMost], inbox_bar;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x % a.cluster);
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / a.cluster) * a.rows;
@@ -666,12 +662,11 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     uint4* ring = reinterpret_cast<uint4*>(dyn);
     const uint32_t full = tcdt::smem_addr(full_bar), empty = tcdt::smem_addr(empty_bar);
     // the teacher's entries: tokens (-1: padding, or another CTA's; -2 up to a multiple of 4), P_k (before
-    // that its logit), log P_k, the student's logits there
+    // that its logit), the student's logits there
     const int K4 = (a.K + 3) & ~3;
     int* tok = reinterpret_cast<int*>(ring + a.slots * kChunk);
     float* P = reinterpret_cast<float*>(tok + K4);
-    float* logP = P + K4;
-    float* zt = logP + K4;
+    float* zt = P + K4;
     TopState* top = reinterpret_cast<TopState*>(ring + a.slots * kChunk);
 
     if (tid == 0) {
@@ -679,7 +674,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             tcdt::mbar_init(full + 8 * i, 1);
             tcdt::mbar_init(empty + 8 * i, kWarps);
         }
-        for (int i = 0; i < 2; ++i) tcdt::mbar_init(tcdt::smem_addr(&inbox_bar[i]), static_cast<uint32_t>(a.cluster));
+        tcdt::mbar_init(tcdt::smem_addr(&inbox_bar), static_cast<uint32_t>(a.cluster));
         gave_up = 0;
         tcdt::fence_mbar_init();
     }
@@ -698,7 +693,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                 const int chunks = seg.chunks(), again = GRAD ? chunks - min(chunks, a.slots) : 0;
                 for (int i = 0; i < chunks + again; ++i) {
                     const int from = (i < chunks ? i : i - chunks) * kChunk;
-                    ok = wait_copy(empty + 8 * slot, parity, 3 * a.limit_ns(), &gave_up);
+                    ok = wait_slot(empty + 8 * slot, parity, 3 * a.limit_ns(), &gave_up);
                     if (!ok) break;
                     const uint32_t bytes = static_cast<uint32_t>(min(kChunk, seg.n - from)) * 16u;
                     tcdt::mbar_arrive_expect_tx(full + 8 * slot, bytes);
@@ -730,7 +725,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
 #ifdef TCDT_FAULT_INJECTION
         if (taken++ == a.fi_late_chunk && a.fi_here(rank) && (a.fi_late_warps >> warp & 1u)) late = true;
 #endif
-        if (!late && !wait_copy(full + 8 * slot, parity, a.limit_ns(), &gave_up)) late = true;
+        if (!late && !wait_limited(full + 8 * slot, parity, a.limit_ns())) late = true, gave_up = 1;
         const uint4* at = ring + slot * kChunk + tid;
         const bool inside = !late && (chunk + 1) * kChunk <= seg.n;
         if (inside) {
@@ -755,7 +750,6 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     for (int64_t r = row0; r < row1; ++r) {
         const Segment<E> seg(a.z, r * a.ld, a.V, rank, a.cluster, a.per);
         const int chunks = seg.chunks(), kept = GRAD ? min(chunks, a.slots) : 0;    // kept in the ring
-        const int turn = static_cast<int>(r - row0);
 
         // The given token, or the teacher's entries, and the elements beside
         // the vectors: asked for here, used once the first chunk is there.
@@ -878,7 +872,6 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                 for (int k = lane; k < a.K; k += 32) {
                     const float l = (P[k] - m) * a.c - log2_total, Pk = total != 0.f ? ex2(l) : 0.f;
                     P[k] = Pk;
-                    logP[k] = l * kLn2;
                     if (tok[k] >= 0 && !(Pk <= 0.f)) {
                         A = fmaf(Pk, l * kLn2 - (zt[k] - sm) * a.inv_t, A);
                         p += Pk;
@@ -892,27 +885,28 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             if (warp == 0) A = all.A, p = all.P;
         }
         if constexpr (TOP)
-            select_top<E>(*top, top->list[turn & 1], &top->count[turn & 1], seg, ordered(bucket_max), bucket_batch,
-                          bucket_second, a.top);
+            select_top<E>(*top, seg, ordered(bucket_max), bucket_batch, bucket_second, a.top);
         // The segments' statistics into every CTA's shared memory, lane i's
         // copy to CTA i, and the row's joined from them.
         if (warp == 0) {
             Exchange x{s, A, p};
             bool arrived = true;
             if (a.cluster > 1) {
-                const uint32_t bar = tcdt::smem_addr(&inbox_bar[turn & 1]);
+                const uint32_t bar = tcdt::smem_addr(&inbox_bar);
 #ifdef TCDT_FAULT_INJECTION
                 if (a.fi_silent && a.fi_here(rank)) {
                 } else
 #endif
                 if (lane < a.cluster) {
-                    const uint32_t to = tcdt::map_to_cta(tcdt::smem_addr(&inbox[turn & 1][rank]), static_cast<uint32_t>(lane));
+                    const uint32_t to = tcdt::map_to_cta(tcdt::smem_addr(&inbox[rank]), static_cast<uint32_t>(lane));
                     st_cluster_f32(to, x.s.m), st_cluster_f32(to + 4, x.s.S), st_cluster_f32(to + 8, x.s.U);
                     st_cluster_f32(to + 12, x.A), st_cluster_f32(to + 16, x.P);
                     tcdt::mbar_arrive_cluster(tcdt::map_to_cta(bar, static_cast<uint32_t>(lane)));
                 }
-                arrived = __all_sync(~0u, wait_cluster(bar, static_cast<uint32_t>(turn >> 1) & 1u, 2 * a.limit_ns()));
-                x = lane < a.cluster ? inbox[turn & 1][lane] : Exchange{empty_stats(), 0.f, 0.f};
+                // (a cluster's only row is phase 0; with the constant the compiler's arrangement of the whole
+                // kernel took 2048 x 65537 with gradient from 98.1 us to 99.1)
+                arrived = __all_sync(~0u, wait_cluster(bar, static_cast<uint32_t>(r - row0) & 1u, 2 * a.limit_ns()));
+                x = lane < a.cluster ? inbox[lane] : Exchange{empty_stats(), 0.f, 0.f};
                 s = warp_join<kEntropy>(x.s, kMaxCluster, a.c);
             }
             float l = 0.f, sum_P = 0.f;
@@ -924,7 +918,10 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             }
             if (!arrived) s.S = NAN, l = NAN;
             __syncwarp();
-            if (lane == 0) all = {s, l, sum_P}, heard = arrived;
+            if (lane == 0) {
+                all = {s, l, sum_P};
+                if constexpr (TOP) heard = arrived;
+            }
         }
         sync_threads();
         s = all.s;
@@ -1050,8 +1047,8 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                 // the segments' lists side by side; a key's place is its place in its own list and the
                 // number of larger keys in each of the others
                 const int n = a.top, lists = a.cluster;
-                const uint64_t* keys = top->list[turn & 1];
-                const int* count = &top->count[turn & 1];
+                const uint64_t* keys = top->list;
+                const int* count = &top->count;
                 int total = 0;
                 for (int o = 0; o < lists; ++o)
                     total += lists == 1 ? *count
@@ -1173,7 +1170,7 @@ gemm_status_t launch(Args a, int64_t T, int device, int sms, cudaStream_t stream
     // The ring takes what shared memory kCtas CTAs an SM leave.
     constexpr int kCtas = ctas_of(GRAD);
     const int64_t chunks = (a.V / Ele<E>::kPer + kChunk - 1) / kChunk;
-    const int64_t beside = TOP ? static_cast<int64_t>(sizeof(TopState)) : OP == kDistill ? (a.K + 3) / 4 * 64 : 0;
+    const int64_t beside = TOP ? static_cast<int64_t>(sizeof(TopState)) : OP == kDistill ? (a.K + 3) / 4 * 48 : 0;
     int64_t slots = (kSharedOfSm / kCtas - 2048 - beside) / (kChunk * 16);
     const int64_t ctas_at_once = static_cast<int64_t>(kCtas) * sms;
     // CTAs of a row.  A gradient's rows in flight, which it reads twice, are to
@@ -1195,7 +1192,7 @@ gemm_status_t launch(Args a, int64_t T, int device, int sms, cudaStream_t stream
     // Two rows one after another save a start where a row is short and the
     // CTAs are many (8192 x 8192 bf16 with gradient: 83 us with one, 74 with
     // two, 77 with four; 4096 x 131072 bf16, 64 alternatives: 217, 230, 241).
-    const int64_t rows = each <= 2 && T * cluster >= 8 * ctas_at_once ? 2 : 1;
+    const int64_t rows = cluster == 1 && each <= 2 && T >= 8 * ctas_at_once ? 2 : 1;
     if (slots > each * rows) slots = each * rows;
     if (slots > kSlotsMost) slots = kSlotsMost;
     a.T = T;
