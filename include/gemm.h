@@ -399,9 +399,15 @@ gemm_status_t gemm_schedule_model(int sm_count, gemm_dtype_t in_dtype, int64_t M
  * boundaries and lda and ldb are multiples of 16 (K may be anything); D needs
  * element alignment.
  *
- * The codes are multiplied as fp16 values with fp32 accumulation, so a sum is
- * exact while its partial sums stay below 2^24 in magnitude (always for
- * K <= 1040) and is rounded as an fp32 sum beyond; scales, bias and activation
+ * The codes are multiplied as fp16 values with fp32 accumulation: a sum is
+ * exact while its partial sums stay within 2^24 in magnitude (always for
+ * K <= 1024, with codes of -127..127 for K <= 1040).  Beyond, the tensor cores
+ * drop the bits that do not fit, toward zero, at every step of 16 codes:
+ * products that all have one sign came out smaller by up to 2^-19 of their sum
+ * at K = 2048, 2^-15.8 at 8192 and 2^-14.1 at 16384 (the tests allow
+ * K 2^-26).  Calls of few tokens (1 or 2, up to 8 with small weights) sum whole
+ * numbers for K < 2^17 and round once, so there a token's results may differ
+ * from those of the same token in a larger call.  Scales, bias and activation
  * are applied in fp32 and D is rounded once, to nearest even.
  *
  * Errors, streams and the plan's rules are gemm_run's; a plan of another input

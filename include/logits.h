@@ -74,9 +74,11 @@ gemm_status_t logits_logprobs(int device, gemm_dtype_t dtype, const void *logits
  * sum_i (g[i] logprob[i] + h[i] entropy[i]):
  *   dlogits[i * ldd + j] = (g (1[j = y] - p_j) - h p_j (log p_j + entropy)) / temperature,
  * its g terms left out where y is outside 0..V-1.  g or h may be NULL (zeros);
- * tokens may be NULL only with g.  The logits are read once and dlogits is
- * written once; dlogits may be the logits themselves (same pointer and
- * stride), and overlaps them in no other way. */
+ * tokens may be NULL only with g.  dlogits is written once; of the logits, what
+ * a row has beyond the 64 KB or less that each of its CTAs keeps on chip is read
+ * twice, the second time from L2 while the rows worked on at once fit it.  dlogits may be
+ * the logits themselves (same pointer and stride), and overlaps them in no
+ * other way. */
 gemm_status_t logits_logprobs_grad(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V,
                                    int64_t ld, const int64_t *tokens, float temperature, const float *g,
                                    const float *h, float *logprob, float *entropy, float *lse, void *dlogits,
@@ -100,8 +102,8 @@ gemm_status_t logits_distill(int device, gemm_dtype_t dtype, const void *logits,
 
 /* logits_distill, and the gradient for the logits of sum_i w[i] loss[i]:
  *   dlogits[i * ldd + j] = w temperature (Q_j - sum over k with token j of P_k),
- * zeros where the loss has no real entry.  In place as for
- * logits_logprobs_grad; the logits are read once. */
+ * zeros where the loss has no real entry.  Reads, and in place, as for
+ * logits_logprobs_grad. */
 gemm_status_t logits_distill_grad(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V,
                                   int64_t ld, int64_t K, const int64_t *teacher_tokens, gemm_dtype_t teacher_dtype,
                                   const void *teacher_logits, int64_t ldt, float temperature, const float *w,

@@ -149,9 +149,8 @@ def token_logprobs(logits, tokens=None, top: int = 0, *, temperature: float = 1.
 def token_logprobs_grad(logits, tokens=None, grad_logprob=None, grad_entropy=None, *, temperature: float = 1.0,
                         dlogits=None, stream=None) -> TokenLogprobsGrad:
     """token_logprobs without alternatives, and the gradient for the logits of
-    sum(grad_logprob * logprob + grad_entropy * entropy), one read of the
-    logits and one write of the gradient (logits_logprobs_grad).  dlogits may
-    be the logits themselves."""
+    sum(grad_logprob * logprob + grad_entropy * entropy), in one kernel
+    (logits_logprobs_grad).  dlogits may be the logits themselves."""
     import torch
     T, V, ld = _matrix(logits, "logits")
     dev = logits.device
@@ -204,9 +203,8 @@ def distill_topk(logits, teacher_tokens, teacher_logits, *, temperature: float =
 def distill_topk_grad(logits, teacher_tokens, teacher_logits, weight, *, temperature: float = 1.0, dlogits=None,
                       stream=None):
     """distill_topk's loss and the gradient for the logits of
-    sum(weight * loss), one read of the logits and one write of the gradient
-    (logits_distill_grad).  Returns (loss, dlogits); dlogits may be the logits
-    themselves."""
+    sum(weight * loss), in one kernel (logits_distill_grad).  Returns
+    (loss, dlogits); dlogits may be the logits themselves."""
     import torch
     T, V, ld = _matrix(logits, "logits")
     dev = logits.device
