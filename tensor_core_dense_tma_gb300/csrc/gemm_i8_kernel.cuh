@@ -1,5 +1,7 @@
-// gemm_i8_kernel.cuh -- the kernels of the 8-bit integer product for few
-// tokens: weights are read as 8-bit codes, once, and widened on chip.
+// gemm_i8_kernel.cuh -- the kernels of the 8-bit integer product that read the
+// weights as 8-bit codes and widen them on chip: dot products for a few tokens,
+// tiles on one CTA, tiles on CTA pairs.  A tile of tokens reads all weights, from
+// L2 where another one has just read them.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -628,8 +628,8 @@ __device__ __forceinline__ void select_top(TopState& t, const Segment<E>& seg, u
 }
 
 // A cluster of a.cluster CTAs computes a row, a segment each, or one CTA a.rows
-// rows one after another (a.rows is 1 in clusters).  A segment comes in chunks through a ring in shared
-// memory: one warp starts asynchronous copies, into a slot as soon as all
+// rows one after another (a.rows is 1 in clusters).  A segment comes in chunks
+// through a ring in shared memory: one warp starts asynchronous copies, into a slot as soon as all
 // computing warps have given it back, and so runs ahead into the next row
 // while this one's sums are joined, its alternatives selected or its gradient
 // written.  The gradient takes the last chunks first, where the statistics left
@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                     a.logprob[r] = token < 0 ? 0.f : nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
                 if (a.entropy) a.entropy[r] = entropy;
             } else {
-                a.loss[r] = a.t * a.t * all.A;
+                a.loss[r] = a.t * (a.t * all.A);      // t^2 itself may be 0
             }
         }
 
