@@ -78,7 +78,8 @@ gemm_status_t logits_logprobs(int device, gemm_dtype_t dtype, const void *logits
  * a row has beyond the 64 KB or less that each of its CTAs keeps on chip is read
  * twice, the second time from L2 while the rows worked on at once fit it.  dlogits may be
  * the logits themselves (same pointer and stride), and overlaps them in no
- * other way. */
+ * other way.  A row of dlogits that starts elsewhere within 16 bytes than its
+ * logits is stored element by element: right, and up to three times slower. */
 gemm_status_t logits_logprobs_grad(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V,
                                    int64_t ld, const int64_t *tokens, float temperature, const float *g,
                                    const float *h, float *logprob, float *entropy, float *lse, void *dlogits,

@@ -7,7 +7,10 @@ computation is one CUDA kernel per call on the given (or current) stream.
 
 ``logits`` is a T x V device tensor of fp32, fp16 or bf16 with unit column
 stride; rows may be padded (the product that feeds on a gradient wants row
-strides of whole 16 bytes, and an allocated gradient has them).
+strides of whole 16 bytes, and an allocated gradient has them).  Logits should
+have such rows too, or the gradient be given with the logits' stride: a gradient
+row that starts elsewhere within 16 bytes than its logits is stored element by
+element (2048 x 65537 bf16 282 us, with equal rows 96).
 
 What a call allocates belongs to torch's current stream; with another
 ``stream`` order the two, as for any tensor used on a second stream.
