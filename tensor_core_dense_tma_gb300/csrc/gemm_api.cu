@@ -492,13 +492,15 @@ gemm_status_t run_keep_nan(gemm_plan* plan, const void* A, const void* B, void* 
     }
     if (ch.kind != kCfgPair256) {
         // ReLU that keeps a NaN is built for this configuration, the choice of nine
-        // in ten of the sizes that come here
-        const int kind = plan->forced_kind, splits = plan->forced_splits;
+        // in ten of the sizes that come here; what the plan is pinned to is for others
+        const int kind = plan->forced_kind, splits = plan->forced_splits, division = plan->forced_division;
         plan->forced_kind = kCfgPair256;
         plan->forced_splits = 0;
+        plan->forced_division = GEMM_DIVISION_AUTO;
         ch = choose(plan, M, N, K, GEMM_F32, false, &valid);
         plan->forced_kind = kind;
         plan->forced_splits = splits;
+        plan->forced_division = division;
         if (!valid) return GEMM_ERR_UNSUPPORTED;
     }
     const Problem pr = make_problem(ch.swap, A, B, M, N, K, lda, ldb, GEMM_ROW_MAJOR, GEMM_COL_MAJOR, ep);

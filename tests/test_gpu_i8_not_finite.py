@@ -113,3 +113,27 @@ def test_activation_of_an_empty_sum_keeps_a_nan(plan, act):
     A, W = torch.zeros((5, 0), dtype=torch.int8, device="cuda"), torch.zeros((3, 0), dtype=torch.int8, device="cuda")
     D = plan.gemm_i8(A, W.t(), bias=bias, act=act)
     assert torch.isnan(D[:, 1]).all() and not torch.isnan(D[:, [0, 2]]).any()
+
+
+@pytest.mark.parametrize("M,N,K", [(4708, 8192, 2048), (4100, 4096, 2048), (1200, 16384, 4096)], ids=lambda v: str(v))
+def test_relu_on_a_pinned_plan(tc, M, N, K):
+    """Whatever a plan is pinned to, ReLU runs where no activation does."""
+    A, _ = codes(M, K, 3)
+    W, _ = codes(N, K, 4)
+    scale = torch.full((M,), 1e-3, device="cuda")
+    ran = 0
+    with tc.Plan("f16", 0) as plan:
+        for config in ("auto", "single_128x256", "pair_256x224", "pair_256x256"):
+            for division in ("auto", "whole", "split", "early_split", "halves", "stream_k"):
+                plan.force_config(config)
+                plan.force_division(division)
+                try:
+                    want = plan.gemm_i8(A, W.t(), row_scale=scale)
+                except tc.GemmError as e:
+                    assert e.status == 2
+                    continue
+                ran += 1
+                assert torch.equal(plan.gemm_i8(A, W.t(), row_scale=scale, act="relu"), want.clamp(min=0))
+        torch.cuda.synchronize()
+        assert plan.device_status() == 0
+    assert ran > 8
