@@ -7,6 +7,11 @@
  *   logits_logprobs_grad  the first three, and the gradient for the logits
  *   logits_distill        distillation loss against a teacher's top logits
  *   logits_distill_grad   that, and the gradient for the logits
+ *   logits_policy         clipped policy loss of given tokens, with a KL term
+ *                         and an entropy bonus
+ *   logits_policy_grad    that, and the gradient for the logits
+ *   logits_preference     preference loss of paired sequences
+ *   logits_preference_grad  that, and the gradient for the logits
  *
  * The logits are T rows of V values, row-major, element (i, j) at
  * [i * ld + j], ld >= V, of type GEMM_F32, GEMM_F16 or GEMM_BF16; nothing
@@ -23,7 +28,8 @@
  *
  * Memory and streams.  All pointers are DEVICE pointers owned by the caller
  * and aligned to their element; nothing is kept after a call returns, there
- * is no workspace and no allocation.  A call launches one kernel on `stream`
+ * is no workspace (but what logits_preference_grad is given) and no allocation.
+ * A call launches one kernel (a preference loss two, with gradient three) on `stream`
  * (a cudaStream_t; NULL = the legacy default stream) of `device` (a CUDA
  * ordinal, made current while the call runs and then restored) and
  * synchronises nothing, so it may be captured in a graph.  Calls are
@@ -109,6 +115,80 @@ gemm_status_t logits_distill_grad(int device, gemm_dtype_t dtype, const void *lo
                                   int64_t ld, int64_t K, const int64_t *teacher_tokens, gemm_dtype_t teacher_dtype,
                                   const void *teacher_logits, int64_t ldt, float temperature, const float *w,
                                   float *loss, float *lse, void *dlogits, int64_t ldd, void *stream);
+
+/* Clipped policy loss.  Row i, with y = tokens[i], logprob = x_y - lse, the
+ * log-probability old_logprob[i] of y under the policy that sampled it and
+ * r = exp(logprob - old_logprob), has
+ *   loss[i] = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *             + kl_coef kl[i] - entropy_bonus entropy[i],   A = advantage[i],
+ *   kl[i]   = exp(d) - 1 - d,  d = ref_logprob[i] - logprob
+ *             (an estimate of the divergence from the reference policy that is
+ *             never negative; 0 where ref_logprob is NULL),
+ *   entropy[i] = -sum_j p_j log p_j.
+ * A row with y outside 0..V-1 (a prompt's, padding: say -1) has zeros for all
+ * of them and its logits are not read.  A masked token (logit -inf) has
+ * logprob -inf and r = 0.  logprob, kl and entropy may be NULL. */
+typedef struct {
+    const float *old_logprob;  /* [T] */
+    const float *advantage;    /* [T] */
+    const float *ref_logprob;  /* [T], or NULL with kl_coef 0 */
+    float clip_low;            /* 0..1 */
+    float clip_high;           /* 0 or more, finite */
+    float kl_coef;             /* finite */
+    float entropy_bonus;       /* finite */
+} logits_policy_t;
+
+gemm_status_t logits_policy(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V, int64_t ld,
+                            const int64_t *tokens, float temperature, const logits_policy_t *policy, float *loss,
+                            float *logprob, float *kl, float *entropy, void *stream);
+
+/* logits_policy, and the gradient for the logits of sum_i w[i] loss[i]:
+ *   dlogits[i * ldd + j] = w (g (1[j = y] - p_j) + entropy_bonus p_j (log p_j + entropy)) / temperature,
+ *   g = (r A <= clip(r) A ? -r A : 0) + kl_coef (1 - exp(d)).
+ * Rows without a token and rows of weight 0 have zeros, whatever they hold.
+ * Reads, and in place, as for logits_logprobs_grad. */
+gemm_status_t logits_policy_grad(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V, int64_t ld,
+                                 const int64_t *tokens, float temperature, const logits_policy_t *policy,
+                                 const float *w, float *loss, float *logprob, float *kl, float *entropy, void *dlogits,
+                                 int64_t ldd, void *stream);
+
+/* Preference loss of pairs of sequences.  Sequence s = 0 .. 2 pairs - 1 has the
+ * rows offsets[s] .. offsets[s + 1] - 1 (offsets has 2 pairs + 1 entries that
+ * do not decrease, within 0..T; others are cut off at 0 and T, and what no
+ * sequence or more than one would hold is then undefined).  Rows outside
+ * all sequences belong to no pair.  With logprob[i] of tokens[i] as above (0
+ * where it is outside 0..V-1: such a row, say a prompt's, is not read and counts
+ * for nothing),
+ *   reward[s] = beta sum_{i in s} (logprob[i] - ref_logprob[i]),
+ *   m = reward[2 q] - reward[2 q + 1],
+ *   loss[q] = -(1 - smoothing) log sigma(m) - smoothing log sigma(-m),
+ * sigma(m) = 1 / (1 + exp(-m)): sequence 2 q is the preferred one of pair q.
+ * Sums over rows are 64-bit.  A sequence without rows has reward 0; ref_logprob
+ * may be NULL (zeros).  logprob is written for all T rows. */
+typedef struct {
+    const int64_t *offsets;    /* [2 pairs + 1] */
+    int64_t pairs;
+    const float *ref_logprob;  /* [T], or NULL */
+    float beta;                /* finite */
+    float smoothing;           /* 0..1 */
+} logits_preference_t;
+
+gemm_status_t logits_preference(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V, int64_t ld,
+                                const int64_t *tokens, float temperature, const logits_preference_t *preference,
+                                float *loss, float *reward, float *logprob, void *stream);
+
+/* logits_preference, and the gradient for the logits of sum_q w[q] loss[q]:
+ *   dlogits[i * ldd + j] = g (1[j = y] - p_j) / temperature,
+ *   g = +-w beta (smoothing sigma(m) - (1 - smoothing) sigma(-m)), + in sequence 2 q.
+ * Rows without a token, in no sequence or in a pair of weight 0 have zeros,
+ * whatever they hold.  The logits of the others are read twice.  dlogits may be the logits
+ * themselves, as for logits_logprobs_grad.  work: 16 T bytes of the caller's,
+ * 16-byte aligned, this call's alone until it has ended. */
+gemm_status_t logits_preference_grad(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V,
+                                     int64_t ld, const int64_t *tokens, float temperature,
+                                     const logits_preference_t *preference, const float *w, float *loss,
+                                     float *reward, float *logprob, void *dlogits, int64_t ldd, void *work,
+                                     void *stream);
 
 #ifdef __cplusplus
 }

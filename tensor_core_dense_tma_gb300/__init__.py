@@ -39,7 +39,8 @@ __all__ = [
     "gemm_plan_host_trace", "gemm_plan_host_trace_read",
     "gemm_run_i8", "gemm_run_i8_dynamic", "gemm_quantize_rows_i8", "quantize_rows_i8",
     "token_logprobs", "token_logprobs_grad", "distill_topk", "distill_topk_grad", "TokenLogprobs",
-    "TokenLogprobsGrad",
+    "TokenLogprobsGrad", "policy_loss", "policy_loss_grad", "PolicyLoss", "PolicyLossGrad",
+    "preference_loss", "preference_loss_grad", "PreferenceLoss", "PreferenceLossGrad",
 ]
 
 STATUS = {
@@ -820,3 +821,7 @@ class Plan:
 TokenLogprobs, TokenLogprobsGrad = _logits.TokenLogprobs, _logits.TokenLogprobsGrad
 token_logprobs, token_logprobs_grad = _logits.token_logprobs, _logits.token_logprobs_grad
 distill_topk, distill_topk_grad = _logits.distill_topk, _logits.distill_topk_grad
+policy_loss, policy_loss_grad = _logits.policy_loss, _logits.policy_loss_grad
+PolicyLoss, PolicyLossGrad = _logits.PolicyLoss, _logits.PolicyLossGrad
+preference_loss, preference_loss_grad = _logits.preference_loss, _logits.preference_loss_grad
+PreferenceLoss, PreferenceLossGrad = _logits.PreferenceLoss, _logits.PreferenceLossGrad

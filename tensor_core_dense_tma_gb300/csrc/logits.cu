@@ -1,6 +1,7 @@
 // logits.cu -- operators on the rows of a logits matrix (include/logits.h):
 // token log-probabilities with entropy and top alternatives, distillation
-// from a teacher's top logits, and the gradients of both.
+// from a teacher's top logits, a clipped policy loss, a preference loss of paired
+// sequences, and the gradients of the four.
 //
 // Mathematics.  With c = log2(e) / temperature and a running maximum m of the
 // row's logits z, one pass keeps
@@ -55,7 +56,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kMaxExtent = 0x7FFFFFFF - 4096;
 
 // operator and outputs of an instantiation
-constexpr int kLogprobs = 0, kDistill = 1;
+constexpr int kLogprobs = 0, kDistill = 1, kPolicy = 2, kScore = 3;   // kScore: the rows of a preference loss
+
+struct __align__(16) RowState {
+    float m, log2_S, g, unused;       // log2_S is +inf where the row's gradient is 0 whatever g is
+};
 
 struct Args {
     const void* z;
@@ -79,9 +84,17 @@ struct Args {
     int64_t ldt;
     const void* teacher;
     int teacher_type;
-    const float* w;
+    const float* w;      // and of a policy loss
     float* loss;
-    // both
+    // policy loss: e^(logprob - old) is clipped to lo..hi
+    const float* old_logprob;
+    const float* advantage;
+    const float* ref_logprob;
+    float* kl;
+    float lo, hi, kl_coef, bonus;
+    // preference loss: (maximum, log2 S, gradient of the loss for logprob) of each row
+    RowState* state;
+    // all
     float* lse;
     void* dz;
     int64_t ldd;
@@ -149,6 +162,10 @@ __device__ __forceinline__ bool wait_slot(uint32_t bar, uint32_t parity, uint64_
         if (*gave_up || tcdt::globaltimer_ns() - t0 > limit_ns) return false;
     return true;
 }
+
+// Waits for the kernel before this one in the stream, where this one was
+// launched dependent on it.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Two 32-bit values as a register pair.
 __device__ __forceinline__ uint64_t bit_pair(uint32_t x, uint32_t y) {
@@ -447,6 +464,27 @@ __device__ __forceinline__ float teacher_value(const void* p, int type, int64_t 
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
 }
 
+// Policy loss of a row without its entropy bonus, its KL term and the loss's
+// derivative with respect to the log-probability.  With d = ref - logprob the
+// KL term is e^d - 1 - d >= 0, from expm1: for small d it is d^2 / 2, of which
+// e^d in fp32 would keep nothing.  A NaN is not lost in the minimum.
+struct PolicyLoss {
+    float loss, kl, slope;
+};
+
+__device__ __forceinline__ PolicyLoss policy_loss(const Args& a, int64_t r, float logprob) {
+    const float A = a.advantage[r], ratio = expf(logprob - a.old_logprob[r]);
+    const float free = ratio * A, bounded = fminf(fmaxf(ratio, a.lo), a.hi) * A;
+    PolicyLoss l{-bounded, 0.f, 0.f};
+    if (!(free > bounded)) l.loss = l.slope = -free;
+    if (a.ref_logprob) {
+        const float d = a.ref_logprob[r] - logprob, e = expm1f(d);
+        l.kl = e == INFINITY ? e : e - d;
+        if (a.kl_coef != 0.f) l.loss = fmaf(a.kl_coef, l.kl, l.loss), l.slope = fmaf(-a.kl_coef, e, l.slope);
+    }
+    return l;
+}
+
 // What a CTA of a row tells the others: its statistics, and its part of a
 // distillation loss, sum P_k (log P_k - (z_k - m) / temperature) and sum P_k
 // over the tokens in its segment.
@@ -648,7 +686,7 @@ __device__ __forceinline__ void select_top(TopState& t, const Segment<E>& seg, u
 template <typename E, int OP, bool GRAD, bool TOP>
 __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args a) {
     constexpr int kPer = Ele<E>::kPer;
-    constexpr bool kEntropy = OP == kLogprobs;
+    constexpr bool kEntropy = OP == kLogprobs || OP == kPolicy;
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
     __shared__ Exchange inbox[kMaxCluster], all;
@@ -668,6 +706,18 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     float* P = reinterpret_cast<float*>(tok + K4);
     float* zt = P + K4;
     TopState* top = reinterpret_cast<TopState*>(ring + a.slots * kChunk);
+
+    // Rows of a policy or preference loss without a token are not read: all of theirs
+    // is 0.  Those of weight 0 have a gradient of zeros, whatever they hold.
+    auto unread = [&](int64_t r) {
+        if constexpr (OP != kPolicy && OP != kScore) return false;
+        const int64_t y = a.tokens[r];
+        return y < 0 || y >= a.V;
+    };
+    auto weightless = [&](int64_t r) {
+        if constexpr (OP != kPolicy) return false;
+        return a.w[r] == 0.f;
+    };
 
     if (tid == 0) {
         for (int i = 0; i < a.slots; ++i) {
@@ -689,8 +739,9 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             uint32_t parity = 1;            // an empty ring's slots count as given back
             bool ok = true;
             for (int64_t r = row0; ok && r < row1; ++r) {
+                if (unread(r)) continue;
                 const Segment<E> seg(a.z, r * a.ld, a.V, rank, a.cluster, a.per);
-                const int chunks = seg.chunks(), again = GRAD ? chunks - min(chunks, a.slots) : 0;
+                const int chunks = seg.chunks(), again = GRAD && !weightless(r) ? chunks - min(chunks, a.slots) : 0;
                 for (int i = 0; i < chunks + again; ++i) {
                     const int from = (i < chunks ? i : i - chunks) * kChunk;
                     ok = wait_slot(empty + 8 * slot, parity, 3 * a.limit_ns(), &gave_up);
@@ -750,6 +801,31 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     for (int64_t r = row0; r < row1; ++r) {
         const Segment<E> seg(a.z, r * a.ld, a.V, rank, a.cluster, a.per);
         const int chunks = seg.chunks(), kept = GRAD ? min(chunks, a.slots) : 0;    // kept in the ring
+        // the segment's part of a gradient of zeros
+        auto store_zeros = [&](E* out) {
+            const bool whole = (reinterpret_cast<uintptr_t>(out + seg.first) & 15) == 0;
+            const E zero = Ele<E>::round(0.f);
+            if (whole)
+                for (int v = tid; v < seg.n; v += kThreads)
+                    __stcs(reinterpret_cast<uint4*>(out + seg.first) + v, make_uint4(0u, 0u, 0u, 0u));
+            else
+                for (int64_t i = tid; i < static_cast<int64_t>(seg.n) * kPer; i += kThreads) out[seg.first + i] = zero;
+            if (tid < seg.head) out[tid] = zero;
+            if (tid < seg.tail) out[seg.after + tid] = zero;
+        };
+        if constexpr (OP == kPolicy || OP == kScore) {
+            if (unread(r)) {
+                if (rank == 0 && tid == 0) {
+                    if constexpr (OP == kPolicy) a.loss[r] = 0.f;
+                    else if (a.state) a.state[r] = {0.f, INFINITY, 0.f, 0.f};
+                    if (a.logprob) a.logprob[r] = 0.f;
+                    if (a.entropy) a.entropy[r] = 0.f;
+                    if (a.kl) a.kl[r] = 0.f;
+                }
+                if constexpr (GRAD) store_zeros(static_cast<E*>(a.dz) + r * a.ldd);
+                continue;
+            }
+        }
 
         // The given token, or the teacher's entries, and the elements beside
         // the vectors: asked for here, used once the first chunk is there.
@@ -757,7 +833,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         int64_t y[kEntries] = {};
         int token = -1;
         float z_token = 0.f;
-        if constexpr (OP == kLogprobs) {
+        if constexpr (OP != kDistill) {
             y[0] = a.tokens ? a.tokens[r] : -1;
         } else {
 #pragma unroll
@@ -772,7 +848,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         const float x_head = tid < seg.head ? Ele<E>::load(seg.row + tid) : -INFINITY;
         const float x_tail = tid < seg.tail ? Ele<E>::load(seg.row + seg.after + tid) : -INFINITY;
         auto given = [&] {
-            if constexpr (OP == kLogprobs) {
+            if constexpr (OP != kDistill) {
                 if (y[0] >= 0 && y[0] < a.V) {
                     token = static_cast<int>(y[0]);
                     z_token = Ele<E>::load(seg.row + token);
@@ -929,12 +1005,24 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         const bool nothing = s.S == 0.f;
         const float log2_S = lg2(s.S);
         const float entropy = nothing ? 0.f : kLn2 * (log2_S - s.U / s.S);
+        PolicyLoss policy{};
+        if constexpr (OP == kPolicy) {
+            const float logprob = nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
+            policy = policy_loss(a, r, logprob);
+            if (a.bonus != 0.f) policy.loss = fmaf(-a.bonus, entropy, policy.loss);
+        }
         if (rank == 0 && tid == 0) {
             if (a.lse) a.lse[r] = nothing ? -INFINITY : fmaf(s.m, a.inv_t, kLn2 * log2_S);
-            if constexpr (OP == kLogprobs) {
+            if constexpr (OP != kDistill) {
                 if (a.logprob)
                     a.logprob[r] = token < 0 ? 0.f : nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
-                if (a.entropy) a.entropy[r] = entropy;
+                if (kEntropy && a.entropy) a.entropy[r] = entropy;
+                if constexpr (OP == kPolicy) {
+                    a.loss[r] = policy.loss;
+                    if (a.kl) a.kl[r] = policy.kl;
+                }
+                if constexpr (OP == kScore)
+                    if (a.state) a.state[r] = {s.m, nothing ? INFINITY : log2_S, 0.f, 0.f};
             } else {
                 a.loss[r] = a.t * (a.t * all.A);      // t^2 itself may be 0
             }
@@ -943,8 +1031,16 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         if constexpr (GRAD) {
             // p_j (ga + gb log2 p_j), and the given tokens' terms put in at the end
             float ga, gb = 0.f, g_token;
-            if constexpr (OP == kLogprobs) {
-                const float g = token >= 0 && a.g ? a.g[r] : 0.f, h = a.h ? a.h[r] : 0.f;
+            if constexpr (OP != kDistill) {
+                float g, h;
+                if constexpr (OP == kPolicy) {
+                    const float w = a.w[r];
+                    g = w * policy.slope;
+                    h = a.bonus != 0.f ? -a.bonus * w : 0.f;
+                } else {
+                    g = token >= 0 && a.g ? a.g[r] : 0.f;
+                    h = a.h ? a.h[r] : 0.f;
+                }
                 ga = -a.inv_t * fmaf(h, entropy, g);
                 gb = -a.inv_t * h * kLn2;
                 g_token = a.inv_t * g;
@@ -961,14 +1057,22 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             auto gradient = [&](uint64_t x2) {
                 uint64_t l2 = fma2(add2(x2, m2), c2, shift2);
                 uint64_t g2 = ga2;
-                if constexpr (OP == kLogprobs) {
+                if constexpr (OP != kDistill) {
                     l2 = max_nan2(l2, -200.f);
                     g2 = fma2(gb2, l2, ga2);
                 }
                 return mul2(ex2_2(l2), g2);
             };
             if ((slot -= kept) < 0) slot += a.slots, parity ^= 1u;
-            for (int i = 0; i < chunks; ++i) {
+            const bool zeros = weightless(r);
+            if (zeros) {
+                for (int i = 0; i < kept; ++i) {
+                    uint4 q[kUnroll];
+                    take(seg, chunks - kept + i, true, q);
+                }
+                store_zeros(out);
+            }
+            for (int i = 0; i < chunks && !zeros; ++i) {
                 const int b = i < kept ? chunks - kept + i : i - kept;
                 uint4 q[kUnroll];
                 const bool inside = take(seg, b, true, q);
@@ -1006,15 +1110,15 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                     }
                 }
             }
-            if (tid < kPer) {
+            if (tid < kPer && !zeros) {
                 float x0, x1;
                 unpair(gradient(pair(x_head, x_tail)), x0, x1);
                 if (tid < seg.head) out[tid] = Ele<E>::round(x0);
                 if (tid < seg.tail) out[seg.after + tid] = Ele<E>::round(x1);
             }
             sync_threads();
-            if constexpr (OP == kLogprobs) {
-                if (tid == 0 && token >= 0 && !nothing && seg.holds(token)) {
+            if constexpr (OP != kDistill) {
+                if (tid == 0 && token >= 0 && !nothing && !zeros && seg.holds(token)) {
                     const float l = max_nan((z_token - s.m) * a.c - log2_S, -200.f);
                     out[token] = Ele<E>::round(fmaf(ex2(l), fmaf(gb, l, ga), g_token));
                 }
@@ -1093,6 +1197,147 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     // nobody leaves while its shared memory may still be read
     __syncwarp();
     if (a.cluster > 1) tcdt::cluster_sync_all();
+}
+
+// ---- preference loss ---------------------------------------------------------
+// The rows' log-probabilities and statistics (rows_kernel), then the pairs, then
+// the gradient: a row's factor depends on all rows of its pair, so its logits are
+// read a second time.  The gradient goes through the rows from the last one to
+// the first: what the statistics read last is then still in L2.
+struct Pairs {
+    const int64_t* offsets;           // [2 pairs + 1]
+    const float* ref;                 // [T] or null
+    const float* logprob;             // [T]
+    const int64_t* tokens;            // [T]
+    const float* w;                   // [pairs] or null
+    int64_t T;
+    int32_t V;
+    float beta, smoothing;
+    float* loss;                      // [pairs]
+    float* reward;                    // [2 pairs]
+    RowState* state;                  // [T]
+};
+
+constexpr int kPairThreads = 512;
+
+// One CTA a pair.  Sums of a few thousand log-probabilities are kept in 64 bits:
+// their difference is what counts.  The order of the additions is fixed.
+__global__ void __launch_bounds__(kPairThreads) pairs_kernel(const Pairs a) {
+    __shared__ double part[2][kPairThreads / 32];
+    __shared__ float slope[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t pair = blockIdx.x;
+    int64_t at[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) at[i] = min(max(a.offsets[2 * pair + i], int64_t(0)), a.T);
+    grid_wait();                      // the rows' log-probabilities are there
+    auto scored = [&](int64_t r) {
+        const int64_t y = a.tokens[r];
+        return y >= 0 && y < a.V;
+    };
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        double sum = 0;
+        for (int64_t r = at[side] + tid; r < at[side + 1]; r += kPairThreads)
+            if (scored(r)) sum += static_cast<double>(a.logprob[r]) - (a.ref ? static_cast<double>(a.ref[r]) : 0.0);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) part[side][warp] = sum;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        double reward[2] = {};
+        for (int side = 0; side < 2; ++side) {
+            for (int w = 0; w < kPairThreads / 32; ++w) reward[side] += part[side][w];
+            reward[side] *= a.beta;
+            a.reward[2 * pair + side] = static_cast<float>(reward[side]);
+        }
+        // -log sigma(m) = log1p(e^-|m|) + max(-m, 0), sigma from the same exponential
+        const double m = reward[0] - reward[1], e = a.smoothing;
+        const double x = exp(-fabs(m)), l = log1p(x);
+        const double less = x / (1 + x), more = 1 / (1 + x);
+        const double right = e == 1 ? 0 : (1 - e) * (l + (m < 0 ? -m : 0)), wrong = e == 0 ? 0 : e * (l + (m > 0 ? m : 0));
+        a.loss[pair] = static_cast<float>(m != m ? m : right + wrong);
+        if (a.w) {
+            const double d = e * (m < 0 ? less : more) - (1 - e) * (m < 0 ? more : less);
+            const float g = a.w[pair] == 0.f ? 0.f : static_cast<float>(d * a.beta * a.w[pair]);
+            slope[0] = g, slope[1] = -g;
+        }
+    }
+    if (!a.w) return;
+    __syncthreads();
+    for (int side = 0; side < 2; ++side)
+        for (int64_t r = at[side] + tid; r < at[side + 1]; r += kPairThreads) a.state[r].g = slope[side];
+}
+
+constexpr int kGradThreads = 256, kGradUnroll = 4;
+constexpr int kGradVectors = kGradThreads * kGradUnroll * 4;     // of a CTA: 64 KB
+
+// dlogits of a part of a row, g (1[j = y] - p_j) / temperature.
+template <typename E>
+__global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const Args a, int parts) {
+    constexpr int kPer = Ele<E>::kPer;
+    const int tid = threadIdx.x;
+    const int64_t r = a.T - 1 - static_cast<int64_t>(blockIdx.x) / parts;
+    const int part = static_cast<int>(blockIdx.x % parts);
+    const Segment<E> seg(a.z, r * a.ld, a.V, part, parts, kGradVectors);
+    E* out = static_cast<E*>(a.dz) + r * a.ldd;
+    const bool whole = (reinterpret_cast<uintptr_t>(out + seg.first) & 15) == 0;
+    grid_wait();
+    const RowState s = a.state[r];
+    const bool zeros = s.g == 0.f || s.log2_S == INFINITY;
+    const int64_t y = a.tokens[r];
+    const float g = s.g * a.inv_t, shift = s.log2_S;
+    auto p = [&](float z) { return ex2(fmaf(z - s.m, a.c, -shift)); };
+    auto value = [&](float z, int j) { return zeros ? 0.f : j == y ? fmaf(-g, p(z), g) : -g * p(z); };
+    const uint64_t c2 = pair(a.c, a.c), m2 = pair(-s.m, -s.m), shift2 = pair(-shift, -shift), g2 = pair(-g, -g);
+    for (int v0 = tid; v0 < seg.n; v0 += kGradThreads * kGradUnroll) {
+        uint4 q[kGradUnroll];
+        if (!zeros) {
+#pragma unroll
+            for (int k = 0; k < kGradUnroll; ++k)
+                if (v0 + k * kGradThreads < seg.n) q[k] = seg.load(v0 + k * kGradThreads);
+        }
+#pragma unroll
+        for (int k = 0; k < kGradUnroll; ++k) {
+            const int v = v0 + k * kGradThreads;
+            if (v >= seg.n) continue;
+            uint64_t x[kPer / 2];
+            if (zeros) {
+#pragma unroll
+                for (int e = 0; e < kPer / 2; ++e) x[e] = 0;
+            } else {
+                Ele<E>::pairs(q[k], x);
+#pragma unroll
+                for (int e = 0; e < kPer / 2; ++e) x[e] = mul2(ex2_2(fma2(add2(x[e], m2), c2, shift2)), g2);
+                const int64_t j = y - (seg.first + static_cast<int64_t>(v) * kPer);
+                if (j >= 0 && j < kPer) {
+#pragma unroll
+                    for (int e = 0; e < kPer / 2; ++e) {
+                        float lo, hi;
+                        unpair(x[e], lo, hi);
+                        x[e] = pair(j == 2 * e ? lo + g : lo, j == 2 * e + 1 ? hi + g : hi);
+                    }
+                }
+            }
+            if (whole) {
+                __stcs(reinterpret_cast<uint4*>(out + seg.first) + v, Ele<E>::pack_pairs(x));
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer / 2; ++e) {
+                    float lo, hi;
+                    unpair(x[e], lo, hi);
+                    E* to = out + seg.first + static_cast<int64_t>(v) * kPer + 2 * e;
+                    to[0] = Ele<E>::round(lo), to[1] = Ele<E>::round(hi);
+                }
+            }
+        }
+    }
+    if (tid < seg.head) out[tid] = Ele<E>::round(value(zeros ? 0.f : Ele<E>::load(seg.row + tid), tid));
+    if (tid < seg.tail) {
+        const int j = seg.after + tid;
+        out[j] = Ele<E>::round(value(zeros ? 0.f : Ele<E>::load(seg.row + j), j));
+    }
 }
 
 bool float_type(gemm_dtype_t d) { return d == GEMM_F32 || d == GEMM_F16 || d == GEMM_BF16; }
@@ -1288,6 +1533,116 @@ void fill_distill(Args& a, int64_t K, const int64_t* teacher_tokens, gemm_dtype_
     a.lse = lse;
 }
 
+gemm_status_t check_preference(gemm_dtype_t dtype, const void* logits, int64_t T, int64_t V, int64_t ld,
+                               const int64_t* tokens, float temperature, const logits_preference_t* preference,
+                               const float* loss, const float* reward, const float* logprob) {
+    const gemm_status_t st = check_rows(dtype, logits, T, V, ld, temperature);
+    if (st != GEMM_OK) return st;
+    if (!preference) return GEMM_ERR_INVALID_ARG;
+    const logits_preference_t& q = *preference;
+    if (q.pairs < 0 || !std::isfinite(q.beta) || !(q.smoothing >= 0.f && q.smoothing <= 1.f)) return GEMM_ERR_INVALID_ARG;
+    if (q.pairs > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
+    if (q.pairs > 0 && (!q.offsets || !loss || !reward)) return GEMM_ERR_INVALID_ARG;
+    if (T > 0 && (!tokens || !logprob)) return GEMM_ERR_INVALID_ARG;
+    if (!aligned(tokens, 8) || !aligned(q.offsets, 8) || !aligned(q.ref_logprob, 4) || !aligned(loss, 4) ||
+        !aligned(reward, 4) || !aligned(logprob, 4))
+        return GEMM_ERR_MISALIGNED;
+    return GEMM_OK;
+}
+
+// A kernel that may start while the one before it in the stream ends (it waits
+// for it itself, see grid_wait).
+template <typename... P, typename... A>
+gemm_status_t launch_dependent(void (*kernel)(P...), unsigned ctas, unsigned threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
+template <typename E>
+gemm_status_t launch_score_grad(const Args& a, cudaStream_t stream) {
+    const int64_t vectors = a.V / Ele<E>::kPer;
+    const int64_t parts = vectors > 0 ? (vectors + kGradVectors - 1) / kGradVectors : 1;
+    if (parts * a.T > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;
+    return launch_dependent(score_grad_kernel<E>, static_cast<unsigned>(parts * a.T), kGradThreads, stream, a,
+                            static_cast<int>(parts));
+}
+
+// a.dz null: without the gradient.
+gemm_status_t run_preference(int device, gemm_dtype_t dtype, Args a, int64_t T, const logits_preference_t& q,
+                             const float* w, float* reward, void* stream) {
+    if (T == 0 && q.pairs == 0) return GEMM_OK;
+    int sms = 0;
+    gemm_status_t st = sms_of(device, &sms);
+    if (st != GEMM_OK) return st;
+    const OnDevice on(device);
+    if (!on.ok) return GEMM_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.T = T;
+    // refused before anything is launched
+    if (a.dz && a.V > 0 && T * ((a.V / 4 + kGradVectors - 1) / kGradVectors + 1) > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;
+    st = launch_type<kScore, false, false>(device, dtype, a, T, stream);
+    if (st == GEMM_OK && q.pairs > 0) {
+        Pairs p{q.offsets, q.ref_logprob, a.logprob, a.tokens, w, T, a.V, q.beta, q.smoothing, a.loss, reward, a.state};
+        st = launch_dependent(pairs_kernel, static_cast<unsigned>(q.pairs), kPairThreads, s, p);
+    }
+    if (st != GEMM_OK || !a.dz || T == 0) return st;
+    if (dtype == GEMM_F32) return launch_score_grad<float>(a, s);
+    if (dtype == GEMM_F16) return launch_score_grad<__half>(a, s);
+    return launch_score_grad<__nv_bfloat16>(a, s);
+}
+
+void fill_preference(Args& a, const int64_t* tokens, float* loss, float* logprob) {
+    a.tokens = tokens;
+    a.loss = loss;
+    a.logprob = logprob;
+}
+
+gemm_status_t check_policy(gemm_dtype_t dtype, const void* logits, int64_t T, int64_t V, int64_t ld,
+                           const int64_t* tokens, float temperature, const logits_policy_t* policy,
+                           const float* loss, const float* logprob, const float* kl, const float* entropy) {
+    const gemm_status_t st = check_rows(dtype, logits, T, V, ld, temperature);
+    if (st != GEMM_OK) return st;
+    if (!policy) return GEMM_ERR_INVALID_ARG;
+    const logits_policy_t& q = *policy;
+    if (!(q.clip_low >= 0.f && q.clip_low <= 1.f) || !(q.clip_high >= 0.f) || !std::isfinite(q.clip_high) ||
+        !std::isfinite(q.kl_coef) || !std::isfinite(q.entropy_bonus))
+        return GEMM_ERR_INVALID_ARG;
+    if (q.kl_coef != 0.f && !q.ref_logprob) return GEMM_ERR_INVALID_ARG;
+    if (T > 0 && (!tokens || !q.old_logprob || !q.advantage || !loss)) return GEMM_ERR_INVALID_ARG;
+    if (!aligned(tokens, 8) || !aligned(q.old_logprob, 4) || !aligned(q.advantage, 4) || !aligned(q.ref_logprob, 4) ||
+        !aligned(loss, 4) || !aligned(logprob, 4) || !aligned(kl, 4) || !aligned(entropy, 4))
+        return GEMM_ERR_MISALIGNED;
+    return GEMM_OK;
+}
+
+void fill_policy(Args& a, const int64_t* tokens, const logits_policy_t& q, float* loss, float* logprob, float* kl,
+                 float* entropy) {
+    a.tokens = tokens;
+    a.old_logprob = q.old_logprob;
+    a.advantage = q.advantage;
+    a.ref_logprob = q.ref_logprob;
+    a.lo = 1.0f - q.clip_low;
+    a.hi = 1.0f + q.clip_high;
+    a.kl_coef = q.kl_coef;
+    a.bonus = q.entropy_bonus;
+    a.loss = loss;
+    a.logprob = logprob;
+    a.kl = kl;
+    a.entropy = entropy;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1369,6 +1724,66 @@ gemm_status_t logits_distill_grad(int device, gemm_dtype_t dtype, const void* lo
     a.dz = dlogits;
     a.ldd = ldd;
     return launch_type<kDistill, true, false>(device, dtype, a, T, stream);
+}
+
+gemm_status_t logits_policy(int device, gemm_dtype_t dtype, const void* logits, int64_t T, int64_t V, int64_t ld,
+                            const int64_t* tokens, float temperature, const logits_policy_t* policy, float* loss,
+                            float* logprob, float* kl, float* entropy, void* stream) {
+    const gemm_status_t st =
+        check_policy(dtype, logits, T, V, ld, tokens, temperature, policy, loss, logprob, kl, entropy);
+    if (st != GEMM_OK) return st;
+    Args a{};
+    fill_rows(a, logits, V, ld, temperature);
+    fill_policy(a, tokens, *policy, loss, logprob, kl, entropy);
+    return launch_type<kPolicy, false, false>(device, dtype, a, T, stream);
+}
+
+gemm_status_t logits_policy_grad(int device, gemm_dtype_t dtype, const void* logits, int64_t T, int64_t V, int64_t ld,
+                                 const int64_t* tokens, float temperature, const logits_policy_t* policy,
+                                 const float* w, float* loss, float* logprob, float* kl, float* entropy, void* dlogits,
+                                 int64_t ldd, void* stream) {
+    gemm_status_t st = check_policy(dtype, logits, T, V, ld, tokens, temperature, policy, loss, logprob, kl, entropy);
+    if (st == GEMM_OK) st = check_gradient(dtype, dlogits, T, V, ldd);
+    if (st != GEMM_OK) return st;
+    if (T > 0 && !w) return GEMM_ERR_INVALID_ARG;
+    if (!aligned(w, 4)) return GEMM_ERR_MISALIGNED;
+    Args a{};
+    fill_rows(a, logits, V, ld, temperature);
+    fill_policy(a, tokens, *policy, loss, logprob, kl, entropy);
+    a.w = w;
+    a.dz = dlogits;
+    a.ldd = ldd;
+    return launch_type<kPolicy, true, false>(device, dtype, a, T, stream);
+}
+
+gemm_status_t logits_preference(int device, gemm_dtype_t dtype, const void* logits, int64_t T, int64_t V, int64_t ld,
+                                const int64_t* tokens, float temperature, const logits_preference_t* preference,
+                                float* loss, float* reward, float* logprob, void* stream) {
+    const gemm_status_t st =
+        check_preference(dtype, logits, T, V, ld, tokens, temperature, preference, loss, reward, logprob);
+    if (st != GEMM_OK) return st;
+    Args a{};
+    fill_rows(a, logits, V, ld, temperature);
+    fill_preference(a, tokens, loss, logprob);
+    return run_preference(device, dtype, a, T, *preference, nullptr, reward, stream);
+}
+
+gemm_status_t logits_preference_grad(int device, gemm_dtype_t dtype, const void* logits, int64_t T, int64_t V,
+                                     int64_t ld, const int64_t* tokens, float temperature,
+                                     const logits_preference_t* preference, const float* w, float* loss, float* reward,
+                                     float* logprob, void* dlogits, int64_t ldd, void* work, void* stream) {
+    gemm_status_t st = check_preference(dtype, logits, T, V, ld, tokens, temperature, preference, loss, reward, logprob);
+    if (st == GEMM_OK) st = check_gradient(dtype, dlogits, T, V, ldd);
+    if (st != GEMM_OK) return st;
+    if ((preference->pairs > 0 && !w) || (T > 0 && !work)) return GEMM_ERR_INVALID_ARG;
+    if (!aligned(w, 4) || !aligned(work, 16)) return GEMM_ERR_MISALIGNED;
+    Args a{};
+    fill_rows(a, logits, V, ld, temperature);
+    fill_preference(a, tokens, loss, logprob);
+    a.dz = V > 0 ? dlogits : nullptr;
+    a.ldd = ldd;
+    a.state = static_cast<RowState*>(work);
+    return run_preference(device, dtype, a, T, *preference, w, reward, stream);
 }
 
 #ifdef TCDT_FAULT_INJECTION

@@ -1,9 +1,11 @@
 """Operators on the rows of a logits matrix (the C ABI of ``include/logits.h``):
 token log-probabilities with entropy and top alternatives, distillation from
-a teacher's top logits, and the gradients of both for the logits.
+a teacher's top logits, a clipped policy loss, a preference loss of paired
+sequences, and the gradients of all four for the logits.
 
 Like the rest of the binding, the functions check and marshal arguments; the
-computation is one CUDA kernel per call on the given (or current) stream.
+computation is one CUDA kernel per call (two or three for the preference loss)
+on the given (or current) stream.
 
 ``logits`` is a T x V device tensor of fp32, fp16 or bf16 with unit column
 stride; rows may be padded (the product that feeds on a gradient wants row
@@ -21,7 +23,8 @@ import ctypes
 from typing import NamedTuple
 
 __all__ = ["TokenLogprobs", "TokenLogprobsGrad", "token_logprobs", "token_logprobs_grad", "distill_topk",
-           "distill_topk_grad", "MAX_TOP", "MAX_TEACHER"]
+           "distill_topk_grad", "PolicyLoss", "PolicyLossGrad", "policy_loss", "policy_loss_grad",
+           "PreferenceLoss", "PreferenceLossGrad", "preference_loss", "preference_loss_grad", "MAX_TOP", "MAX_TEACHER"]
 
 MAX_TOP = 128
 MAX_TEACHER = 1024
@@ -42,6 +45,47 @@ class TokenLogprobsGrad(NamedTuple):
     dlogits: object        # [T, V] of the logits' type
 
 
+class PolicyLoss(NamedTuple):
+    loss: object           # [T] fp32
+    logprob: object        # [T] fp32
+    kl: object             # [T] fp32
+    entropy: object        # [T] fp32
+
+
+class PolicyLossGrad(NamedTuple):
+    loss: object
+    logprob: object
+    kl: object
+    entropy: object
+    dlogits: object        # [T, V] of the logits' type
+
+
+class PreferenceLoss(NamedTuple):
+    loss: object           # [pairs] fp32
+    reward: object         # [2 pairs] fp32
+    logprob: object        # [T] fp32
+
+
+class PreferenceLossGrad(NamedTuple):
+    loss: object
+    reward: object
+    logprob: object
+    dlogits: object        # [T, V] of the logits' type
+
+
+class _Policy(ctypes.Structure):
+    """logits_policy_t."""
+    _fields_ = [("old_logprob", ctypes.c_void_p), ("advantage", ctypes.c_void_p), ("ref_logprob", ctypes.c_void_p),
+                ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("entropy_bonus", ctypes.c_float)]
+
+
+class _Preference(ctypes.Structure):
+    """logits_preference_t."""
+    _fields_ = [("offsets", ctypes.c_void_p), ("pairs", ctypes.c_int64), ("ref_logprob", ctypes.c_void_p),
+                ("beta", ctypes.c_float), ("smoothing", ctypes.c_float)]
+
+
 def declare(lib: ctypes.CDLL) -> None:
     p, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
     rows = [i32, i32, p, i64, i64, i64]
@@ -50,7 +94,14 @@ def declare(lib: ctypes.CDLL) -> None:
     teacher = [i64, p, i32, p, i64, f32]
     lib.logits_distill.argtypes = rows + teacher + [p, p, p]
     lib.logits_distill_grad.argtypes = rows + teacher + [p, p, p, p, i64, p]
-    for f in (lib.logits_logprobs, lib.logits_logprobs_grad, lib.logits_distill, lib.logits_distill_grad):
+    policy = [p, f32, ctypes.POINTER(_Policy)]
+    lib.logits_policy.argtypes = rows + policy + [p, p, p, p, p]
+    lib.logits_policy_grad.argtypes = rows + policy + [p, p, p, p, p, p, i64, p]
+    preference = [p, f32, ctypes.POINTER(_Preference)]
+    lib.logits_preference.argtypes = rows + preference + [p, p, p, p]
+    lib.logits_preference_grad.argtypes = rows + preference + [p, p, p, p, p, i64, p, p]
+    for f in (lib.logits_logprobs, lib.logits_logprobs_grad, lib.logits_distill, lib.logits_distill_grad,
+              lib.logits_policy, lib.logits_policy_grad, lib.logits_preference, lib.logits_preference_grad):
         f.restype = i32
 
 
@@ -221,3 +272,105 @@ def distill_topk_grad(logits, teacher_tokens, teacher_logits, weight, *, tempera
     _call("logits_distill_grad", dev.index, code, logits.data_ptr(), T, V, ld, *teacher, temperature, w,
           loss.data_ptr(), None, dlogits.data_ptr(), ldd, _stream(stream, dev))
     return loss, dlogits
+
+
+def _policy_args(logits, tokens, old_logprob, advantage, ref_logprob, clip, kl, entropy_bonus):
+    """The rows' size and type, and the arguments from the tokens to the policy."""
+    import torch
+    T, V, ld = _matrix(logits, "logits")
+    dev = logits.device
+    code = _dtype(logits)
+    if tokens is None or old_logprob is None or advantage is None:
+        raise ValueError("tokens, old_logprob and advantage must be given")
+    if kl != 0 and ref_logprob is None:
+        raise ValueError("a KL term needs ref_logprob")
+    low, high = clip
+    tok = _vector(tokens, T, torch.int64, dev, "tokens")
+    policy = _Policy(_vector(old_logprob, T, torch.float32, dev, "old_logprob"),
+                     _vector(advantage, T, torch.float32, dev, "advantage"),
+                     _vector(ref_logprob, T, torch.float32, dev, "ref_logprob"), low, high, kl, entropy_bonus)
+    out = [torch.empty((T,), dtype=torch.float32, device=dev) for _ in range(4)]
+    return (T, V, ld), dev, (dev.index, code, logits.data_ptr(), T, V, ld, tok), policy, out
+
+
+def policy_loss(logits, tokens, old_logprob, advantage, ref_logprob=None, *, clip=(0.2, 0.2), kl: float = 0.0,
+                entropy_bonus: float = 0.0, temperature: float = 1.0, stream=None) -> PolicyLoss:
+    """Clipped policy loss of each row's token (int64): -min(r A, clip(r, 1 - clip[0],
+    1 + clip[1]) A) + kl * KL term - entropy_bonus * entropy, with
+    r = exp(logprob - old_logprob) and A the advantage (fp32 vectors).
+    ref_logprob gives the KL term against a reference policy.  A row with a
+    token outside 0..V-1 has zeros and is not read (logits_policy)."""
+    _, dev, rows, policy, out = _policy_args(logits, tokens, old_logprob, advantage, ref_logprob, clip, kl,
+                                             entropy_bonus)
+    _call("logits_policy", *rows, temperature, ctypes.byref(policy), *(v.data_ptr() for v in out),
+          _stream(stream, dev))
+    return PolicyLoss(*out)
+
+
+def policy_loss_grad(logits, tokens, old_logprob, advantage, weight, ref_logprob=None, *, clip=(0.2, 0.2),
+                     kl: float = 0.0, entropy_bonus: float = 0.0, temperature: float = 1.0, dlogits=None,
+                     stream=None) -> PolicyLossGrad:
+    """policy_loss and the gradient for the logits of sum(weight * loss), in
+    one kernel (logits_policy_grad).  Rows without a token or of weight 0 have
+    gradients of zeros.  dlogits may be the logits themselves."""
+    import torch
+    if weight is None:
+        raise ValueError("weight must be given")
+    (T, _, _), dev, rows, policy, out = _policy_args(logits, tokens, old_logprob, advantage, ref_logprob, clip, kl,
+                                                     entropy_bonus)
+    w = _vector(weight, T, torch.float32, dev, "weight")
+    dlogits, ldd = _gradient(dlogits, logits)
+    _call("logits_policy_grad", *rows, temperature, ctypes.byref(policy), w, *(v.data_ptr() for v in out),
+          dlogits.data_ptr(), ldd, _stream(stream, dev))
+    return PolicyLossGrad(*out, dlogits)
+
+
+def _preference_args(logits, tokens, offsets, ref_logprob, beta, smoothing):
+    import torch
+    T, V, ld = _matrix(logits, "logits")
+    dev = logits.device
+    code = _dtype(logits)
+    if tokens is None or offsets is None:
+        raise ValueError("tokens and offsets must be given")
+    tok = _vector(tokens, T, torch.int64, dev, "tokens")
+    if offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
+        raise ValueError("offsets must have an entry for each sequence of a pair and one more")
+    pairs = (offsets.shape[0] - 1) // 2
+    preference = _Preference(_vector(offsets, offsets.shape[0], torch.int64, dev, "offsets"), pairs,
+                             _vector(ref_logprob, T, torch.float32, dev, "ref_logprob"), beta, smoothing)
+    f32 = torch.float32
+    out = [torch.empty((n,), dtype=f32, device=dev) for n in (pairs, 2 * pairs, T)]
+    return pairs, T, dev, (dev.index, code, logits.data_ptr(), T, V, ld, tok), preference, out
+
+
+def preference_loss(logits, tokens, offsets, ref_logprob=None, *, beta: float = 0.1, smoothing: float = 0.0,
+                    temperature: float = 1.0, stream=None) -> PreferenceLoss:
+    """Preference loss of pairs of packed sequences: sequence s has the rows
+    offsets[s] .. offsets[s + 1] - 1 (int64, on the device), 2q is the
+    preferred one of pair q and 2q + 1 the other.  A sequence's reward is beta
+    times the sum of logprob - ref_logprob over its rows whose token (int64) is
+    in 0..V-1, the loss -(1 - smoothing) log sigma(m) - smoothing log sigma(-m)
+    of the rewards' difference m (logits_preference)."""
+    _, _, dev, rows, preference, out = _preference_args(logits, tokens, offsets, ref_logprob, beta, smoothing)
+    _call("logits_preference", *rows, temperature, ctypes.byref(preference), *(v.data_ptr() for v in out),
+          _stream(stream, dev))
+    return PreferenceLoss(*out)
+
+
+def preference_loss_grad(logits, tokens, offsets, weight, ref_logprob=None, *, beta: float = 0.1,
+                         smoothing: float = 0.0, temperature: float = 1.0, dlogits=None,
+                         stream=None) -> PreferenceLossGrad:
+    """preference_loss and the gradient for the logits of sum(weight * loss),
+    weight one fp32 number a pair (logits_preference_grad).  Rows without a
+    token or in no sequence have gradients of zeros.  dlogits may be the logits
+    themselves."""
+    import torch
+    if weight is None:
+        raise ValueError("weight must be given")
+    pairs, T, dev, rows, preference, out = _preference_args(logits, tokens, offsets, ref_logprob, beta, smoothing)
+    w = _vector(weight, pairs, torch.float32, dev, "weight")
+    dlogits, ldd = _gradient(dlogits, logits)
+    work = torch.empty((T, 4), dtype=torch.float32, device=dev)
+    _call("logits_preference_grad", *rows, temperature, ctypes.byref(preference), w, *(v.data_ptr() for v in out),
+          dlogits.data_ptr(), ldd, work.data_ptr(), _stream(stream, dev))
+    return PreferenceLossGrad(*out, dlogits)
