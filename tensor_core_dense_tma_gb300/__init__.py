@@ -25,6 +25,7 @@ import os
 import threading
 
 from . import build as _build_mod
+from . import adapters as _adapters
 from . import logits as _logits
 
 __all__ = [
@@ -40,7 +41,7 @@ __all__ = [
     "gemm_run_i8", "gemm_run_i8_dynamic", "gemm_quantize_rows_i8", "quantize_rows_i8",
     "token_logprobs", "token_logprobs_grad", "distill_topk", "distill_topk_grad", "TokenLogprobs",
     "TokenLogprobsGrad", "policy_loss", "policy_loss_grad", "PolicyLoss", "PolicyLossGrad",
-    "preference_loss", "preference_loss_grad", "PreferenceLoss", "PreferenceLossGrad",
+    "preference_loss", "preference_loss_grad", "PreferenceLoss", "PreferenceLossGrad", "AdaptersGrad",
 ]
 
 STATUS = {
@@ -146,6 +147,7 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.gemm_quantize_rows_i8.argtypes = [i32, p, i32, i64, i64, i64, p, i64, p, p]
     lib.gemm_quantize_rows_i8.restype = i32
     _logits.declare(lib)
+    _adapters.declare(lib)
     lib.gemm_status_string.argtypes = [i32]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_measure_mma_rate.argtypes = [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_double),
@@ -540,6 +542,9 @@ def quantize_rows_i8(X, Q=None, scale=None, *, stream=None):
     return Q, scale
 
 
+AdaptersGrad = _adapters.AdaptersGrad
+
+
 class Plan:
     """A gemm plan bound to one device and one input type."""
 
@@ -709,6 +714,26 @@ class Plan:
             raise ValueError("X must be a 2-D fp32, fp16 or bf16 tensor, B a 2-D int8 one")
         return self._run_i8(X, B, D, None, col_scale, bias, act, out_dtype if D is not None else out_dtype or xt,
                             stream)
+
+    def linear_adapters(self, X, B, down, up, index, scale=None, D=None, *, bias=None, hidden=None,
+                        out_dtype: str | None = None, stream=None):
+        """(D, hidden): D = X@B + bias and, added to row i, up[g] (scale[g] *
+        down[g] X[i]) of its adapter g = index[i] (int32, one per row; outside
+        0..G-1: none), on an "f16" or "bf16" plan (gemm_run_adapters).  X is row-major
+        M x K, B K x N in either order, down G x R x K, up G x N x R (R <= 128, either of
+        the last two dimensions contiguous), scale G fp32 numbers, bias N.  D is of
+        the plan's type unless out_dtype or D says otherwise.  hidden (M rows, as
+        gemm_adapters_hidden_width says, allocated if not given) is what
+        linear_adapters_grad wants of the forward pass."""
+        return _adapters.linear(self, X, B, down, up, index, scale, D, bias, hidden, out_dtype, stream)
+
+    def linear_adapters_grad(self, dY, B, X, hidden, down, up, index, scale=None, dX=None, *, d_down=None, d_up=None,
+                             stream=None) -> AdaptersGrad:
+        """Gradients of sum(dY * linear_adapters(...)) for X, down and up: B, X, down,
+        up, index and scale as given to that call, hidden as it returned it
+        (gemm_run_adapters, gemm_adapters_grad).  d_down and d_up are of the
+        plan's type unless given as fp32; an adapter without rows has zeros."""
+        return _adapters.linear_grad(self, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up, stream)
 
     def _resolve(self, A, B, C, D, out_dtype):
         """Sizes, storage orders and leading dimensions from the tensors'

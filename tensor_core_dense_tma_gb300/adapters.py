@@ -1,0 +1,219 @@
+"""Low-rank adapters of many requests beside a shared product (the C ABI of
+``include/adapters.h``): ``Plan.linear_adapters`` and ``Plan.linear_adapters_grad``.
+
+This module reads sizes, storage orders and strides from the tensors; the
+computation is the library's kernels on the given (or current) stream.  A
+stack of factors is G x R x K (``down``) or G x N x R (``up``), with unit stride
+along either of its last two dimensions: ``up.transpose(1, 2)`` is a ``down``
+for the backward direction without a copy.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+__all__ = ["AdaptersGrad", "MAX_RANK"]
+
+MAX_RANK = 128
+
+
+class AdaptersGrad(NamedTuple):
+    dX: object             # [M, K] of the plan's type
+    d_down: object         # [G, R, K]
+    d_up: object           # [G, N, R]
+
+
+class Adapters(ctypes.Structure):
+    """gemm_adapters_t."""
+    _fields_ = [("count", ctypes.c_int64), ("rank", ctypes.c_int64), ("down", ctypes.c_void_p),
+                ("down_ld", ctypes.c_int64), ("down_stride", ctypes.c_int64), ("down_layout", ctypes.c_int),
+                ("up", ctypes.c_void_p), ("up_ld", ctypes.c_int64), ("up_stride", ctypes.c_int64),
+                ("up_layout", ctypes.c_int), ("scale", ctypes.c_void_p), ("index", ctypes.c_void_p)]
+
+
+def declare(lib: ctypes.CDLL) -> None:
+    p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    stacks = ctypes.POINTER(Adapters)
+    lib.gemm_adapters_hidden_width.argtypes = [i64]
+    lib.gemm_adapters_hidden_width.restype = i64
+    lib.gemm_adapters_work_bytes.argtypes = [i64, i64]
+    lib.gemm_adapters_work_bytes.restype = i64
+    lib.gemm_run_adapters.argtypes = [p, p, p, p, i64, i64, i64, i64, i64, i64, i32, i32, p, stacks, p, i64, p, p]
+    lib.gemm_run_adapters.restype = i32
+    lib.gemm_adapters_grad.argtypes = [p, p, p, i64, i64, i64, i64, i64, stacks, p, p, i64, i32, p, i64, i64, p, i64,
+                                       i64, p]
+    lib.gemm_adapters_grad.restype = i32
+
+
+_calls: dict = {}     # the library's entry points and torch, filled on the first use
+
+
+def _lib():
+    if not _calls:
+        import torch
+        from . import load, DTYPE, GemmError
+        lib = load()
+        _calls.update(torch=torch, error=GemmError, run=lib.gemm_run_adapters, grad=lib.gemm_adapters_grad,
+                      work=lib.gemm_adapters_work_bytes,
+                      codes={torch.float16: DTYPE["f16"], torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"]},
+                      types={"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32})
+    return _calls["torch"]
+
+
+def hidden_width(rank: int) -> int:
+    """Columns of the hidden rows of adapters of this rank (gemm_adapters_hidden_width)."""
+    return 32 if rank <= 16 else 64 if rank <= 32 else 128 if rank <= 64 else 256
+
+
+def _row_ld(t, what: str, dev, dtype):
+    """Row stride of a row-major matrix of the plan's type on its device."""
+    if t.dim() != 2 or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{what} must be a 2-D {dtype} tensor on X's device")
+    (r, c), (s0, s1) = t.shape, t.stride()
+    if (c > 1 and s1 != 1) or (r > 1 and s0 < c):
+        raise ValueError(f"{what} must be row-major (strides {t.stride()})")
+    return s0 if r > 1 else -(-c // 8) * 8
+
+
+def _order(r, c, s0, s1):
+    """(leading dimension, layout) of an r x c matrix, or None: by the dimension
+    that has unit stride and more than one element.  A single row or column has
+    no stride of its own: any will do."""
+    if c > 1 and s1 == 1 and (s0 >= c or r <= 1):
+        return (s0 if r > 1 else -(-c // 8) * 8), 0
+    if r > 1 and s0 == 1 and (s1 >= r or c <= 1):
+        return (s1 if c > 1 else -(-r // 8) * 8), 1
+    if c <= 1:
+        return (s0 if r > 1 else 8), 0
+    return (s1, 1) if r <= 1 else None
+
+
+def _stack(t, what: str, dev, dtype, shape):
+    """(address, leading dimension, stride, layout) of a stack of matrices."""
+    if t.dim() != 3 or t.dtype != dtype or t.device != dev or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be a {shape[0]} x {shape[1]} x {shape[2]} {dtype} tensor on X's device")
+    s, s0, s1 = t.stride()
+    order = _order(shape[1], shape[2], s0, s1)
+    if order is None:
+        raise ValueError(f"{what} must have unit stride along one of its last two dimensions (strides {t.stride()})")
+    return t.data_ptr(), order[0], (s if shape[0] > 1 else 0), order[1]
+
+
+def _adapters(down, up, index, scale, M, N, K, dev, dtype):
+    torch = _calls["torch"]
+    if down.dim() != 3 or up.dim() != 3:
+        raise ValueError("down must be G x R x K, up G x N x R")
+    G, R = down.shape[0], down.shape[1]
+    if not 1 <= R <= MAX_RANK:
+        raise ValueError(f"the rank must be 1..{MAX_RANK}")
+    if index.dtype != torch.int32 or index.shape != (M,) or index.device != dev or (M > 1 and index.stride(0) != 1):
+        raise ValueError("index must be a contiguous int32 vector with one entry per row on X's device")
+    if scale is not None and (scale.dtype != torch.float32 or scale.shape != (G,) or scale.device != dev
+                              or (G > 1 and scale.stride(0) != 1)):
+        raise ValueError("scale must be a contiguous fp32 vector with one entry per adapter on X's device")
+    return Adapters(G, R, *_stack(down, "down", dev, dtype, (G, R, K)), *_stack(up, "up", dev, dtype, (G, N, R)),
+                    scale.data_ptr() if scale is not None else None, index.data_ptr())
+
+
+def _hidden(hidden, what, M, R, dev, dtype):
+    width = hidden_width(R)
+    if hidden is None:
+        hidden = _calls["torch"].empty((M, width), dtype=dtype, device=dev)
+        return hidden, width
+    if tuple(hidden.shape) != (M, width):
+        raise ValueError(f"{what} must be {M} x {width}")
+    return hidden, _row_ld(hidden, what, dev, dtype)
+
+
+def _columns(B, K, what: str, dev, dtype):
+    """(N, leading dimension, layout) of the K x N matrix B."""
+    if B.dim() != 2 or B.dtype != dtype or B.device != dev:
+        raise ValueError(f"{what} must be a 2-D {dtype} tensor on X's device")
+    if B.shape[0] != K:
+        raise ValueError("inner dimensions differ")
+    order = _order(*B.shape, *B.stride())
+    if order is None:
+        raise ValueError(f"{what} must be row- or column-major (strides {B.stride()})")
+    return B.shape[1], *order
+
+
+def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, stream):
+    """Plan.linear_adapters."""
+    torch = _lib()
+    dev, dtype = X.device, _calls["types"].get(plan.in_dtype)
+    if dtype not in (torch.float16, torch.bfloat16) or dev.type != "cuda" or X.dim() != 2:
+        raise ValueError("adapters take 2-D device tensors and an f16 or bf16 plan")
+    M, K = X.shape
+    ldx = _row_ld(X, "X", dev, dtype)
+    N, ldb, layout = _columns(B, K, "B", dev, dtype)
+    a = _adapters(down, up, index, scale, M, N, K, dev, dtype)
+    if D is None:
+        D = torch.empty((M, N), dtype=_calls["types"][out_dtype or plan.in_dtype], device=dev)
+        ldd = N
+    else:
+        if out_dtype is not None and D.dtype != _calls["types"][out_dtype]:
+            raise ValueError("D must have the output type")
+        d0, d1 = D.stride() if D.dim() == 2 else (0, 0)
+        if D.dtype not in _calls["codes"] or D.shape != (M, N) or D.device != dev or (N > 1 and d1 != 1) or \
+                (M > 1 and d0 < N):
+            raise ValueError("D must be a row-major M x N matrix on X's device")
+        ldd = d0 if M > 1 else N
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or bias.device != dev
+                             or (N > 1 and bias.stride(0) != 1)):
+        raise ValueError("bias must be a contiguous fp32 vector of length N on X's device")
+    hidden, ldh = _hidden(hidden, "hidden", M, a.rank, dev, dtype)
+    need = _calls["work"](M, N)
+    work = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    st = _calls["run"](plan.handle, X.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, ldx, ldb, ldd, layout,
+                       _calls["codes"][D.dtype], bias.data_ptr() if bias is not None else None, ctypes.byref(a),
+                       hidden.data_ptr(), ldh, work.data_ptr() if need else None, stream)
+    if st != 0:
+        raise _calls["error"](st, "gemm_run_adapters")
+    return D, hidden
+
+
+def _gradient(t, dtype, dev, shape, what):
+    """(tensor, leading dimension, stride) of an output stack, allocated if not given."""
+    G, rows, cols = shape
+    if t is None:
+        return _calls["torch"].empty(shape, dtype=dtype, device=dev), cols, rows * cols
+    if tuple(t.shape) != shape or t.device != dev:
+        raise ValueError(f"{what} must be a {G} x {rows} x {cols} tensor on X's device")
+    s, s0, s1 = t.stride()
+    if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols) or (G > 1 and s < (rows - 1) * s0 + cols):
+        raise ValueError(f"{what} must have unit stride along its last dimension (strides {t.stride()})")
+    return t, (s0 if rows > 1 else cols), (s if G > 1 else 0)
+
+
+def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up, stream):
+    """Plan.linear_adapters_grad."""
+    torch = _lib()
+    dev, dtype = X.device, _calls["types"].get(plan.in_dtype)
+    if X.dim() != 2 or dY.dim() != 2 or B.dim() != 2 or down.dim() != 3 or up.dim() != 3:
+        raise ValueError("X, dY and B must be 2-D, down and up 3-D tensors")
+    (M, K), N, G, R = X.shape, dY.shape[1], down.shape[0], down.shape[1]
+    if dY.shape[0] != M or B.shape != (K, N):
+        raise ValueError("dY must be M x N, B K x N")
+    ldx = _row_ld(X, "X", dev, dtype)
+    lddy = _row_ld(dY, "dY", dev, dtype)
+    hidden, ldh = _hidden(hidden, "hidden", M, R, dev, dtype)
+    like = d_down if d_down is not None else d_up
+    out = dtype if like is None else like.dtype
+    if out not in (torch.float32, dtype) or (d_up is not None and d_up.dtype != out):
+        raise ValueError("d_down and d_up must both be fp32 or both of the plan's type")
+    d_down, down_ld, down_stride = _gradient(d_down, out, dev, (G, R, K), "d_down")
+    d_up, up_ld, up_stride = _gradient(d_up, out, dev, (G, N, R), "d_up")
+    # dX is the same product the other way round, and leaves p as its hidden rows
+    p = torch.empty_strided((M, hidden_width(R)), (ldh, 1), dtype=dtype, device=dev)
+    dX, _ = linear(plan, dY, B.t(), up.transpose(1, 2), down.transpose(1, 2), index, scale, dX, None, p, None, stream)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    a = Adapters(G, R, None, 0, 0, 0, None, 0, 0, 0, None, index.data_ptr())
+    st = _calls["grad"](plan.handle, X.data_ptr(), dY.data_ptr(), M, N, K, ldx, lddy, ctypes.byref(a),
+                        hidden.data_ptr(), p.data_ptr(), ldh, _calls["codes"][out], d_down.data_ptr(), down_ld,
+                        down_stride, d_up.data_ptr(), up_ld, up_stride, stream)
+    if st != 0:
+        raise _calls["error"](st, "gemm_adapters_grad")
+    return AdaptersGrad(dX, d_down, d_up)
