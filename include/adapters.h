@@ -5,7 +5,7 @@
  *
  *   gemm_run_adapters      D = X W + bias + (the rows' adapters)
  *   gemm_adapters_grad     gradients of the adapters' two factors
- *   gemm_adapters_work_bytes, gemm_adapters_hidden_width
+ *   gemm_adapters_hidden_width  columns of the rows that the two share
  *
  * Row i has the adapter g = index[i]; a value outside 0..count-1 (say -1) means
  * none.  With A = down[g] (rank x K), U = up[g] (N x rank), s = scale[g],
@@ -38,7 +38,7 @@
  * rounded once.
  *
  * Memory, streams and errors are gemm.h's: device pointers of the caller;
- * X, W, down, up, dD, hidden and work start on 16-byte boundaries and so do
+ * X, W, down, up, dD and hidden start on 16-byte boundaries and so do
  * their rows and an adapter's factors (GEMM_ERR_MISALIGNED); one plan is
  * used by one stream at a time; a wait inside a kernel that ran out is in
  * gemm_plan_device_status.  Nothing is allocated, so calls may be captured.
@@ -77,17 +77,12 @@ typedef struct {
  * rank; 0 for a rank out of range. */
 int64_t gemm_adapters_hidden_width(int64_t rank);
 
-/* Bytes of `work` of a gemm_run_adapters call of this size (0 or more). */
-int64_t gemm_adapters_work_bytes(int64_t M, int64_t N);
-
 /* D (M x N, row-major) of X (M x K, row-major) and W (K x N, either layout).
- * bias is [N] or NULL.  hidden (M rows of ldh elements) is written; work is
- * gemm_adapters_work_bytes bytes, this call's alone until it has ended (NULL
- * where that is 0). */
+ * bias is [N] or NULL.  hidden (M rows of ldh elements) is written. */
 gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void *X, const void *W, void *D, int64_t M, int64_t N,
                                 int64_t K, int64_t ldx, int64_t ldw, int64_t ldd, gemm_layout_t layoutW,
                                 gemm_dtype_t out_dtype, const float *bias, const gemm_adapters_t *adapters,
-                                void *hidden, int64_t ldh, void *work, void *stream);
+                                void *hidden, int64_t ldh, void *stream);
 
 /* d_down[g * down_stride + r * down_ld + k] and d_up[g * up_stride + n * up_ld + r],
  * of all `count` adapters (zeros for one without rows), from X (M x K), dD

@@ -36,9 +36,7 @@ def declare(lib: ctypes.CDLL) -> None:
     stacks = ctypes.POINTER(Adapters)
     lib.gemm_adapters_hidden_width.argtypes = [i64]
     lib.gemm_adapters_hidden_width.restype = i64
-    lib.gemm_adapters_work_bytes.argtypes = [i64, i64]
-    lib.gemm_adapters_work_bytes.restype = i64
-    lib.gemm_run_adapters.argtypes = [p, p, p, p, i64, i64, i64, i64, i64, i64, i32, i32, p, stacks, p, i64, p, p]
+    lib.gemm_run_adapters.argtypes = [p, p, p, p, i64, i64, i64, i64, i64, i64, i32, i32, p, stacks, p, i64, p]
     lib.gemm_run_adapters.restype = i32
     lib.gemm_adapters_grad.argtypes = [p, p, p, i64, i64, i64, i64, i64, stacks, p, p, i64, i32, p, i64, i64, p, i64,
                                        i64, p]
@@ -54,7 +52,6 @@ def _lib():
         from . import load, DTYPE, GemmError
         lib = load()
         _calls.update(torch=torch, error=GemmError, run=lib.gemm_run_adapters, grad=lib.gemm_adapters_grad,
-                      work=lib.gemm_adapters_work_bytes,
                       codes={torch.float16: DTYPE["f16"], torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"]},
                       types={"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32})
     return _calls["torch"]
@@ -162,13 +159,11 @@ def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, strea
                              or (N > 1 and bias.stride(0) != 1)):
         raise ValueError("bias must be a contiguous fp32 vector of length N on X's device")
     hidden, ldh = _hidden(hidden, "hidden", M, a.rank, dev, dtype)
-    need = _calls["work"](M, N)
-    work = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev.index)
     st = _calls["run"](plan.handle, X.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, ldx, ldb, ldd, layout,
                        _calls["codes"][D.dtype], bias.data_ptr() if bias is not None else None, ctypes.byref(a),
-                       hidden.data_ptr(), ldh, work.data_ptr() if need else None, stream)
+                       hidden.data_ptr(), ldh, stream)
     if st != 0:
         raise _calls["error"](st, "gemm_run_adapters")
     return D, hidden

@@ -11,128 +11,109 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <climits>
-#include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "adapters.h"
+#include "adapters_kernel.cuh"
 #include "gemm_internal.cuh"
 
 using namespace tcdt_host;
 
 namespace {
 
-constexpr int kThreads = 256;
+using tcdt::adapter_split;
+using tcdt::adapter_value;
+using tcdt::FactorGradArgs;
+using tcdt::HiddenArgs;
 
-// A stack of matrices, element (g, i, j) at p + g * stride + i * si + j * sj.
-struct Stack {
-    const void* p;
-    int64_t stride, si, sj;
-};
+// ---- h of a few rows ---------------------------------------------------------
+// One CTA for a row and four of its values: X and four rows of A are read once,
+// 16 bytes a load, all loads of a thread under way together (K = 8192: four
+// of X and sixteen of A), so a call takes about as long as one trip to memory.  With
+// more rows X and A come again from L2 each time: hidden_tile_kernel then.
+constexpr int kRowThreads = 256, kRowValues = 4;
 
-struct Rows {
+struct RowArgs {
+    const uint16_t* X;
+    int64_t ldx, K;
+    const uint16_t* down;             // [adapter][rank][K]
+    int64_t down_ld, down_stride;
     const int32_t* index;
     const float* scale;
-    int32_t count, rank, part;      // part: columns of the high parts, and of the low ones
-    int64_t M;
+    int32_t count, rank, part;
+    uint16_t* hidden;
+    int64_t ldh;
+    uint32_t bf16;
 };
 
-__device__ __forceinline__ float value(__half x) { return __half2float(x); }
-__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float value(float x) { return x; }
-template <typename E>
-__device__ __forceinline__ E rounded(float x);
-template <>
-__device__ __forceinline__ __half rounded<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ float rounded<float>(float x) { return x; }
-
-// The adapter of a row, -1 for none.
-__device__ __forceinline__ int adapter_of(const Rows& a, int64_t i) {
-    const int g = a.index[i];
-    return g >= 0 && g < a.count ? g : -1;
+__device__ __forceinline__ void unpack8(const uint4& v, bool bf16, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = adapter_value(w[e] & 0xFFFFu, bf16);
+        x[2 * e + 1] = adapter_value(w[e] >> 16, bf16);
+    }
 }
 
-// h as its two parts; an infinity or a NaN is all in the high one.
-template <typename E>
-__device__ __forceinline__ void store_hidden(E* row, int r, int part, float h) {
-    const E high = rounded<E>(h);
-    const float rest = h - value(high);
-    row[r] = high;
-    row[part + r] = rounded<E>(isfinite(value(high)) ? rest : 0.f);
-}
-
-template <typename E>
-__device__ __forceinline__ float load_hidden(const E* row, int r, int part) {
-    return value(row[r]) + value(row[part + r]);
-}
-
-// h of a row, one CTA a row.
-template <typename E>
-__global__ void __launch_bounds__(kThreads) hidden_kernel(const Rows a, const E* X, int64_t ldx, int64_t K,
-                                                          const Stack down, E* hidden, int64_t ldh) {
-    const int64_t i = blockIdx.x;
+__global__ void __launch_bounds__(kRowThreads) hidden_rows_kernel(const RowArgs a) {
+    __shared__ float part[kRowThreads / 32][kRowValues];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = adapter_of(a, i);
-    const E* x = X + i * ldx;
-    E* row = hidden + i * ldh;
-    const float s = g < 0 ? 0.f : a.scale ? a.scale[g] : 1.f;
-    const E* A = static_cast<const E*>(down.p) + (g < 0 ? 0 : g) * down.stride;
-    for (int r = a.rank + tid; r < a.part; r += kThreads) store_hidden<E>(row, r, a.part, 0.f);
-    for (int r0 = 0; r0 < a.rank; r0 += kThreads / 32) {
-        const int r = r0 + warp;
-        float h = 0.f;
-        if (g >= 0 && r < a.rank)
-            for (int64_t k = lane; k < K; k += 32) h = fmaf(value(x[k]), value(A[r * down.si + k * down.sj]), h);
-        for (int o = 16; o; o >>= 1) h += __shfl_xor_sync(~0u, h, o);
-        if (lane == 0 && r < a.rank) store_hidden<E>(row, r, a.part, g < 0 ? 0.f : s * h);
+    const int64_t i = blockIdx.y;
+    const int r0 = blockIdx.x * kRowValues;
+    const bool bf16 = a.bf16 != 0;
+    tcdt::griddep_launch();
+    const int g = a.index[i];
+    float sum[kRowValues] = {};
+    const bool mine = g >= 0 && g < a.count && r0 < a.rank;
+    if (mine) {
+        const uint16_t* x = a.X + i * a.ldx;
+        const uint16_t* A[kRowValues];
+#pragma unroll
+        for (int r = 0; r < kRowValues; ++r) A[r] = a.down + g * a.down_stride + min(r0 + r, a.rank - 1) * a.down_ld;
+        const int64_t vectors = a.K >> 3;
+#pragma unroll 4
+        for (int64_t v = tid; v < vectors; v += kRowThreads) {
+            float xv[8];
+            unpack8(__ldg(reinterpret_cast<const uint4*>(x) + v), bf16, xv);
+#pragma unroll
+            for (int r = 0; r < kRowValues; ++r) {
+                float av[8];
+                unpack8(__ldg(reinterpret_cast<const uint4*>(A[r]) + v), bf16, av);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[r] = fmaf(xv[e], av[e], sum[r]);
+            }
+        }
+        const int64_t k = vectors * 8 + tid;
+        if (k < a.K) {
+            const float xv = adapter_value(x[k], bf16);
+#pragma unroll
+            for (int r = 0; r < kRowValues; ++r) sum[r] = fmaf(xv, adapter_value(A[r][k], bf16), sum[r]);
+        }
     }
-}
-
-// D = work + bias + U h.
-template <typename E, typename O>
-__global__ void __launch_bounds__(kThreads) add_kernel(const Rows a, const float* work, const float* bias, int64_t N,
-                                                       const Stack up, const E* hidden, int64_t ldh, O* D, int64_t ldd) {
-    __shared__ float h[GEMM_ADAPTERS_MAX_RANK];
-    const int64_t i = blockIdx.x;
-    const int g = adapter_of(a, i);
-    if (threadIdx.x < a.rank) h[threadIdx.x] = load_hidden<E>(hidden + i * ldh, threadIdx.x, a.part);
+#pragma unroll
+    for (int r = 0; r < kRowValues; ++r) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum[r] += __shfl_xor_sync(~0u, sum[r], o);
+        if (lane == 0) part[warp][r] = sum[r];
+    }
     __syncthreads();
-    const int64_t n = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
-    if (n >= N) return;
-    const E* U = static_cast<const E*>(up.p) + (g < 0 ? 0 : g) * up.stride + n * up.si;
-    float y = 0.f;
-    if (g >= 0)
-        for (int r = 0; r < a.rank; ++r) y = fmaf(value(U[r * up.sj]), h[r], y);
-    y += work[i * N + n];
-    D[i * ldd + n] = rounded<O>(bias ? y + bias[n] : y);
-}
-
-// sum over an adapter's rows of left[i] right[i]^T for 16 of the rank's values and
-// 256 columns: out[g * stride + r * sr + c * sc].
-template <typename E, typename O>
-__global__ void __launch_bounds__(kThreads) factor_grad_kernel(const Rows a, const E* hidden, int64_t ldh, const E* X,
-                                                               int64_t ldx, int64_t columns, O* out, int64_t stride,
-                                                               int64_t sr, int64_t sc) {
-    const int g = blockIdx.z, r0 = blockIdx.y * 16;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    float sum[16] = {};
-    for (int64_t i = 0; i < a.M; ++i) {
-        if (adapter_of(a, i) != g) continue;
-        const float x = c < columns ? value(X[i * ldx + c]) : 0.f;
-        for (int r = 0; r < 16; ++r)
-            if (r0 + r < a.rank) sum[r] = fmaf(load_hidden<E>(hidden + i * ldh, r0 + r, a.part), x, sum[r]);
+    if (tid < kRowValues) {
+        const int r = r0 + tid;
+        float h = 0.f;
+        for (int w = 0; w < kRowThreads / 32; ++w) h += part[w][tid];
+        h = mine && r < a.rank ? (a.scale ? a.scale[g] * h : h) : 0.f;
+        uint16_t hi, lo;
+        adapter_split(h, bf16, hi, lo);
+        a.hidden[i * a.ldh + r] = hi;
+        a.hidden[i * a.ldh + a.part + r] = lo;
     }
-    if (c >= columns) return;
-    for (int r = 0; r < 16; ++r)
-        if (r0 + r < a.rank) out[g * stride + (r0 + r) * sr + c * sc] = rounded<O>(sum[r]);
 }
 
 // ---- host ------------------------------------------------------------------
 constexpr int64_t kMaxExtent = 0x7FFFF000;
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxStride = int64_t(1) << 39;      // elements: below 2^40 bytes, what a tensor map takes
+constexpr int64_t kRowsMost = 32;                     // rows that hidden_rows_kernel takes
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 bool layout_ok(gemm_layout_t l) { return l == GEMM_ROW_MAJOR || l == GEMM_COL_MAJOR; }
 
@@ -168,7 +149,8 @@ gemm_status_t check_adapters(const gemm_plan* plan, int64_t M, int64_t N, int64_
 gemm_status_t check_stack(int64_t count, const void* p, int64_t inner, int64_t ld, int64_t stride) {
     if (count == 0) return GEMM_OK;
     if (!p || ld < inner || stride < 0) return GEMM_ERR_INVALID_ARG;
-    if (ld > kMaxStride || stride > kMaxStride) return GEMM_ERR_UNSUPPORTED;
+    if (count > 1 && stride == 0) return GEMM_ERR_INVALID_ARG;
+    if (ld >= kMaxStride || stride >= kMaxStride) return GEMM_ERR_UNSUPPORTED;
     if (!aligned(p, 16) || ld % 8 || (count > 1 && stride % 8)) return GEMM_ERR_MISALIGNED;
     return GEMM_OK;
 }
@@ -176,52 +158,99 @@ gemm_status_t check_stack(int64_t count, const void* p, int64_t inner, int64_t l
 gemm_status_t check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
     if (rows == 0 || cols == 0) return GEMM_OK;
     if (!p || ld < cols) return GEMM_ERR_INVALID_ARG;
-    if (ld > kMaxStride) return GEMM_ERR_UNSUPPORTED;
+    if (ld >= kMaxStride) return GEMM_ERR_UNSUPPORTED;
     return aligned(p, 16) && ld % 8 == 0 ? GEMM_OK : GEMM_ERR_MISALIGNED;
 }
 
-Rows rows_of(const gemm_adapters_t& a, int64_t M) {
-    return {a.index, a.scale, static_cast<int32_t>(a.count), static_cast<int32_t>(a.rank), part_of(a.rank), M};
+gemm_status_t check_gradient(int64_t count, int64_t ld, int64_t stride, int64_t inner) {
+    if (count == 0) return GEMM_OK;
+    if (ld < inner || stride < 0) return GEMM_ERR_INVALID_ARG;
+    return ld >= kMaxStride || stride >= kMaxStride ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
 }
 
-gemm_status_t launched(gemm_plan* plan) {
-    if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_CUDA;
+gemm_status_t launched(gemm_plan* plan, cudaError_t e) {
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
     ++plan->launches;
     return GEMM_OK;
 }
 
-template <typename E>
-gemm_status_t run_hidden(gemm_plan* plan, const Rows& r, const void* X, int64_t ldx, int64_t K, const Stack& down,
+// One of the two tile kernels, in clusters of `splits` CTAs.
+template <typename Args>
+gemm_status_t launch_tiles(gemm_plan* plan, void (*kernel)(Args), const Args& a, int64_t ctas, bool& prepared,
+                           cudaStream_t s) {
+    const int most = tcdt::kAdapterSharedBytes + 1024;
+    if (ctas > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;
+    if (!prepared) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        prepared = true;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(tcdt::kAdapterThreads, 1, 1);
+    cfg.dynamicSmemBytes = most;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.splits > 1 ? 1 : 0;
+    return launched(plan, cudaLaunchKernelEx(&cfg, kernel, a));
+}
+
+// CTAs of a cluster: as many (a power of two) as fill two CTAs an SM once, while each has `least`
+// blocks of the long axis.
+int splits_of(const gemm_plan* plan, int64_t tiles, int64_t blocks, int64_t least) {
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= 2 * plan->sm_count && blocks >= 2 * s * least) s *= 2;
+    return s;
+}
+
+gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* X, int64_t ldx, int64_t M, int64_t K,
                          void* hidden, int64_t ldh, cudaStream_t s) {
-    if (r.M == 0) return GEMM_OK;
-    hidden_kernel<E><<<static_cast<unsigned>(r.M), kThreads, 0, s>>>(r, static_cast<const E*>(X), ldx, K, down,
-                                                                     static_cast<E*>(hidden), ldh);
-    return launched(plan);
-}
-
-template <typename E>
-gemm_status_t run_add(gemm_plan* plan, const Rows& r, const void* work, const float* bias, int64_t N, const Stack& up,
-                      const void* hidden, int64_t ldh, gemm_dtype_t out, void* D, int64_t ldd, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(r.M), static_cast<unsigned>((N + kThreads - 1) / kThreads), 1);
-    const float* w = static_cast<const float*>(work);
-    const E* h = static_cast<const E*>(hidden);
-    if (out == GEMM_F32) add_kernel<E, float><<<grid, kThreads, 0, s>>>(r, w, bias, N, up, h, ldh, static_cast<float*>(D), ldd);
-    else if (out == GEMM_F16) add_kernel<E, __half><<<grid, kThreads, 0, s>>>(r, w, bias, N, up, h, ldh, static_cast<__half*>(D), ldd);
-    else add_kernel<E, __nv_bfloat16><<<grid, kThreads, 0, s>>>(r, w, bias, N, up, h, ldh, static_cast<__nv_bfloat16*>(D), ldd);
-    return launched(plan);
-}
-
-template <typename E>
-gemm_status_t run_factor_grad(gemm_plan* plan, const Rows& r, const void* hidden, int64_t ldh, const void* X, int64_t ldx,
-                              int64_t columns, gemm_dtype_t out, void* d, int64_t stride, int64_t sr, int64_t sc,
-                              cudaStream_t s) {
-    if (!d || columns == 0 || r.count == 0) return GEMM_OK;
-    const dim3 grid(static_cast<unsigned>((columns + kThreads - 1) / kThreads), static_cast<unsigned>((r.rank + 15) / 16),
-                    static_cast<unsigned>(r.count));
-    const E *h = static_cast<const E*>(hidden), *x = static_cast<const E*>(X);
-    if (out == GEMM_F32) factor_grad_kernel<E, float><<<grid, kThreads, 0, s>>>(r, h, ldh, x, ldx, columns, static_cast<float*>(d), stride, sr, sc);
-    else factor_grad_kernel<E, E><<<grid, kThreads, 0, s>>>(r, h, ldh, x, ldx, columns, static_cast<E*>(d), stride, sr, sc);
-    return launched(plan);
+    const bool row = a.down_layout == GEMM_ROW_MAJOR;
+    const int part = part_of(a.rank);
+    const uint32_t bf16 = plan->in_dtype == GEMM_BF16 ? 1u : 0u;
+    if (row && M <= kRowsMost) {
+        const RowArgs r{static_cast<const uint16_t*>(X), ldx, K, static_cast<const uint16_t*>(a.down), a.down_ld,
+                        a.down_stride, a.index, a.scale, static_cast<int32_t>(a.count), static_cast<int32_t>(a.rank), part,
+                        static_cast<uint16_t*>(hidden), ldh, bf16};
+        hidden_rows_kernel<<<dim3(part / kRowValues, static_cast<unsigned>(M)), kRowThreads, 0, s>>>(r);
+        return launched(plan, cudaGetLastError());
+    }
+    HiddenArgs h;
+    std::memset(&h, 0, sizeof(h));
+    h.index = a.index;
+    h.scale = a.scale;
+    h.count = static_cast<int32_t>(a.count);
+    h.rank = static_cast<int32_t>(a.rank);
+    h.part = part;
+    h.rr = (h.rank + 15) / 16 * 16;
+    h.a_mn = row ? 0u : 1u;
+    h.per_stage = row ? 128 / h.rr : h.rr <= 64 ? 2 : 1;
+    h.idesc = make_idesc(true, input_format(plan->in_dtype), false, !row, 128, h.rr);
+    h.M = static_cast<int32_t>(M);
+    h.k_blocks = static_cast<int32_t>((K + 63) / 64);
+    h.splits = splits_of(plan, (M + 127) / 128, h.k_blocks, 4);
+    h.stages = tcdt::kAdapterSharedBytes / tcdt::kHiddenStage;
+    h.hidden = static_cast<uint16_t*>(hidden);
+    h.ldh = ldh;
+    h.bf16 = bf16;
+    h.status = plan->d_status;
+    h.timeout_ns = plan->timeout_ns;
+    gemm_status_t st = encode_map(plan, &h.tmX, X, K, M, ldx, 64, 128, plan->in_dtype);
+    if (st == GEMM_OK)
+        st = row ? encode_stack(plan, &h.tmA, a.down, K, a.rank, a.count, a.down_ld, a.down_stride, h.rr)
+                 : encode_stack(plan, &h.tmA, a.down, a.rank, K, a.count, a.down_ld, a.down_stride, 64);
+    if (st != GEMM_OK) return st;
+    return launch_tiles(plan, tcdt::hidden_tile_kernel, h, (M + 127) / 128 * h.splits,
+                        plan->adapters_prepared[0], s);
 }
 
 }  // namespace
@@ -232,12 +261,10 @@ int64_t gemm_adapters_hidden_width(int64_t rank) {
     return rank < 1 || rank > GEMM_ADAPTERS_MAX_RANK ? 0 : 2 * part_of(rank);
 }
 
-int64_t gemm_adapters_work_bytes(int64_t M, int64_t N) { return M > 0 && N > 0 ? M * N * 4 : 0; }
-
 gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void* X, const void* W, void* D, int64_t M, int64_t N,
                                 int64_t K, int64_t ldx, int64_t ldw, int64_t ldd, gemm_layout_t layoutW,
                                 gemm_dtype_t out_dtype, const float* bias, const gemm_adapters_t* adapters,
-                                void* hidden, int64_t ldh, void* work, void* stream) {
+                                void* hidden, int64_t ldh, void* stream) {
     gemm_status_t st = check_adapters(plan, M, N, K, out_dtype, adapters);
     if (st != GEMM_OK) return st;
     const gemm_adapters_t& a = *adapters;
@@ -251,24 +278,28 @@ gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void* X, const void* W, 
     if (st == GEMM_OK) st = check_matrix(X, M, K, ldx);
     if (st == GEMM_OK) st = check_matrix(hidden, M, 2 * part_of(a.rank), ldh);
     if (st != GEMM_OK) return st;
-    if (gemm_adapters_work_bytes(M, N) > 0 && !work) return GEMM_ERR_INVALID_ARG;
-    if (!aligned(bias, 4) || !aligned(work, 16)) return GEMM_ERR_MISALIGNED;
+    if (!aligned(bias, 4)) return GEMM_ERR_MISALIGNED;
     if (M == 0) return GEMM_OK;
     const OnDevice on(plan->device);
     if (!on.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Rows r = rows_of(a, M);
-    const Stack down{a.down, a.down_stride, down_row ? a.down_ld : 1, down_row ? 1 : a.down_ld};
-    const Stack up{a.up, a.up_stride, up_row ? a.up_ld : 1, up_row ? 1 : a.up_ld};
-    const bool half = plan->in_dtype == GEMM_F16;
-    st = half ? run_hidden<__half>(plan, r, X, ldx, K, down, hidden, ldh, s)
-              : run_hidden<__nv_bfloat16>(plan, r, X, ldx, K, down, hidden, ldh, s);
+    if (K == 0 || a.count == 0) {
+        // no adapter adds anything
+        st = launched(plan, cudaMemset2DAsync(hidden, ldh * 2, 0, 4 * part_of(a.rank), M, s));
+        if (st != GEMM_OK || N == 0) return st;
+        const gemm_epilogue_t ep{bias, nullptr, nullptr, GEMM_ACT_NONE};
+        return gemm_run_ep(plan, X, W, nullptr, D, M, N, K, ldx, ldw, ldd, GEMM_ROW_MAJOR, layoutW, GEMM_F32, out_dtype,
+                           1.0f, 0.0f, &ep, stream);
+    }
+    Choice ch;
+    if (N > 0) {
+        st = choose_adapters(plan, M, N, K, layoutW, out_dtype, s, &ch);
+        if (st != GEMM_OK) return st;
+    }
+    st = run_hidden(plan, a, X, ldx, M, K, hidden, ldh, s);
     if (st != GEMM_OK || N == 0) return st;
-    st = gemm_run(plan, X, W, nullptr, work, M, N, K, ldx, ldw, N, GEMM_ROW_MAJOR, layoutW, GEMM_F32, GEMM_F32, 1.0f,
-                  0.0f, stream);
-    if (st != GEMM_OK) return st;
-    return half ? run_add<__half>(plan, r, work, bias, N, up, hidden, ldh, out_dtype, D, ldd, s)
-                : run_add<__nv_bfloat16>(plan, r, work, bias, N, up, hidden, ldh, out_dtype, D, ldd, s);
+    const AdapterProblem p{a.index, a.count, a.rank, part_of(a.rank), hidden, ldh, a.up, a.up_ld, a.up_stride, a.up_layout};
+    return launch_adapters(plan, ch, X, W, D, M, N, K, ldx, ldw, ldd, layoutW, out_dtype, bias, p, s);
 }
 
 gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD, int64_t M, int64_t N, int64_t K,
@@ -279,35 +310,54 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     if (st != GEMM_OK) return st;
     if (out_dtype != GEMM_F32 && out_dtype != plan->in_dtype) return GEMM_ERR_UNSUPPORTED;
     const gemm_adapters_t& a = *adapters;
-    const int64_t width = 2 * part_of(a.rank);
+    const int part = part_of(a.rank);
     if (d_down) {
         st = check_matrix(X, M, K, ldx);
-        if (st == GEMM_OK) st = check_matrix(p, M, width, ldh);
-        if (st == GEMM_OK && (down_ld < K || down_stride < 0)) st = GEMM_ERR_INVALID_ARG;
-        if (st == GEMM_OK && (down_ld > kMaxStride || down_stride > kMaxStride)) st = GEMM_ERR_UNSUPPORTED;
+        if (st == GEMM_OK) st = check_matrix(p, M, 2 * part, ldh);
+        if (st == GEMM_OK) st = check_gradient(a.count, down_ld, down_stride, K);
     }
     if (d_up && st == GEMM_OK) {
         st = check_matrix(dD, M, N, lddd);
-        if (st == GEMM_OK) st = check_matrix(h, M, width, ldh);
-        if (st == GEMM_OK && (up_ld < a.rank || up_stride < 0)) st = GEMM_ERR_INVALID_ARG;
-        if (st == GEMM_OK && (up_ld > kMaxStride || up_stride > kMaxStride)) st = GEMM_ERR_UNSUPPORTED;
+        if (st == GEMM_OK) st = check_matrix(h, M, 2 * part, ldh);
+        if (st == GEMM_OK) st = check_gradient(a.count, up_ld, up_stride, a.rank);
     }
     if (st != GEMM_OK) return st;
     const uintptr_t esz = out_dtype == GEMM_F32 ? 4 : 2;
     if (!aligned(d_down, esz) || !aligned(d_up, esz)) return GEMM_ERR_MISALIGNED;
-    if (a.count == 0 || (!d_down && !d_up)) return GEMM_OK;
+    FactorGradArgs f;
+    std::memset(&f, 0, sizeof(f));
+    if (d_down) f.f[0].blocks = static_cast<int32_t>((K + 127) / 128);
+    if (d_up) f.f[1].blocks = static_cast<int32_t>((N + 127) / 128);
+    const int64_t items = a.count * (f.f[0].blocks + static_cast<int64_t>(f.f[1].blocks));
+    if (items == 0) return GEMM_OK;
     const OnDevice on(plan->device);
     if (!on.ok) return GEMM_ERR_CUDA;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Rows r = rows_of(a, M);
-    if (plan->in_dtype == GEMM_F16) {
-        st = run_factor_grad<__half>(plan, r, p, ldh, X, ldx, K, out_dtype, d_down, down_stride, down_ld, 1, s);
-        if (st == GEMM_OK) st = run_factor_grad<__half>(plan, r, h, ldh, dD, lddd, N, out_dtype, d_up, up_stride, 1, up_ld, s);
-    } else {
-        st = run_factor_grad<__nv_bfloat16>(plan, r, p, ldh, X, ldx, K, out_dtype, d_down, down_stride, down_ld, 1, s);
-        if (st == GEMM_OK) st = run_factor_grad<__nv_bfloat16>(plan, r, h, ldh, dD, lddd, N, out_dtype, d_up, up_stride, 1, up_ld, s);
+    const void* left[2] = {X, dD};
+    const void* right[2] = {p, h};
+    const int64_t columns[2] = {K, N}, ld[2] = {ldx, lddd};
+    for (int i = 0; i < 2 && M > 0; ++i) {
+        if (f.f[i].blocks == 0) continue;
+        st = encode_map(plan, &f.f[i].tmX, left[i], columns[i], M, ld[i], 64, 64, plan->in_dtype);
+        if (st == GEMM_OK) st = encode_map(plan, &f.f[i].tmH, right[i], 2 * part, M, ldh, 64, 64, plan->in_dtype);
+        if (st != GEMM_OK) return st;
     }
-    return st;
+    f.f[0].out = d_down, f.f[0].stride = down_stride, f.f[0].sr = down_ld, f.f[0].sc = 1;
+    f.f[1].out = d_up, f.f[1].stride = up_stride, f.f[1].sr = 1, f.f[1].sc = up_ld;
+    f.f[0].columns = static_cast<int32_t>(K), f.f[1].columns = static_cast<int32_t>(N);
+    f.index = a.index;
+    f.rank = static_cast<int32_t>(a.rank);
+    f.part = part;
+    f.idesc = make_idesc(true, input_format(plan->in_dtype), true, true, 128, 2 * part);
+    f.M = M;
+    const int stage = tcdt::factor_stage_bytes(part);
+    f.stages = tcdt::kAdapterSharedBytes / stage;
+    if (f.stages > tcdt::kAdapterMaxStages) f.stages = tcdt::kAdapterMaxStages;
+    f.splits = splits_of(plan, items, (M + 63) / 64, 4);
+    f.out_kind = out_dtype == GEMM_F32 ? 0u : out_dtype == GEMM_F16 ? 1u : 2u;
+    f.status = plan->d_status;
+    f.timeout_ns = plan->timeout_ns;
+    return launch_tiles(plan, tcdt::factor_grad_kernel, f, items * f.splits, plan->adapters_prepared[1],
+                        static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

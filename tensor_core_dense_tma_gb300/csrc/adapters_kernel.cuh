@@ -1,0 +1,491 @@
+// adapters_kernel.cuh -- the low-rank products of adapters.cu on the tensor cores:
+// h = s A X of 128 rows at a time, and the gradients of the factors.
+//
+// Both read a long operand once (X, or dD) and multiply it by something narrow,
+// so both are bound by that operand's stream: tiles are as wide as an MMA is tall
+// (128), the narrow side is its N, and the long axis (K, or the rows) is shared by a
+// cluster of CTAs whose fp32 sums meet through distributed shared memory, in the
+// order of their ranges.  Every wait is bounded as in gemm_kernel.cuh.
+#pragma once
+
+#include "gemm_kernel.cuh"
+
+namespace tcdt {
+
+constexpr int kAdapterThreads = 192;                  // producer, MMA and four epilogue warps
+constexpr int kAdapterSharedBytes = 96 * 1024;        // of stages: two CTAs an SM
+constexpr int kAdapterMaxStages = 6;
+constexpr uint32_t kChunk = 8192;                     // 64 x 64 16-bit elements
+
+// Barriers of the two kernels, in static shared memory.
+struct AdapterPipe {
+    uint64_t full[kAdapterMaxStages], ready[kAdapterMaxStages], empty[kAdapterMaxStages], acc;
+    uint32_t tmem;
+    int abort_flag, drained;
+};
+
+__device__ __forceinline__ void adapter_pipe_init(AdapterPipe& q, int stages) {
+    for (int i = 0; i < stages; ++i) {
+        mbar_init(smem_addr(&q.full[i]), 1);
+        mbar_init(smem_addr(&q.ready[i]), 4);
+        mbar_init(smem_addr(&q.empty[i]), 1);
+    }
+    mbar_init(smem_addr(&q.acc), 1);
+    q.abort_flag = 0;
+    fence_mbar_init();
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint16_t adapter_bits(float x, bool bf16) {
+    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+}
+
+// h as its two parts; an infinity or a NaN is all in the high one.
+__device__ __forceinline__ void adapter_split(float h, bool bf16, uint16_t& high, uint16_t& low) {
+    high = adapter_bits(h, bf16);
+    const float x = adapter_value(high, bf16);
+    low = adapter_bits(isfinite(x) ? h - x : 0.0f, bf16);
+}
+
+// Stage and phase of a ring.
+struct RingAt {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++stage == stages) stage = 0, phase ^= 1u;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// h = s A X
+// ---------------------------------------------------------------------------
+struct HiddenArgs {
+    CUtensorMap tmX;          // boxes of 64 x 128 rows
+    CUtensorMap tmA;          // [adapter][rank][K], boxes of 64 x rr, or [adapter][K][rank], of 64 x 64
+    const int32_t* index;
+    const float* scale;
+    int32_t count, rank, part;
+    int32_t rr;               // the rank in whole 16s: N of the MMAs
+    int32_t per_stage;        // adapters of a stage
+    uint32_t a_mn;            // 1: down factors are rank-contiguous
+    uint32_t idesc;
+    int32_t M, k_blocks, splits, stages;
+    uint16_t* hidden;
+    int64_t ldh;
+    uint32_t bf16;
+    int* status;
+    uint64_t timeout_ns;
+};
+
+constexpr int kHiddenStage = 128 * 128 + 128 * 128;
+
+// A cluster of a.splits CTAs computes 128 rows.  All adapters of a tile
+// accumulate in the same columns of tensor memory, each in its own rows (MMAs
+// that leave the others as they are), so one pass over X serves any number; with more
+// than fit a stage, X comes again from L2 with the next ones.
+// 8192 x 8192 bf16, 4 adapters of rank 64: see the table of DESIGN.
+__global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __grid_constant__ HiddenArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ AdapterPipe q;
+    __shared__ int list[128], listed;
+    __shared__ uint32_t off[128][4];          // rows that are not the adapter's
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int row0 = static_cast<int>(blockIdx.x / a.splits) * 128;
+    const uint32_t tmem_cols = a.rr <= 32 ? 32u : a.rr <= 64 ? 64u : 128u;
+    const bool bf16 = a.bf16 != 0;
+
+    griddep_launch();
+    if (warp == 0) {
+        if (lane == 0) adapter_pipe_init(q, a.stages);
+        AdapterWalk<128> walk(a.index, a.count, row0, a.M, lane);
+        uint32_t m[4];
+        int g, n = 0;
+        while (walk.next(g, m)) {
+            if (lane == 0) {
+                list[n] = g;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) off[n][w] = m[w];
+            }
+            ++n;
+        }
+        if (lane == 0) listed = n;
+        __syncwarp();
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(smem_addr(&q.tmem), tmem_cols);
+        tmem_relinquish_alloc_permit<1>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = q.tmem;
+    const int n = listed;
+    const int kb0 = a.k_blocks * rank / a.splits, kb1 = a.k_blocks * (rank + 1) / a.splits;
+    const int groups = (n + a.per_stage - 1) / a.per_stage;
+    const uint32_t a_bytes = a.a_mn ? (a.rr <= 64 ? kChunk : 2 * kChunk) : static_cast<uint32_t>(a.rr) * 128u;
+    const WaitCtx wctx{a.status, a.timeout_ns, &q.abort_flag};
+    auto stage_at = [&](int s) { return base + static_cast<uint32_t>(s) * kHiddenStage; };
+    bool ok = true;
+
+    if (warp == 0) {
+        RingAt at;
+        int64_t issued = 0;
+        for (int kb = kb0; ok && kb < kb1; ++kb)
+            for (int j = 0; j < groups; ++j) {
+                if (!warp_wait_phase(smem_addr(&q.empty[at.stage]), at.phase ^ 1u, wctx, kSiteProducerEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = smem_addr(&q.full[at.stage]), sx = stage_at(at.stage), sa = sx + 128 * 128;
+                const int first = j * a.per_stage, here = min(a.per_stage, n - first);
+                if (elect_one_sync()) {
+                    mbar_arrive_expect_tx(bar, 128 * 128 + here * a_bytes);
+                    tma_load_2d(sx, &a.tmX, bar, 64 * kb, row0);
+                    for (int i = 0; i < here; ++i) {
+                        const int g = list[first + i];
+                        const uint32_t dst = sa + i * a_bytes;
+                        if (a.a_mn) {
+                            tma_load_3d(dst, &a.tmA, bar, 0, 64 * kb, g);
+                            if (a.rr > 64) tma_load_3d(dst + kChunk, &a.tmA, bar, 64, 64 * kb, g);
+                        } else {
+                            tma_load_3d(dst, &a.tmA, bar, 64 * kb, 0, g);
+                        }
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                at.next(a.stages);
+            }
+        if (!ok) {
+            // wind down: let the copies already issued land before exiting
+            for (int i = 0; i < a.stages && i < issued; ++i) {
+                if (--at.stage < 0) at.stage = a.stages - 1, at.phase ^= 1u;
+                wait_phase_drain(smem_addr(&q.full[at.stage]), at.phase, 100000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        RingAt at;
+        const uint32_t lbo = a.a_mn ? kChunk : 16u, kstep = a.a_mn ? 16u * 128u : 32u;
+        for (int kb = kb0; ok && kb < kb1; ++kb)
+            for (int j = 0; j < groups; ++j) {
+                if (!warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteMmaFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t sx = stage_at(at.stage), sa = sx + 128 * 128;
+                const int first = j * a.per_stage, here = min(a.per_stage, n - first);
+                if (elect_one_sync()) {
+                    for (int i = 0; i < here; ++i) {
+                        const uint32_t m[4] = {off[first + i][0], off[first + i][1], off[first + i][2], off[first + i][3]};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_f16_ss_rows<1>(tmem, smem_desc_sw128(sx + k * 32u, 16u, 1024u),
+                                                smem_desc_sw128(sa + i * a_bytes + k * kstep, lbo, 1024u), a.idesc, m,
+                                                kb != kb0 || k != 0 ? 1u : 0u);
+                    }
+                    umma_commit<1>(smem_addr(&q.empty[at.stage]));
+                }
+                __syncwarp();
+                at.next(a.stages);
+            }
+        if (elect_one_sync()) umma_commit<1>(smem_addr(&q.acc));
+        __syncwarp();
+        if (!ok) wait_phase_drain(smem_addr(&q.acc), 0, 100000000ull);
+    }
+    __syncwarp();
+    // the four epilogue warps: this CTA's sums of 128 rows, in shared memory, rows rr + 4 apart
+    const int pitch = a.rr + 4;
+    float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_addr(smem_raw)));
+    const int t = static_cast<int>(threadIdx.x) - 64;
+    if (warp >= 2) {
+        ok = warp_wait_phase(smem_addr(&q.acc), 0, wctx, kSiteEpilogueAccFull);
+        if (ok && n > 0) {
+            tc_fence_after_sync();
+            const int quad = warp & 3, row = 32 * quad + lane;
+            for (int c = 0; c < a.rr; c += 16) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * quad) << 16) + c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<uint4*>(sums + row * pitch + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+            }
+            tc_fence_before_sync();
+        }
+        __syncwarp();
+    }
+    if (a.splits > 1) cluster_sync_all();
+    else __syncthreads();
+    if (warp >= 2) {
+        // this CTA's share of the rows: sums of all ranges in their order, four columns a thread
+        const int rows = 128 / a.splits, quads = a.part / 4;
+        for (int i = t; i < rows * quads; i += 128) {
+            const int row = rank * rows + i / quads, c = i % quads * 4;
+            if (row0 + row >= a.M) continue;
+            const int g = __ldg(a.index + row0 + row);
+            float v[4] = {};
+            if (g >= 0 && g < a.count && c < a.rr) {
+                const uint32_t from = smem_addr(sums + row * pitch + c);
+                for (int s = 0; s < a.splits; ++s) {
+                    const uint32_t p = a.splits > 1 ? map_to_cta(from, static_cast<uint32_t>(s)) : from;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += a.splits > 1 ? ld_cluster_f32(p + 4u * e) : ld_shared_f32(p + 4u * e);
+                }
+                const float scale = a.scale ? __ldg(a.scale + g) : 1.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = c + e < a.rank ? v[e] * scale : 0.0f;
+            }
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) adapter_split(v[e], bf16, hi[e], lo[e]);
+            uint16_t* out = a.hidden + (row0 + row) * a.ldh + c;
+            *reinterpret_cast<uint2*>(out) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(out + a.part) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        }
+    }
+    __syncwarp();
+    // nobody leaves while its sums may still be read
+    if (a.splits > 1) cluster_sync_all();
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem, tmem_cols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradients of the factors: for an adapter g, sum over its rows of x[i] h[i]^T
+// ---------------------------------------------------------------------------
+struct FactorArgs {
+    CUtensorMap tmX, tmH;     // of each 64 x 64 boxes
+    void* out;                // element (g, r, c) at out[g * stride + r * sr + c * sc]
+    int64_t stride, sr, sc;
+    int32_t columns, blocks;  // blocks of 128 columns
+};
+
+struct FactorGradArgs {
+    FactorArgs f[2];          // down (X and p) and up (dD and h)
+    const int32_t* index;
+    int32_t rank, part;
+    uint32_t idesc;
+    int64_t M;
+    int32_t splits, stages;
+    uint32_t out_kind;        // 0 fp32, 1 fp16, 2 bf16
+    int* status;
+    uint64_t timeout_ns;
+};
+
+constexpr int kFactorWindow = 1024;       // tiles of 64 rows looked through at once
+constexpr int kFactorPitch = 129;         // of the sums in shared memory: both orders of reading free of conflicts
+
+__host__ __device__ constexpr int factor_stage_bytes(int part) { return 2 * 8192 + (part <= 32 ? 1 : part / 32) * 8192; }
+
+// A cluster of a.splits CTAs computes the gradient of 128 columns of one factor:
+// the 64-row tiles that hold rows of the adapter, in their order, are shared out
+// evenly.  Both operands are read as they lie (the sum runs over their rows, so
+// both are MN-major).  In a tile that has other rows too, the epilogue warps
+// zero those of both operands in shared memory first: zeros in h alone would let an
+// infinity in x through.
+__global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __grid_constant__ FactorGradArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ AdapterPipe q;
+    __shared__ uint8_t holds[kFactorWindow];          // 0: no row of g, 1: some, 2: nothing else
+    __shared__ uint16_t list[kFactorWindow];          // tiles with rows of g; bit 15: others too
+    __shared__ int listed;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int64_t item = blockIdx.x / a.splits;
+    const int blocks = a.f[0].blocks + a.f[1].blocks;
+    const int g = static_cast<int>(item / blocks);
+    int block = static_cast<int>(item % blocks);
+    const int which = block >= a.f[0].blocks ? 1 : 0;
+    if (which) block -= a.f[0].blocks;
+    const FactorArgs& f = a.f[which];
+    const int col0 = 128 * block;
+    const int chunks = a.part <= 32 ? 1 : a.part / 32;     // of h
+    const uint32_t stage_bytes = static_cast<uint32_t>(factor_stage_bytes(a.part));
+    const uint32_t tmem_cols = 2u * static_cast<uint32_t>(a.part);
+    if (threadIdx.x == 0) adapter_pipe_init(q, a.stages);
+    if (warp == 1) {
+        tmem_alloc<1>(smem_addr(&q.tmem), tmem_cols);
+        tmem_relinquish_alloc_permit<1>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = q.tmem;
+    const WaitCtx wctx{a.status, a.timeout_ns, &q.abort_flag};
+    auto stage_at = [&](int s) { return base + static_cast<uint32_t>(s) * stage_bytes; };
+    RingAt at;
+    bool ok = true;
+    int64_t used = 0;                    // stages that this CTA has gone through
+
+    for (int64_t w0 = 0; w0 * 64 < a.M; w0 += kFactorWindow) {
+        const int tiles = static_cast<int>(min(static_cast<int64_t>(kFactorWindow), (a.M + 63) / 64 - w0));
+        // eight tiles a warp at a time, so that their loads overlap
+        for (int t0 = warp * 8; t0 < tiles; t0 += 6 * 8) {
+            int x[8][2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t row = (w0 + t0 + i) * 64 + 32 * h + lane;
+                    x[i][h] = t0 + i < tiles && row < a.M ? __ldg(a.index + row) : g;
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool all = __all_sync(0xffffffffu, x[i][0] == g && x[i][1] == g);
+                const bool any = __any_sync(0xffffffffu, x[i][0] == g || x[i][1] == g);
+                if (lane == 0 && t0 + i < tiles) holds[t0 + i] = all ? 2 : any ? 1 : 0;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int n = 0;
+            for (int t0 = 0; t0 < tiles; t0 += 32) {
+                const int h = t0 + lane < tiles ? holds[t0 + lane] : 0;
+                const uint32_t some = __ballot_sync(0xffffffffu, h != 0);
+                if (h) list[n + __popc(some & ((1u << lane) - 1u))] = static_cast<uint16_t>((t0 + lane) | (h == 1 ? 0x8000 : 0));
+                n += __popc(some);
+            }
+            if (lane == 0) listed = n;
+        }
+        __syncthreads();
+        const int first = listed * rank / a.splits, last = listed * (rank + 1) / a.splits;
+        if (warp == 0) {
+            for (int i = first; ok && i < last; ++i) {
+                if (!warp_wait_phase(smem_addr(&q.empty[at.stage]), at.phase ^ 1u, wctx, kSiteProducerEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = smem_addr(&q.full[at.stage]), sx = stage_at(at.stage), sh = sx + 2 * kChunk;
+                const int row = static_cast<int>((w0 + (list[i] & 0x7FFF)) * 64);
+                if (elect_one_sync()) {
+                    mbar_arrive_expect_tx(bar, stage_bytes);
+                    tma_load_2d(sx, &f.tmX, bar, col0, row);
+                    tma_load_2d(sx + kChunk, &f.tmX, bar, col0 + 64, row);
+                    for (int c = 0; c < chunks; ++c) tma_load_2d(sh + c * kChunk, &f.tmH, bar, 64 * c, row);
+                }
+                __syncwarp();
+                ++used;
+                at.next(a.stages);
+            }
+        } else if (warp == 1) {
+            for (int i = first; ok && i < last; ++i) {
+                if (!warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteMmaFull) ||
+                    !warp_wait_phase(smem_addr(&q.ready[at.stage]), at.phase, wctx, kSiteMmaFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t sx = stage_at(at.stage), sh = sx + 2 * kChunk;
+                if (elect_one_sync()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f16_ss<1>(tmem, smem_desc_sw128(sx + k * 2048u, kChunk, 1024u),
+                                       smem_desc_sw128(sh + k * 2048u, kChunk, 1024u), a.idesc, used || k ? 1u : 0u);
+                    umma_commit<1>(smem_addr(&q.empty[at.stage]));
+                }
+                __syncwarp();
+                ++used;
+                at.next(a.stages);
+            }
+        } else {
+            for (int i = first; ok && i < last; ++i) {
+                if (!warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteEpilogueAccFull)) {
+                    ok = false;
+                    break;
+                }
+                if (list[i] & 0x8000) {
+                    const int row = (static_cast<int>(threadIdx.x) - 64) >> 1;      // two threads a row of 128 bytes a chunk
+                    const int64_t at_row = (w0 + (list[i] & 0x7FFF)) * 64 + row;
+                    if (at_row < a.M && __ldg(a.index + at_row) != g) {
+                        const uint32_t s = stage_at(at.stage) + static_cast<uint32_t>(row) * 128u + (threadIdx.x & 1u) * 64u;
+                        for (int c = 0; c < 2 + chunks; ++c)
+#pragma unroll
+                            for (int b = 0; b < 64; b += 16) st_shared_v4(s + c * kChunk + b, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&q.ready[at.stage]));
+                ++used;
+                at.next(a.stages);
+            }
+        }
+        __syncwarp();
+        __syncthreads();      // the list is done with
+    }
+    if (warp == 0 && !ok) {
+        for (int i = 0; i < a.stages && i < used; ++i) {
+            if (--at.stage < 0) at.stage = a.stages - 1, at.phase ^= 1u;
+            wait_phase_drain(smem_addr(&q.full[at.stage]), at.phase, 100000000ull);
+        }
+    }
+    if (warp == 1) {
+        if (elect_one_sync()) umma_commit<1>(smem_addr(&q.acc));
+        __syncwarp();
+        if (!ok) wait_phase_drain(smem_addr(&q.acc), 0, 100000000ull);
+    }
+    __syncwarp();
+    // the sums of this CTA's rows, [rank][column], in shared memory
+    float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_addr(smem_raw)));
+    if (warp >= 2) {
+        ok = ok && warp_wait_phase(smem_addr(&q.acc), 0, wctx, kSiteEpilogueAccFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tc_fence_after_sync();
+            const int quad = warp & 3;
+            float* to = sums + 32 * quad + lane;
+            for (int r = 0; r < a.rank; r += 16) {
+                uint32_t hi[16], lo[16];
+                if (used) {
+                    const uint32_t from = tmem + (static_cast<uint32_t>(32 * quad) << 16) + r;
+                    tmem_ld_32x32b_x16(from, hi);
+                    tmem_ld_32x32b_x16(from + a.part, lo);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (r + i < a.rank)
+                        to[(r + i) * kFactorPitch] = used ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : 0.0f;
+            }
+            tc_fence_before_sync();
+        }
+        __syncwarp();
+    }
+    if (a.splits > 1) cluster_sync_all();
+    else __syncthreads();
+    // joined and stored, an equal share by each CTA, in the order of the output's memory
+    const bool by_rank = f.sr == 1;            // consecutive in memory: rank, else columns
+    const int total = a.rank * 128, share = (total + a.splits - 1) / a.splits;
+    for (int i = rank * share + threadIdx.x; i < min(total, (rank + 1) * share); i += kAdapterThreads) {
+        const int r = by_rank ? i % a.rank : i / 128, c = by_rank ? i / a.rank : i % 128;
+        if (col0 + c >= f.columns) continue;
+        const uint32_t from = smem_addr(sums + r * kFactorPitch + c);
+        float v = 0.0f;
+        for (int s = 0; s < a.splits; ++s)
+            v += a.splits > 1 ? ld_cluster_f32(map_to_cta(from, static_cast<uint32_t>(s))) : ld_shared_f32(from);
+        const int64_t o = g * f.stride + r * f.sr + (col0 + c) * f.sc;
+        if (a.out_kind == 0) static_cast<float*>(f.out)[o] = v;
+        else static_cast<uint16_t*>(f.out)[o] = adapter_bits(v, a.out_kind == 2);
+    }
+    __syncwarp();
+    if (a.splits > 1) cluster_sync_all();
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem, tmem_cols);
+    }
+}
+
+}  // namespace tcdt

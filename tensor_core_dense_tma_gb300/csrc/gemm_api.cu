@@ -507,6 +507,37 @@ gemm_status_t run_keep_nan(gemm_plan* plan, const void* A, const void* B, void* 
     return launch_pair256_ep_nan(plan, out_slot(GEMM_F32, out), ch, pr, D, ldd, s);
 }
 
+gemm_status_t choose_adapters(gemm_plan* plan, int64_t M, int64_t N, int64_t K, gemm_layout_t layoutW,
+                              gemm_dtype_t out, cudaStream_t s, Choice* ch) {
+    bool valid = true;
+    *ch = select_choice(plan, M, N, K, GEMM_ROW_MAJOR, layoutW, GEMM_F32, out, &valid, nullptr);
+    if (!valid) return GEMM_ERR_UNSUPPORTED;
+    if (!ch->early) return GEMM_OK;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess ||
+        (capture != cudaStreamCaptureStatusNone &&
+         cudaMemsetAsync(plan->d_flags, 0, kNumCounters * sizeof(unsigned), s) != cudaSuccess)) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
+gemm_status_t launch_adapters(gemm_plan* plan, const Choice& ch, const void* X, const void* W, void* D, int64_t M,
+                              int64_t N, int64_t K, int64_t ldx, int64_t ldw, int64_t ldd, gemm_layout_t layoutW,
+                              gemm_dtype_t out, const float* bias, const AdapterProblem& a, cudaStream_t s) {
+    const gemm_epilogue_t ep{bias, nullptr, nullptr, GEMM_ACT_NONE};
+    const Problem pr = make_problem(ch.swap, X, W, M, N, K, ldx, ldw, GEMM_ROW_MAJOR, layoutW, &ep);
+    const int slot = out_slot(GEMM_F32, out);
+    switch (ch.kind) {
+        case kCfgSingle16: return launch_single16_adapters(plan, slot, ch, pr, D, ldd, a, s);
+        case kCfgSingle64: return launch_single64_adapters(plan, slot, ch, pr, D, ldd, a, s);
+        case kCfgSingle256: return launch_single256_adapters(plan, slot, ch, pr, D, ldd, a, s);
+        case kCfgPair224: return launch_pair224_adapters(plan, slot, ch, pr, D, ldd, a, s);
+        default: return launch_pair256_adapters(plan, slot, ch, pr, D, ldd, a, s);
+    }
+}
+
 }  // namespace tcdt_host
 
 extern "C" {

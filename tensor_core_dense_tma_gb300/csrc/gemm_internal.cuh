@@ -129,13 +129,14 @@ struct gemm_plan {
     uint64_t timeout_ns = 2000000000ull;
     uint64_t launches = 0;
     tcdt_host::EncodeTiledFn encode = nullptr;
-    bool attr_set[tcdt_host::kNumCfgKinds][12] = {};  // [kind][output slot + 4 * epilogue form]
+    bool attr_set[tcdt_host::kNumCfgKinds][16] = {};  // [kind][output slot + 4 * epilogue form, 3: with adapters]
     int units[tcdt_host::kNumCfgKinds] = {};  // co-resident CTAs (single) or CTA pairs (pair)
     size_t ws_bytes = 0;          // capacity of d_ws
     void* d_i8[tcdt_host::kI8Buffers] = {};   // gemm_run_i8's codes and row scales: the last one is in use (owned)
     int i8_buffers = 0;
     size_t i8_bytes = 0;          // capacity of the last of them
     bool i8_prepared[5][3] = {};  // its kernels' shared-memory opt-in done ([tile][output])
+    bool adapters_prepared[2] = {};   // the same for hidden_tile_kernel and factor_grad_kernel
     int forced_kind = -1;         // gemm_plan_force_config
 #ifdef TCDT_FAULT_INJECTION
     int64_t fi_skip_load = -1;    // test builds only
@@ -215,6 +216,36 @@ TCDT_DECLARE_KIND_IN(pair256, tf32)
 gemm_status_t launch_pair256_ep_nan(gemm_plan* plan, int slot, const Choice& ch, const Problem& pr, void* D,
                                     int64_t ldd, cudaStream_t s);
 
+// The adapters of a product D = X W + bias (see adapters.h): h as it was left by
+// the kernel launched before, and the up factors.
+struct AdapterProblem {
+    const int32_t* index;
+    int64_t count, rank;
+    int part;                        // columns of h's high parts
+    const void* hidden;
+    int64_t ldh;
+    const void* up;
+    int64_t up_ld, up_stride;
+    gemm_layout_t up_layout;
+};
+#define TCDT_DECLARE_ADAPTERS(name)                                                                      \
+    gemm_status_t launch_##name##_adapters(gemm_plan* plan, int slot, const Choice& ch, const Problem& pr, void* D, \
+                                           int64_t ldd, const AdapterProblem& a, cudaStream_t s);
+TCDT_DECLARE_ADAPTERS(single16)
+TCDT_DECLARE_ADAPTERS(single64)
+TCDT_DECLARE_ADAPTERS(single256)
+TCDT_DECLARE_ADAPTERS(pair256)
+TCDT_DECLARE_ADAPTERS(pair224)
+#undef TCDT_DECLARE_ADAPTERS
+// D = X W + bias + adapters of checked arguments, fp32 accumulation, X row-major,
+// M, N, K > 0: the configuration (its flags reset where `s` is being captured:
+// a graph's launches all have one tag), then the launch.
+gemm_status_t choose_adapters(gemm_plan* plan, int64_t M, int64_t N, int64_t K, gemm_layout_t layoutW,
+                              gemm_dtype_t out, cudaStream_t s, Choice* ch);
+gemm_status_t launch_adapters(gemm_plan* plan, const Choice& ch, const void* X, const void* W, void* D, int64_t M,
+                              int64_t N, int64_t K, int64_t ldx, int64_t ldw, int64_t ldd, gemm_layout_t layoutW,
+                              gemm_dtype_t out, const float* bias, const AdapterProblem& a, cudaStream_t s);
+
 // gemm_run_ep's D = act(rs cs A B + bias) of checked arguments, fp32 accumulation, A
 // row-major and B column-major, whose ReLU keeps a NaN.
 gemm_status_t run_keep_nan(gemm_plan* plan, const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
@@ -260,6 +291,23 @@ inline gemm_status_t encode_map(gemm_plan* plan, CUtensorMap* map, const void* p
     return GEMM_OK;
 }
 
+// 3-D tensor map over a stack of matrices of 16-bit elements, `outer` rows of `inner`
+// contiguous elements each, 128-byte swizzle, zero fill outside.
+inline gemm_status_t encode_stack(gemm_plan* plan, CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer,
+                                  uint64_t count, uint64_t ld, uint64_t stride, uint32_t box_outer) {
+    // (a stack of one has no stride of its own, but the map wants one)
+    const cuuint64_t dims[3] = {inner, outer, count};
+    const cuuint64_t strides[2] = {ld * 2, (count > 1 ? stride : ld) * 2};
+    const cuuint32_t box[3] = {64, box_outer, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType dt =
+        plan->in_dtype == GEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = plan->encode(map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
 // tcgen05 instruction descriptor (kind::f16, kind::tf32, kind::f8f6f4):
 //   [4,6) D type (0 f16, 1 f32)   [7,10) A format   [10,13) B format (input_format)
 //   [15] A MN-major   [16] B MN-major   [17,23) N >> 3   [24,29) M >> 4
@@ -290,16 +338,17 @@ void fill_launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, cuda
 }
 
 // Shared-memory opt-in and co-residency of one kernel instantiation.
-template <class Cfg, int EP = tcdt::kEpNone>
+template <class Cfg, int EP = tcdt::kEpNone, class AD = tcdt::NoAdapters>
 gemm_status_t prepare(gemm_plan* plan, int kind, int slot) {
-    if (plan->attr_set[kind][slot + 4 * EP]) return GEMM_OK;
-    auto kern = tcdt::gemm_sm103_kernel<Cfg, EP>;
+    constexpr int form = AD::kOn ? 3 : EP;
+    if (plan->attr_set[kind][slot + 4 * form]) return GEMM_OK;
+    auto kern = tcdt::gemm_sm103_kernel<Cfg, EP, AD>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     fill_launch_config<Cfg>(cfg, attr, nullptr);
     cfg.gridDim = dim3(Cfg::CG * (plan->sm_count / Cfg::CG), 1, 1);
     int units = 0;
@@ -314,7 +363,7 @@ gemm_status_t prepare(gemm_plan* plan, int kind, int slot) {
     cudaGetLastError();
     if (units <= 0) units = plan->sm_count / Cfg::CG;
     if (plan->units[kind] == 0 || units < plan->units[kind]) plan->units[kind] = units;
-    plan->attr_set[kind][slot + 4 * EP] = true;
+    plan->attr_set[kind][slot + 4 * form] = true;
     return GEMM_OK;
 }
 
@@ -359,9 +408,10 @@ inline int fill_schedule(KernelParams& p, const Choice& ch, int64_t M, int64_t N
     return work < ch.units ? static_cast<int>(work) : ch.units;
 }
 
-template <class Cfg, int EP = tcdt::kEpNone>
+template <class Cfg, int EP = tcdt::kEpNone, class AD = tcdt::NoAdapters>
 gemm_status_t launch_tc(gemm_plan* plan, const Choice& ch, const Problem& pr, const void* C, void* D,
-                        int64_t ldc, float alpha, float beta, gemm_dtype_t out_dtype, cudaStream_t stream) {
+                        int64_t ldc, float alpha, float beta, gemm_dtype_t out_dtype, cudaStream_t stream,
+                        const AD& ad = AD{}) {
     const bool a_mn = pr.la == GEMM_COL_MAJOR;   // column-major A is M-contiguous
     const bool b_mn = pr.lb == GEMM_ROW_MAJOR;   // row-major B is N-contiguous
     if ((a_mn || b_mn) && !Cfg::MN_OK) return GEMM_ERR_UNSUPPORTED;
@@ -447,7 +497,7 @@ gemm_status_t launch_tc(gemm_plan* plan, const Choice& ch, const Problem& pr, co
 #endif
 
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     fill_launch_config<Cfg>(cfg, attr, stream);
     cfg.gridDim = dim3(Cfg::CG * units, 1, 1);
     if (pair_launch) {
@@ -460,13 +510,69 @@ gemm_status_t launch_tc(gemm_plan* plan, const Choice& ch, const Problem& pr, co
         cfg.numAttrs = 1;
         cfg.gridDim = dim3(2 * p.num_tiles, 1, 1);
     }
-    if (cudaLaunchKernelEx(&cfg, tcdt::gemm_sm103_kernel<Cfg, EP>, tmA, tmB, tmBh, tmD, tmW, p) != cudaSuccess) {
+    if constexpr (AD::kOn) {
+        // the kernel that makes h may still run: this one waits for it itself
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    if (cudaLaunchKernelEx(&cfg, tcdt::gemm_sm103_kernel<Cfg, EP, AD>, tmA, tmB, tmBh, tmD, tmW, p, ad) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
     ++plan->launches;
     return GEMM_OK;
 }
+
+template <class Cfg>
+gemm_status_t fill_adapters(gemm_plan* plan, tcdt::AdapterArgs& ad, const Problem& pr, const AdapterProblem& a) {
+    const bool mn = a.up_layout == GEMM_COL_MAJOR;
+    ad.index = a.index;
+    ad.count = static_cast<int32_t>(a.count);
+    ad.rank = static_cast<int32_t>(a.rank);
+    ad.part = a.part;
+    ad.u_mn = mn ? 1u : 0u;
+    ad.hidden = static_cast<const uint16_t*>(a.hidden);
+    ad.ldh = a.ldh;
+    ad.up = static_cast<const uint16_t*>(a.up);
+    ad.up_stride = a.up_stride;
+    ad.up_n = mn ? 1 : a.up_ld;
+    ad.up_r = mn ? a.up_ld : 1;
+    ad.bf16 = plan->in_dtype == GEMM_BF16 ? 1u : 0u;
+    if (Cfg::BN <= 64 || a.count == 0) return GEMM_OK;
+    const uint32_t fmt = input_format(plan->in_dtype);
+    ad.idesc = make_idesc(true, fmt, false, mn, Cfg::UMMA_M, Cfg::BN);
+    ad.idesc_half = make_idesc(true, fmt, false, mn, Cfg::UMMA_M, Cfg::BN / 2);
+    gemm_status_t st = encode_map(plan, &ad.tmH, a.hidden, 2 * a.part, pr.M, a.ldh, 64, Cfg::BM, plan->in_dtype);
+    if (st != GEMM_OK) return st;
+    if (mn) return encode_stack(plan, &ad.tmU, a.up, pr.N, a.rank, a.count, a.up_ld, a.up_stride, 64);
+    st = encode_stack(plan, &ad.tmU, a.up, a.rank, pr.N, a.count, a.up_ld, a.up_stride, Cfg::BN_CTA);
+    if (st == GEMM_OK && Cfg::HALVES_OK)
+        st = encode_stack(plan, &ad.tmUh, a.up, a.rank, pr.N, a.count, a.up_ld, a.up_stride, Cfg::BN_CTA_HALF);
+    return st;
+}
+
+template <class Cfg>
+gemm_status_t launch_adapters_cfg(gemm_plan* plan, int slot, const Choice& ch, const Problem& pr, void* D, int64_t ldd,
+                                  gemm_dtype_t out, const AdapterProblem& a, cudaStream_t s) {
+    gemm_status_t st = prepare<Cfg, tcdt::kEpFused, tcdt::AdapterArgs>(plan, ch.kind, slot);
+    if (st != GEMM_OK) return st;
+    tcdt::AdapterArgs ad;
+    std::memset(&ad, 0, sizeof(ad));
+    st = fill_adapters<Cfg>(plan, ad, pr, a);
+    if (st != GEMM_OK) return st;
+    return launch_tc<Cfg, tcdt::kEpFused, tcdt::AdapterArgs>(plan, ch, pr, nullptr, D, ldd, 1.0f, 0.0f, out, s, ad);
+}
+
+#define TCDT_DEFINE_ADAPTERS(name, CfgT)                                                                 \
+    gemm_status_t launch_##name##_adapters(gemm_plan* plan, int slot, const Choice& ch, const Problem& pr, void* D, \
+                                           int64_t ldd, const AdapterProblem& a, cudaStream_t s) {         \
+        if (slot == 0)                                                                                    \
+            return launch_adapters_cfg<CfgT<false, tcdt::kOutF32, tcdt::kInF16>>(plan, slot, ch, pr, D, ldd, GEMM_F32, a, s); \
+        if (slot == 1)                                                                                    \
+            return launch_adapters_cfg<CfgT<false, tcdt::kOutF16, tcdt::kInF16>>(plan, slot, ch, pr, D, ldd, GEMM_F16, a, s); \
+        return launch_adapters_cfg<CfgT<false, tcdt::kOutBF16, tcdt::kInF16>>(plan, slot, ch, pr, D, ldd, GEMM_BF16, a, s);   \
+    }
 
 // Output slots: 0 fp32, 1 fp16, 2 bf16 (fp32 accumulation), 3 fp16 with fp16
 // accumulation (16-bit operands only).

@@ -108,6 +108,76 @@ struct KernelParams {
 #endif
 };
 
+// Low-rank adapters of the rows (include/adapters.h), for the instantiations
+// that add them: element (r, c) gains sum_j h[r][j] U[g][c][j] with g = index[r],
+// h in its two parts.
+//   * Tiles of whole rows: after the last K block, one more step for each adapter
+//     that has rows in the tile, with h as A and U as B.  Its MMAs leave the
+//     other rows of the accumulator as they are (umma_f16_ss_rows), so that
+//     nothing of another adapter, not even an infinity times 0, reaches a row.
+//     A step costs what a K block does: 8192^3 with an adapter of rank 64 a row,
+//     128 K blocks and two steps.
+//   * Transposed tiles (few rows): rows are MMA columns, which cannot be left out, so
+//     the epilogue computes the few products itself (adapters_add).
+struct NoAdapters {
+    static constexpr bool kOn = false;
+};
+
+struct AdapterArgs {
+    static constexpr bool kOn = true;
+    CUtensorMap tmH;          // h, boxes of 64 columns x 128 rows
+    CUtensorMap tmU, tmUh;    // the up factors, [adapter][channel][rank] or [adapter][rank][channel]; half-width items
+    const int32_t* index;     // [rows]
+    int32_t count, rank;
+    int32_t part;             // columns of h's high parts (and of its low ones)
+    uint32_t u_mn;            // 1: U is N-contiguous
+    uint32_t idesc, idesc_half;
+    // transposed tiles: h, and U's element (g, channel, j) at up[g * up_stride + channel * up_n + j * up_r]
+    const uint16_t* hidden;
+    const uint16_t* up;
+    int64_t ldh, up_stride, up_n, up_r;
+    uint32_t bf16;
+};
+
+// The adapters of a tile's rows, each once, in the order of their first rows.
+// A warp's lane i holds rows i, 32 + i, ...; every warp that walks a tile sees
+// the same order.
+template <int ROWS>
+struct AdapterWalk {
+    int idx[ROWS / 32];       // -1: none, or done
+
+    __device__ __forceinline__ AdapterWalk(const int32_t* index, int count, int row0, int M, int lane) {
+#pragma unroll
+        for (int w = 0; w < ROWS / 32; ++w) {
+            const int row = row0 + 32 * w + lane;
+            const int g = row < M ? __ldg(index + row) : -1;
+            idx[w] = g < count ? g : -1;
+        }
+    }
+    // The next adapter, and a bit for each row that it is not the adapter of.
+    __device__ __forceinline__ bool next(int& g, uint32_t (&off)[ROWS / 32]) {
+        g = -1;
+#pragma unroll
+        for (int w = 0; w < ROWS / 32; ++w) {
+            const uint32_t left = __ballot_sync(0xffffffffu, idx[w] >= 0);
+            if (g < 0 && left) g = __shfl_sync(0xffffffffu, idx[w], __ffs(left) - 1);
+        }
+        if (g < 0) return false;
+#pragma unroll
+        for (int w = 0; w < ROWS / 32; ++w) {
+            const bool here = idx[w] == g;
+            off[w] = ~__ballot_sync(0xffffffffu, here);
+            if (here) idx[w] = -1;
+        }
+        return true;
+    }
+};
+
+// Steps of 64 columns of h that an adapter takes; the K steps of 16 in them.
+// With up to 32 columns a part both parts are in the first 64 columns and use the
+// same columns of U.
+__device__ __forceinline__ int adapter_steps(const AdapterArgs& a) { return a.part <= 32 ? 1 : a.part / 32; }
+
 // One output tile is UMMA_M x BN (UMMA_M = 128 * CG).  With CG == 2 a
 // cluster of two CTAs on two SMs computes it with one tcgen05.mma stream:
 // each CTA stages 128 rows of A and BN/2 columns of B and receives 128
@@ -771,6 +841,107 @@ __device__ __forceinline__ void store_d_block(const KernelParams& p, int row0, i
     __syncwarp();
 }
 
+// Transposed tiles: the adapters of W tokens (columns col0 ..) for one channel a
+// lane, four tokens at a time: their 16 values of U and of h are asked for
+// together, so that their latencies overlap.  Lanes 0..15 hold 16 of a token's high
+// parts and 16..31 the low ones (one load), and the sums reach every lane by
+// shuffles.  16 tokens of rank 16 take about 1600 instructions a warp, once a tile.
+__device__ __forceinline__ float adapter_value(uint32_t bits, bool bf16) {
+    return bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+
+// Values j0 .. j0 + 15 of U for a channel, two a word, 0 from the rank on.
+__device__ __forceinline__ void adapter_load_up(const AdapterArgs& a, int g, int channel, int j0, uint32_t (&u)[8]) {
+    const uint16_t* p = a.up + g * a.up_stride + channel * a.up_n + j0 * a.up_r;
+    const int n = a.rank - j0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        if (a.up_r == 1 && 8 * q + 8 <= n) {      // (rows start on 16-byte boundaries)
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 8 * q));
+            u[4 * q] = v.x, u[4 * q + 1] = v.y, u[4 * q + 2] = v.z, u[4 * q + 3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 8 * q + 2 * e;
+                const uint32_t lo = r < n ? __ldg(p + r * a.up_r) : 0u, hi = r + 1 < n ? __ldg(p + (r + 1) * a.up_r) : 0u;
+                u[4 * q + e] = lo | hi << 16;
+            }
+        }
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void adapters_add(const AdapterArgs& a, float (&acc)[W], int channel, bool channel_ok, int col0,
+                                             int tokens, int lane) {
+    int mine = -1;            // the adapter of token col0 + lane
+    if (lane < W && col0 + lane < tokens) mine = __ldg(a.index + col0 + lane);
+    if (mine >= a.count) mine = -1;
+    const uint32_t given = __ballot_sync(0xffffffffu, mine >= 0);
+    if (!given) return;
+    const bool bf16 = a.bf16 != 0;
+    const int own = channel_ok ? channel : 0;
+    const uint16_t* hidden = a.hidden + static_cast<int64_t>(col0) * a.ldh + (lane >> 4) * a.part + (lane & 15);
+#pragma unroll 1
+    for (int j0 = 0; j0 < a.rank; j0 += 16) {
+#pragma unroll 1
+        for (int i0 = 0; i0 < W; i0 += 4) {
+            if (!(given >> i0 & 15u)) continue;
+            uint32_t u[4][8], h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int g = __shfl_sync(0xffffffffu, mine, i0 + i);
+                if (g >= 0) {
+                    adapter_load_up(a, g, own, j0, u[i]);
+                    h[i] = hidden[(i0 + i) * a.ldh + j0];
+                } else {
+                    h[i] = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[i][e] = 0;
+                }
+            }
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = adapter_value(h[i], bf16);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                y[i] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y[i] = fmaf(__shfl_sync(0xffffffffu, v, 2 * e), adapter_value(u[i][e] & 0xFFFFu, bf16), y[i]);
+                    y[i] = fmaf(__shfl_sync(0xffffffffu, v, 2 * e + 1), adapter_value(u[i][e] >> 16, bf16), y[i]);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                if ((w & ~3) == i0) acc[w] += y[w & 3];
+        }
+    }
+}
+
+// For four tokens of one channel a thread, in the split-K reduction.
+__device__ __forceinline__ void adapters_add_quad(const AdapterArgs& a, float4& acc, int channel, int col0, int tokens) {
+    const bool bf16 = a.bf16 != 0;
+    float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int g = col0 + i < tokens ? __ldg(a.index + col0 + i) : -1;
+        if (g < 0 || g >= a.count) continue;
+        const uint16_t* h = a.hidden + static_cast<int64_t>(col0 + i) * a.ldh;
+#pragma unroll 1
+        for (int j0 = 0; j0 < a.rank; j0 += 16) {
+            uint32_t u[8];
+            adapter_load_up(a, g, channel, j0, u);
+            float y = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                y = fmaf(adapter_value(h[j0 + e], bf16) + adapter_value(h[a.part + j0 + e], bf16),
+                         adapter_value(e & 1 ? u[e / 2] >> 16 : u[e / 2] & 0xFFFFu, bf16), y);
+            v[i] += y;
+        }
+    }
+    acc = make_float4(v[0], v[1], v[2], v[3]);
+}
+
 // alpha * acc (+ beta * C) for W consecutive accumulator columns of one
 // accumulator row, written to D (row-major, or transposed with trans_out).
 template <class Cfg, int EP>
@@ -1041,13 +1212,17 @@ __device__ __forceinline__ void stage_and_store_f32(const void* tmap, const uint
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <class Cfg, int EP = kEpNone>
+template <class Cfg, int EP = kEpNone, class AD = NoAdapters>
 __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
 gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmD,
-                  const __grid_constant__ CUtensorMap tmW, const KernelParams p) {
+                  const __grid_constant__ CUtensorMap tmW, const KernelParams p,
+                  const __grid_constant__ AD ad) {
     constexpr int CG = Cfg::CG;
     constexpr int W = Cfg::W;
+    // tiles of whole rows add the rows' adapters with MMAs, transposed ones in the epilogue
+    constexpr bool kAdapterSteps = AD::kOn && Cfg::BN > 64;
+    constexpr bool kAdapterAdd = AD::kOn && Cfg::BN <= 64;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;   // 128B-swizzle atoms need 1024-byte alignment
@@ -1214,7 +1389,68 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         phase ^= 1u;
                     }
                 }
+                if constexpr (kAdapterSteps) {
+                    // the adapters' steps: h and U in the place of A and B
+                    if (ok && x.kb1 == p.num_k_blocks) {
+                        griddep_wait();      // h comes from the kernel before this one
+                        AdapterWalk<Cfg::UMMA_M> walk(ad.index, ad.count, mb * Cfg::UMMA_M, p.M, lane);
+                        const uint32_t u_tx = ad.u_mn ? static_cast<uint32_t>(b_chunks * 64 * 128)
+                                              : half  ? Cfg::BN_CTA_HALF * 128u
+                                                      : Cfg::BN_CTA * 128u;
+                        const uint32_t tx = CG * (Cfg::A_BYTES + u_tx);
+                        const void* tmu = half && !ad.u_mn ? static_cast<const void*>(&ad.tmUh)
+                                                           : static_cast<const void*>(&ad.tmU);
+                        const int steps = adapter_steps(ad), blocks = ad.part <= 64 ? 1 : 2;
+                        uint32_t off[Cfg::UMMA_M / 32];
+                        int g;
+                        while (ok && walk.next(g, off)) {
+#pragma unroll 1
+                            for (int st = 0; st < steps; ++st) {
+                                if (!warp_wait_phase(empty_bar(stage), phase ^ 1u, wctx, kSiteProducerEmpty)) {
+                                    ok = false;
+                                    break;
+                                }
+                                const uint32_t sa = base + stage * Cfg::STAGE_BYTES;
+                                const uint32_t sb = sa + Cfg::A_BYTES;
+                                const uint32_t fb_local = full_bar(stage);
+                                const int r0 = 64 * (st % blocks);     // first rank column of U in this step
+                                if (elect_one_sync()) {
+                                    if (leader) mbar_arrive_expect_tx(fb_local, tx);
+                                    if constexpr (CG == 1) {
+                                        tma_load_2d(sa, &ad.tmH, fb_local, 64 * st, m0);
+                                        if (ad.u_mn) {
+#pragma unroll 1
+                                            for (int c = 0; c < b_chunks; ++c)
+                                                tma_load_3d(sb + c * Cfg::MN_CHUNK_BYTES, tmu, fb_local, n0 + 64 * c, r0,
+                                                            g);
+                                        } else {
+                                            tma_load_3d(sb, tmu, fb_local, r0, n0, g);
+                                        }
+                                    } else {
+                                        const uint32_t fb = map_to_cta(fb_local, 0);
+                                        tma_load_2d_pair(sa, &ad.tmH, fb, 64 * st, m0);
+                                        if (ad.u_mn) {
+#pragma unroll 1
+                                            for (int c = 0; c < b_chunks; ++c)
+                                                tma_load_3d_pair(sb + c * Cfg::MN_CHUNK_BYTES, tmu, fb, n0 + 64 * c, r0,
+                                                                 g);
+                                        } else {
+                                            tma_load_3d_pair(sb, tmu, fb, r0, n0, g);
+                                        }
+                                    }
+                                }
+                                __syncwarp();
+                                ++issued;
+                                if (++stage == Cfg::STAGES) {
+                                    stage = 0;
+                                    phase ^= 1u;
+                                }
+                            }
+                        }
+                    }
+                }
             }
+            if constexpr (AD::kOn) griddep_wait();    // this kernel ends after the one before it
             if (!ok && leader) {
                 // wind down: let the copies already issued land before exiting
                 int s = stage;
@@ -1291,7 +1527,8 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         // item's last K block the accumulator is complete (the same
                         // lane commits, so the commit covers its MMAs)
                         umma_commit<CG>(empty_bar(stage), kPair);
-                        if (kb + 1 == x.kb1) umma_commit<CG>(accf_bar(buf), kPair);
+                        if (kb + 1 == x.kb1 && !(kAdapterSteps && x.kb1 == p.num_k_blocks))
+                            umma_commit<CG>(accf_bar(buf), kPair);
                     }
                     __syncwarp();
                     if (++stage == Cfg::STAGES) {
@@ -1300,6 +1537,51 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     }
                 }
                 if (!ok) break;
+                if constexpr (kAdapterSteps) {
+                    if (x.kb1 == p.num_k_blocks) {
+                        int mb, nb;
+                        tile_coords(p, x.tile, mb, nb);
+                        AdapterWalk<Cfg::UMMA_M> walk(ad.index, ad.count, mb * Cfg::UMMA_M, p.M, lane);
+                        const uint32_t idesc_u = (Cfg::HALVES_OK && x.half >= 0) ? ad.idesc_half : ad.idesc;
+                        const uint32_t u_lbo = ad.u_mn ? Cfg::MN_CHUNK_BYTES : 16u;
+                        const uint32_t u_kstep = ad.u_mn ? 16u * 128u : 32u;
+                        const int steps = adapter_steps(ad);
+                        uint32_t off[Cfg::UMMA_M / 32];
+                        int g;
+                        while (ok && walk.next(g, off)) {
+#pragma unroll 1
+                            for (int st = 0; st < steps; ++st) {
+                                if (!warp_wait_phase(full_bar(stage), phase, wctx, kSiteMmaFull)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after_sync();
+                                const uint32_t sa = base + stage * Cfg::STAGE_BYTES;
+                                const uint32_t sb = sa + Cfg::A_BYTES;
+                                if (elect_one_sync()) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const int j = (64 * st + 16 * k) & (ad.part - 1);     // rank column
+                                        if (64 * st + 16 * k >= 2 * ad.part || j >= ad.rank) continue;
+                                        const uint64_t adesc = smem_desc_sw128(sa + k * 32u, 16u, 1024u);
+                                        const uint64_t udesc = smem_desc_sw128(
+                                            sb + static_cast<uint32_t>((j & 63) >> 4) * u_kstep, u_lbo, 1024u);
+                                        umma_f16_ss_rows<CG>(d_tmem, adesc, udesc, idesc_u, off, 1u);
+                                    }
+                                    umma_commit<CG>(empty_bar(stage), kPair);
+                                }
+                                __syncwarp();
+                                if (++stage == Cfg::STAGES) {
+                                    stage = 0;
+                                    phase ^= 1u;
+                                }
+                            }
+                        }
+                        if (!ok) break;
+                        if (elect_one_sync()) umma_commit<CG>(accf_bar(buf), kPair);
+                        __syncwarp();
+                    }
+                }
                 if (x.kb1 == x.kb0) {
                     // no K block (not produced by the scheduler): publish the empty accumulator
                     if (elect_one_sync()) umma_commit<CG>(accf_bar(buf), kPair);
@@ -1452,6 +1734,9 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             named_bar_sync(1, 32 * Cfg::NUM_EPI_WARPS);
             if (!epi_ok_flag[iter & 1]) break;
             tc_fence_after_sync();
+            if constexpr (kAdapterAdd) {
+                if (iter == 0) griddep_wait();    // h comes from the kernel before this one
+            }
             const int row = m0 + row_local;
             const bool row_ok = row < p.M;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + buf * Cfg::ACC_COLS;
@@ -1499,6 +1784,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                                 acc[i + 2] = __uint_as_float(r[i + 2]) + q.z;
                                 acc[i + 3] = __uint_as_float(r[i + 3]) + q.w;
                             }
+                            if constexpr (kAdapterAdd) adapters_add<W>(ad, acc, row, row_ok, col0, p.N, lane);
                             epilogue_chunk<Cfg, EP>(p, acc, row, col0, row_ok, lane);
                         }
                     }
@@ -1657,6 +1943,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         float acc[W];
 #pragma unroll
                         for (int i = 0; i < W; ++i) acc[i] = acc_value<Cfg::ACC_F16>(r[i]);
+                        if constexpr (kAdapterAdd) adapters_add<W>(ad, acc, row, row_ok, col0, p.N, lane);
                         epilogue_chunk<Cfg, EP>(p, acc, row, col0, row_ok, lane);
                     }
                 }
@@ -1743,7 +2030,9 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                             const int r = q / QUADS_PER_ROW;
                             const int col = (q - r * QUADS_PER_ROW) * 4;
                             const int grow = m0 + r, gcol = n0 + col;
-                            if (grow < p.M && gcol < p.N) epilogue_quad<Cfg, EP>(p, acc[j], grow, gcol);
+                            if (grow >= p.M || gcol >= p.N) continue;
+                            if constexpr (kAdapterAdd) adapters_add_quad(ad, acc[j], grow, gcol, p.N);
+                            epilogue_quad<Cfg, EP>(p, acc[j], grow, gcol);
                         }
                     }
                 }

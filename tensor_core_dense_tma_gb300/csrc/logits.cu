@@ -163,10 +163,6 @@ __device__ __forceinline__ bool wait_slot(uint32_t bar, uint32_t parity, uint64_
     return true;
 }
 
-// Waits for the kernel before this one in the stream, where this one was
-// launched dependent on it.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Two 32-bit values as a register pair.
 __device__ __forceinline__ uint64_t bit_pair(uint32_t x, uint32_t y) {
     uint64_t v;
@@ -1230,7 +1226,7 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(const Pairs a) {
     int64_t at[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) at[i] = min(max(a.offsets[2 * pair + i], int64_t(0)), a.T);
-    grid_wait();                      // the rows' log-probabilities are there
+    tcdt::griddep_wait();             // the rows' log-probabilities are there
     auto scored = [&](int64_t r) {
         const int64_t y = a.tokens[r];
         return y >= 0 && y < a.V;
@@ -1283,7 +1279,7 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const Args a, 
     const Segment<E> seg(a.z, r * a.ld, a.V, part, parts, kGradVectors);
     E* out = static_cast<E*>(a.dz) + r * a.ldd;
     const bool whole = (reinterpret_cast<uintptr_t>(out + seg.first) & 15) == 0;
-    grid_wait();
+    tcdt::griddep_wait();
     const RowState s = a.state[r];
     const bool zeros = s.g == 0.f || s.log2_S == INFINITY;
     const int64_t y = a.tokens[r];
@@ -1551,7 +1547,7 @@ gemm_status_t check_preference(gemm_dtype_t dtype, const void* logits, int64_t T
 }
 
 // A kernel that may start while the one before it in the stream ends (it waits
-// for it itself, see grid_wait).
+// for it itself, see griddep_wait).
 template <typename... P, typename... A>
 gemm_status_t launch_dependent(void (*kernel)(P...), unsigned ctas, unsigned threads, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg{};

@@ -23,7 +23,7 @@ def lib():
 def test_every_declared_symbol_is_exported(lib):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "adapters.h")).read(), flags=re.S)
     names = set(re.findall(r"\b(gemm_[a-z0-9_]+)\s*\(", text))
-    assert names == {"gemm_adapters_hidden_width", "gemm_adapters_work_bytes", "gemm_run_adapters", "gemm_adapters_grad"}
+    assert names == {"gemm_adapters_hidden_width", "gemm_run_adapters", "gemm_adapters_grad"}
     out = subprocess.run(["nm", "-D", "--defined-only", tcbuild.LIB_PATH], capture_output=True, text=True,
                          check=True).stdout
     assert names <= {line.split()[-1] for line in out.splitlines() if line.strip()}
@@ -35,14 +35,9 @@ def test_hidden_width(lib):
     assert all(lib.gemm_adapters_hidden_width(r) == hidden_width(r) for r in range(1, 129))
 
 
-def test_work_bytes(lib):
-    assert lib.gemm_adapters_work_bytes(0, 64) == 0 and lib.gemm_adapters_work_bytes(-3, 64) == 0
-    assert lib.gemm_adapters_work_bytes(1, 64) >= 0
-
-
 def test_without_a_plan(lib):
     a = Adapters(2, 8, P, 64, 512, 0, P, 8, 256, 0, None, P)
-    run = lambda q: lib.gemm_run_adapters(None, P, P, P, 4, 32, 64, 64, 64, 32, 1, 0, None, q, P, 32, P, None)   # noqa: E731
+    run = lambda q: lib.gemm_run_adapters(None, P, P, P, 4, 32, 64, 64, 64, 32, 1, 0, None, q, P, 32, None)   # noqa: E731
     assert run(ctypes.byref(a)) == 1 and run(None) == 1
     assert lib.gemm_adapters_grad(None, P, P, 4, 32, 64, 64, 32, ctypes.byref(a), P, P, 32, 2, P, 64, 512, P, 8, 256,
                                   None) == 1
