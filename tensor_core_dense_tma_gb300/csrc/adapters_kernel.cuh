@@ -35,9 +35,34 @@ __device__ __forceinline__ void adapter_pipe_init(AdapterPipe& q, int stages) {
     fence_mbar_init();
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+// The sum over the CTAs of a cluster, in their order, of what lies at `at` in the
+// shared memory of each; the loads of all of them are under way together (one after
+// the other they took 0.3 us each).
+constexpr int kMaxSplits = 8;
+
+__device__ __forceinline__ float cluster_sum(uint32_t at, int splits) {
+    float x[kMaxSplits], v = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+        if (s < splits)
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[s]) : "r"(map_to_cta(at, static_cast<uint32_t>(s))));
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+        if (s < splits) v += x[s];
+    return v;
+}
+
+__device__ __forceinline__ float4 cluster_sum4(uint32_t at, int splits) {
+    float4 x[kMaxSplits], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+        if (s < splits)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[s].x), "=f"(x[s].y), "=f"(x[s].z), "=f"(x[s].w)
+                         : "r"(map_to_cta(at, static_cast<uint32_t>(s))));
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+        if (s < splits) v.x += x[s].x, v.y += x[s].y, v.z += x[s].z, v.w += x[s].w;
     return v;
 }
 
@@ -103,7 +128,11 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
 
     griddep_launch();
     if (warp == 0) {
-        if (lane == 0) adapter_pipe_init(q, a.stages);
+        if (lane == 0) {
+            tma_prefetch_desc(&a.tmX);
+            tma_prefetch_desc(&a.tmA);
+            adapter_pipe_init(q, a.stages);
+        }
         AdapterWalk<128> walk(a.index, a.count, row0, a.M, lane);
         uint32_t m[4];
         int g, n = 0;
@@ -234,11 +263,8 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
             float v[4] = {};
             if (g >= 0 && g < a.count && c < a.rr) {
                 const uint32_t from = smem_addr(sums + row * pitch + c);
-                for (int s = 0; s < a.splits; ++s) {
-                    const uint32_t p = a.splits > 1 ? map_to_cta(from, static_cast<uint32_t>(s)) : from;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += a.splits > 1 ? ld_cluster_f32(p + 4u * e) : ld_shared_f32(p + 4u * e);
-                }
+                const float4 sum = a.splits > 1 ? cluster_sum4(from, a.splits) : ld_shared_v4f(from);
+                v[0] = sum.x, v[1] = sum.y, v[2] = sum.z, v[3] = sum.w;
                 const float scale = a.scale ? __ldg(a.scale + g) : 1.0f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = c + e < a.rank ? v[e] * scale : 0.0f;
@@ -314,7 +340,11 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
     const int chunks = a.part <= 32 ? 1 : a.part / 32;     // of h
     const uint32_t stage_bytes = static_cast<uint32_t>(factor_stage_bytes(a.part));
     const uint32_t tmem_cols = 2u * static_cast<uint32_t>(a.part);
-    if (threadIdx.x == 0) adapter_pipe_init(q, a.stages);
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&f.tmX);
+        tma_prefetch_desc(&f.tmH);
+        adapter_pipe_init(q, a.stages);
+    }
     if (warp == 1) {
         tmem_alloc<1>(smem_addr(&q.tmem), tmem_cols);
         tmem_relinquish_alloc_permit<1>();
@@ -468,13 +498,12 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
     // joined and stored, an equal share by each CTA, in the order of the output's memory
     const bool by_rank = f.sr == 1;            // consecutive in memory: rank, else columns
     const int total = a.rank * 128, share = (total + a.splits - 1) / a.splits;
+#pragma unroll 2
     for (int i = rank * share + threadIdx.x; i < min(total, (rank + 1) * share); i += kAdapterThreads) {
         const int r = by_rank ? i % a.rank : i / 128, c = by_rank ? i / a.rank : i % 128;
         if (col0 + c >= f.columns) continue;
         const uint32_t from = smem_addr(sums + r * kFactorPitch + c);
-        float v = 0.0f;
-        for (int s = 0; s < a.splits; ++s)
-            v += a.splits > 1 ? ld_cluster_f32(map_to_cta(from, static_cast<uint32_t>(s))) : ld_shared_f32(from);
+        const float v = a.splits > 1 ? cluster_sum(from, a.splits) : ld_shared_f32(from);
         const int64_t o = g * f.stride + r * f.sr + (col0 + c) * f.sc;
         if (a.out_kind == 0) static_cast<float*>(f.out)[o] = v;
         else static_cast<uint16_t*>(f.out)[o] = adapter_bits(v, a.out_kind == 2);

@@ -532,23 +532,18 @@ gemm_status_t fill_adapters(gemm_plan* plan, tcdt::AdapterArgs& ad, const Proble
     ad.rank = static_cast<int32_t>(a.rank);
     ad.part = a.part;
     ad.u_mn = mn ? 1u : 0u;
-    ad.hidden = static_cast<const uint16_t*>(a.hidden);
-    ad.ldh = a.ldh;
-    ad.up = static_cast<const uint16_t*>(a.up);
-    ad.up_stride = a.up_stride;
-    ad.up_n = mn ? 1 : a.up_ld;
-    ad.up_r = mn ? a.up_ld : 1;
-    ad.bf16 = plan->in_dtype == GEMM_BF16 ? 1u : 0u;
-    if (Cfg::BN <= 64 || a.count == 0) return GEMM_OK;
     const uint32_t fmt = input_format(plan->in_dtype);
-    ad.idesc = make_idesc(true, fmt, false, mn, Cfg::UMMA_M, Cfg::BN);
+    constexpr bool tokens = Cfg::BN <= 64;      // transposed tiles: the untransposed product, 128 x 128
+    ad.idesc = make_idesc(true, fmt, false, mn, Cfg::UMMA_M, tokens ? 128 : Cfg::BN);
     ad.idesc_half = make_idesc(true, fmt, false, mn, Cfg::UMMA_M, Cfg::BN / 2);
-    gemm_status_t st = encode_map(plan, &ad.tmH, a.hidden, 2 * a.part, pr.M, a.ldh, 64, Cfg::BM, plan->in_dtype);
+    const int64_t rows = tokens ? pr.N : pr.M, channels = tokens ? pr.M : pr.N;
+    gemm_status_t st =
+        encode_map(plan, &ad.tmH, a.hidden, 2 * a.part, rows, a.ldh, 64, tokens ? Cfg::BN : Cfg::BM, plan->in_dtype);
     if (st != GEMM_OK) return st;
-    if (mn) return encode_stack(plan, &ad.tmU, a.up, pr.N, a.rank, a.count, a.up_ld, a.up_stride, 64);
-    st = encode_stack(plan, &ad.tmU, a.up, a.rank, pr.N, a.count, a.up_ld, a.up_stride, Cfg::BN_CTA);
-    if (st == GEMM_OK && Cfg::HALVES_OK)
-        st = encode_stack(plan, &ad.tmUh, a.up, a.rank, pr.N, a.count, a.up_ld, a.up_stride, Cfg::BN_CTA_HALF);
+    if (mn) return encode_stack(plan, &ad.tmU, a.up, channels, a.rank, a.count, a.up_ld, a.up_stride, 64);
+    st = encode_stack(plan, &ad.tmU, a.up, a.rank, channels, a.count, a.up_ld, a.up_stride, tokens ? 128 : Cfg::BN_CTA);
+    if (st == GEMM_OK && !tokens && Cfg::HALVES_OK)
+        st = encode_stack(plan, &ad.tmUh, a.up, a.rank, channels, a.count, a.up_ld, a.up_stride, Cfg::BN_CTA_HALF);
     return st;
 }
 

@@ -117,26 +117,25 @@ struct KernelParams {
 //     nothing of another adapter, not even an infinity times 0, reaches a row.
 //     A step costs what a K block does: 8192^3 with an adapter of rank 64 a row,
 //     128 K blocks and two steps.
-//   * Transposed tiles (few rows): rows are MMA columns, which cannot be left out, so
-//     the epilogue computes the few products itself (adapters_add).
+//   * Transposed tiles (few rows): rows are MMA columns there, which cannot be left
+//     out, so the steps compute the untransposed product -- h as A (128 rows are read,
+//     the first BN of them count), the tile's 128 channels of U as B -- into columns of
+//     tensor memory of their own, and the epilogue warps turn it over through shared
+//     memory and add it.  (Computed by the epilogue's threads from registers, 61 x
+//     2055 x 1000 with rank 24 took 50 us: a chain of loads of U and h.)
 struct NoAdapters {
     static constexpr bool kOn = false;
 };
 
 struct AdapterArgs {
     static constexpr bool kOn = true;
-    CUtensorMap tmH;          // h, boxes of 64 columns x 128 rows
+    CUtensorMap tmH;          // h, boxes of 64 columns x 128 rows (transposed tiles: x BN)
     CUtensorMap tmU, tmUh;    // the up factors, [adapter][channel][rank] or [adapter][rank][channel]; half-width items
     const int32_t* index;     // [rows]
     int32_t count, rank;
     int32_t part;             // columns of h's high parts (and of its low ones)
     uint32_t u_mn;            // 1: U is N-contiguous
     uint32_t idesc, idesc_half;
-    // transposed tiles: h, and U's element (g, channel, j) at up[g * up_stride + channel * up_n + j * up_r]
-    const uint16_t* hidden;
-    const uint16_t* up;
-    int64_t ldh, up_stride, up_n, up_r;
-    uint32_t bf16;
 };
 
 // The adapters of a tile's rows, each once, in the order of their first rows.
@@ -172,6 +171,11 @@ struct AdapterWalk {
         return true;
     }
 };
+
+// A 16-bit value of the plan's type.
+__device__ __forceinline__ float adapter_value(uint32_t bits, bool bf16) {
+    return bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
 
 // Steps of 64 columns of h that an adapter takes; the K steps of 16 in them.
 // With up to 32 columns a part both parts are in the first 64 columns and use the
@@ -841,107 +845,6 @@ __device__ __forceinline__ void store_d_block(const KernelParams& p, int row0, i
     __syncwarp();
 }
 
-// Transposed tiles: the adapters of W tokens (columns col0 ..) for one channel a
-// lane, four tokens at a time: their 16 values of U and of h are asked for
-// together, so that their latencies overlap.  Lanes 0..15 hold 16 of a token's high
-// parts and 16..31 the low ones (one load), and the sums reach every lane by
-// shuffles.  16 tokens of rank 16 take about 1600 instructions a warp, once a tile.
-__device__ __forceinline__ float adapter_value(uint32_t bits, bool bf16) {
-    return bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
-}
-
-// Values j0 .. j0 + 15 of U for a channel, two a word, 0 from the rank on.
-__device__ __forceinline__ void adapter_load_up(const AdapterArgs& a, int g, int channel, int j0, uint32_t (&u)[8]) {
-    const uint16_t* p = a.up + g * a.up_stride + channel * a.up_n + j0 * a.up_r;
-    const int n = a.rank - j0;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        if (a.up_r == 1 && 8 * q + 8 <= n) {      // (rows start on 16-byte boundaries)
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 8 * q));
-            u[4 * q] = v.x, u[4 * q + 1] = v.y, u[4 * q + 2] = v.z, u[4 * q + 3] = v.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 8 * q + 2 * e;
-                const uint32_t lo = r < n ? __ldg(p + r * a.up_r) : 0u, hi = r + 1 < n ? __ldg(p + (r + 1) * a.up_r) : 0u;
-                u[4 * q + e] = lo | hi << 16;
-            }
-        }
-    }
-}
-
-template <int W>
-__device__ __forceinline__ void adapters_add(const AdapterArgs& a, float (&acc)[W], int channel, bool channel_ok, int col0,
-                                             int tokens, int lane) {
-    int mine = -1;            // the adapter of token col0 + lane
-    if (lane < W && col0 + lane < tokens) mine = __ldg(a.index + col0 + lane);
-    if (mine >= a.count) mine = -1;
-    const uint32_t given = __ballot_sync(0xffffffffu, mine >= 0);
-    if (!given) return;
-    const bool bf16 = a.bf16 != 0;
-    const int own = channel_ok ? channel : 0;
-    const uint16_t* hidden = a.hidden + static_cast<int64_t>(col0) * a.ldh + (lane >> 4) * a.part + (lane & 15);
-#pragma unroll 1
-    for (int j0 = 0; j0 < a.rank; j0 += 16) {
-#pragma unroll 1
-        for (int i0 = 0; i0 < W; i0 += 4) {
-            if (!(given >> i0 & 15u)) continue;
-            uint32_t u[4][8], h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int g = __shfl_sync(0xffffffffu, mine, i0 + i);
-                if (g >= 0) {
-                    adapter_load_up(a, g, own, j0, u[i]);
-                    h[i] = hidden[(i0 + i) * a.ldh + j0];
-                } else {
-                    h[i] = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) u[i][e] = 0;
-                }
-            }
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v = adapter_value(h[i], bf16);
-                v += __shfl_xor_sync(0xffffffffu, v, 16);
-                y[i] = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    y[i] = fmaf(__shfl_sync(0xffffffffu, v, 2 * e), adapter_value(u[i][e] & 0xFFFFu, bf16), y[i]);
-                    y[i] = fmaf(__shfl_sync(0xffffffffu, v, 2 * e + 1), adapter_value(u[i][e] >> 16, bf16), y[i]);
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                if ((w & ~3) == i0) acc[w] += y[w & 3];
-        }
-    }
-}
-
-// For four tokens of one channel a thread, in the split-K reduction.
-__device__ __forceinline__ void adapters_add_quad(const AdapterArgs& a, float4& acc, int channel, int col0, int tokens) {
-    const bool bf16 = a.bf16 != 0;
-    float v[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int g = col0 + i < tokens ? __ldg(a.index + col0 + i) : -1;
-        if (g < 0 || g >= a.count) continue;
-        const uint16_t* h = a.hidden + static_cast<int64_t>(col0 + i) * a.ldh;
-#pragma unroll 1
-        for (int j0 = 0; j0 < a.rank; j0 += 16) {
-            uint32_t u[8];
-            adapter_load_up(a, g, channel, j0, u);
-            float y = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                y = fmaf(adapter_value(h[j0 + e], bf16) + adapter_value(h[a.part + j0 + e], bf16),
-                         adapter_value(e & 1 ? u[e / 2] >> 16 : u[e / 2] & 0xFFFFu, bf16), y);
-            v[i] += y;
-        }
-    }
-    acc = make_float4(v[0], v[1], v[2], v[3]);
-}
-
 // alpha * acc (+ beta * C) for W consecutive accumulator columns of one
 // accumulator row, written to D (row-major, or transposed with trans_out).
 template <class Cfg, int EP>
@@ -1220,9 +1123,13 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                   const __grid_constant__ AD ad) {
     constexpr int CG = Cfg::CG;
     constexpr int W = Cfg::W;
-    // tiles of whole rows add the rows' adapters with MMAs, transposed ones in the epilogue
-    constexpr bool kAdapterSteps = AD::kOn && Cfg::BN > 64;
-    constexpr bool kAdapterAdd = AD::kOn && Cfg::BN <= 64;
+    // the rows' adapters: tiles of whole rows, transposed tiles (see AdapterArgs)
+    constexpr bool kAdapterRows = AD::kOn && Cfg::BN > 64;
+    constexpr bool kAdapterTokens = AD::kOn && Cfg::BN <= 64;
+    // the untransposed sums of the adapters: 128 columns for each of the two accumulators
+    constexpr int kDeltaCol = 128;
+    constexpr int kTmemCols = kAdapterTokens ? 512 : Cfg::TMEM_COLS;
+    static_assert(!kAdapterTokens || 2 * Cfg::ACC_COLS <= kDeltaCol, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;   // 128B-swizzle atoms need 1024-byte alignment
@@ -1291,7 +1198,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         if (p.splits > 1) tma_prefetch_desc(&tmW);
     }
     if (warp == 1) {
-        tmem_alloc<CG>(smem_addr(tmem_slot), Cfg::TMEM_COLS);
+        tmem_alloc<CG>(smem_addr(tmem_slot), kTmemCols);
         tmem_relinquish_alloc_permit<CG>();
     }
     tc_fence_before_sync();
@@ -1389,19 +1296,22 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         phase ^= 1u;
                     }
                 }
-                if constexpr (kAdapterSteps) {
-                    // the adapters' steps: h and U in the place of A and B
+                if constexpr (AD::kOn) {
+                    // the adapters' steps: h and U in the place of A and B (transposed: of B and A)
                     if (ok && x.kb1 == p.num_k_blocks) {
                         griddep_wait();      // h comes from the kernel before this one
-                        AdapterWalk<Cfg::UMMA_M> walk(ad.index, ad.count, mb * Cfg::UMMA_M, p.M, lane);
+                        constexpr int kRows = kAdapterTokens ? (Cfg::BN + 31) / 32 * 32 : Cfg::UMMA_M;
+                        const int tokens = half ? Cfg::BN / 2 : Cfg::BN;
+                        AdapterWalk<kRows> walk(ad.index, ad.count, kAdapterTokens ? n0 : mb * Cfg::UMMA_M,
+                                                kAdapterTokens ? min(p.N, n0 + tokens) : p.M, lane);
                         const uint32_t u_tx = ad.u_mn ? static_cast<uint32_t>(b_chunks * 64 * 128)
                                               : half  ? Cfg::BN_CTA_HALF * 128u
                                                       : Cfg::BN_CTA * 128u;
-                        const uint32_t tx = CG * (Cfg::A_BYTES + u_tx);
-                        const void* tmu = half && !ad.u_mn ? static_cast<const void*>(&ad.tmUh)
-                                                           : static_cast<const void*>(&ad.tmU);
+                        const uint32_t tx = kAdapterTokens ? Cfg::A_BYTES + Cfg::BN * 128u : CG * (Cfg::A_BYTES + u_tx);
+                        const void* tmu = half && !ad.u_mn && kAdapterRows ? static_cast<const void*>(&ad.tmUh)
+                                                                           : static_cast<const void*>(&ad.tmU);
                         const int steps = adapter_steps(ad), blocks = ad.part <= 64 ? 1 : 2;
-                        uint32_t off[Cfg::UMMA_M / 32];
+                        uint32_t off[kRows / 32];
                         int g;
                         while (ok && walk.next(g, off)) {
 #pragma unroll 1
@@ -1416,7 +1326,16 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                                 const int r0 = 64 * (st % blocks);     // first rank column of U in this step
                                 if (elect_one_sync()) {
                                     if (leader) mbar_arrive_expect_tx(fb_local, tx);
-                                    if constexpr (CG == 1) {
+                                    if constexpr (kAdapterTokens) {
+                                        tma_load_2d(sb, &ad.tmH, fb_local, 64 * st, n0);
+                                        if (ad.u_mn) {
+#pragma unroll
+                                            for (int c = 0; c < 2; ++c)
+                                                tma_load_3d(sa + c * Cfg::MN_CHUNK_BYTES, tmu, fb_local, m0 + 64 * c, r0, g);
+                                        } else {
+                                            tma_load_3d(sa, tmu, fb_local, r0, m0, g);
+                                        }
+                                    } else if constexpr (CG == 1) {
                                         tma_load_2d(sa, &ad.tmH, fb_local, 64 * st, m0);
                                         if (ad.u_mn) {
 #pragma unroll 1
@@ -1527,7 +1446,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         // item's last K block the accumulator is complete (the same
                         // lane commits, so the commit covers its MMAs)
                         umma_commit<CG>(empty_bar(stage), kPair);
-                        if (kb + 1 == x.kb1 && !(kAdapterSteps && x.kb1 == p.num_k_blocks))
+                        if (kb + 1 == x.kb1 && !(AD::kOn && x.kb1 == p.num_k_blocks))
                             umma_commit<CG>(accf_bar(buf), kPair);
                     }
                     __syncwarp();
@@ -1537,18 +1456,28 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     }
                 }
                 if (!ok) break;
-                if constexpr (kAdapterSteps) {
+                if constexpr (AD::kOn) {
                     if (x.kb1 == p.num_k_blocks) {
                         int mb, nb;
                         tile_coords(p, x.tile, mb, nb);
-                        AdapterWalk<Cfg::UMMA_M> walk(ad.index, ad.count, mb * Cfg::UMMA_M, p.M, lane);
-                        const uint32_t idesc_u = (Cfg::HALVES_OK && x.half >= 0) ? ad.idesc_half : ad.idesc;
+                        constexpr int kRows = kAdapterTokens ? (Cfg::BN + 31) / 32 * 32 : Cfg::UMMA_M;
+                        const bool half = Cfg::HALVES_OK && x.half >= 0;
+                        const int tokens = half ? Cfg::BN / 2 : Cfg::BN;
+                        const int n0 = nb * Cfg::BN + (half ? x.half * tokens : 0);
+                        AdapterWalk<kRows> walk(ad.index, ad.count, kAdapterTokens ? n0 : mb * Cfg::UMMA_M,
+                                                kAdapterTokens ? min(p.N, n0 + tokens) : p.M, lane);
+                        const uint32_t idesc_u = half && kAdapterRows ? ad.idesc_half : ad.idesc;
+                        const uint32_t to = kAdapterTokens ? tmem_base + kDeltaCol * (1 + buf) : d_tmem;
                         const uint32_t u_lbo = ad.u_mn ? Cfg::MN_CHUNK_BYTES : 16u;
                         const uint32_t u_kstep = ad.u_mn ? 16u * 128u : 32u;
                         const int steps = adapter_steps(ad);
-                        uint32_t off[Cfg::UMMA_M / 32];
+                        uint32_t off[kRows / 32], rows_off[4 * CG];
+#pragma unroll
+                        for (int w = 0; w < 4 * CG; ++w) rows_off[w] = 0xFFFFFFFFu;
                         int g;
                         while (ok && walk.next(g, off)) {
+#pragma unroll
+                            for (int w = 0; w < kRows / 32; ++w) rows_off[w] = off[w];
 #pragma unroll 1
                             for (int st = 0; st < steps; ++st) {
                                 if (!warp_wait_phase(full_bar(stage), phase, wctx, kSiteMmaFull)) {
@@ -1558,15 +1487,18 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                                 tc_fence_after_sync();
                                 const uint32_t sa = base + stage * Cfg::STAGE_BYTES;
                                 const uint32_t sb = sa + Cfg::A_BYTES;
+                                const uint32_t sh = kAdapterTokens ? sb : sa, su = kAdapterTokens ? sa : sb;
                                 if (elect_one_sync()) {
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) {
                                         const int j = (64 * st + 16 * k) & (ad.part - 1);     // rank column
                                         if (64 * st + 16 * k >= 2 * ad.part || j >= ad.rank) continue;
-                                        const uint64_t adesc = smem_desc_sw128(sa + k * 32u, 16u, 1024u);
+                                        const uint64_t hdesc = smem_desc_sw128(sh + k * 32u, 16u, 1024u);
                                         const uint64_t udesc = smem_desc_sw128(
-                                            sb + static_cast<uint32_t>((j & 63) >> 4) * u_kstep, u_lbo, 1024u);
-                                        umma_f16_ss_rows<CG>(d_tmem, adesc, udesc, idesc_u, off, 1u);
+                                            su + static_cast<uint32_t>((j & 63) >> 4) * u_kstep, u_lbo, 1024u);
+                                        // (transposed: the adapter's first MMA sets its rows)
+                                        umma_f16_ss_rows<CG>(to, hdesc, udesc, idesc_u, rows_off,
+                                                             kAdapterTokens && st == 0 && k == 0 ? 0u : 1u);
                                     }
                                     umma_commit<CG>(empty_bar(stage), kPair);
                                 }
@@ -1734,12 +1666,73 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             named_bar_sync(1, 32 * Cfg::NUM_EPI_WARPS);
             if (!epi_ok_flag[iter & 1]) break;
             tc_fence_after_sync();
-            if constexpr (kAdapterAdd) {
-                if (iter == 0) griddep_wait();    // h comes from the kernel before this one
-            }
             const int row = m0 + row_local;
             const bool row_ok = row < p.M;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + buf * Cfg::ACC_COLS;
+            // Transposed tiles: the adapters' sums of this lane's channel for the tile's tokens,
+            // turned over through the four warps' staging buffers (token i's 128 channels in
+            // 512 bytes, 16-byte units at (unit ^ i % 8): free of conflicts both ways).
+            float delta[kAdapterTokens ? Cfg::BN / W : 1][W];
+            bool adds = false;
+            if constexpr (kAdapterTokens) {
+                adds = x.kb1 == p.num_k_blocks;
+                uint64_t given = 0;          // the tokens that have an adapter
+                if (adds) {
+#pragma unroll
+                    for (int w = 0; w < (Cfg::BN + 31) / 32; ++w) {
+                        const int token = n0 + 32 * w + lane;
+                        const int g = token < p.N && 32 * w + lane < nchunks * W ? __ldg(ad.index + token) : -1;
+                        given |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, g >= 0 && g < ad.count)) << (32 * w);
+                    }
+                    adds = given != 0;       // (the same in the four warps)
+                }
+                if (adds) {
+                    if (lane == 0) bulk_wait_group_read<0>();   // earlier stores have read the buffers
+                    named_bar_sync(1, 32 * Cfg::NUM_EPI_WARPS);
+                    if (32 * quad < Cfg::BN) {
+                        const int token = row_local;      // a lane of tensor memory is a token here
+                        const uint32_t from =
+                            tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + kDeltaCol * (1 + buf);
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[32];
+                            tmem_ld_32x32b_x32(from + 32 * c, r);
+                            tmem_ld_wait();
+                            const uint32_t to = staging_base + static_cast<uint32_t>(token) * 512u;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                st_shared_v4(to + (static_cast<uint32_t>((8 * c + i) ^ (token & 7)) << 4), r[4 * i],
+                                             r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                        }
+                    }
+                    named_bar_sync(1, 32 * Cfg::NUM_EPI_WARPS);
+#pragma unroll
+                    for (int token = 0; token < Cfg::BN; ++token) {
+                        const uint32_t at = staging_base + static_cast<uint32_t>(token) * 512u +
+                                            (static_cast<uint32_t>((row_local >> 2) ^ (token & 7)) << 4) +
+                                            static_cast<uint32_t>(row_local & 3) * 4u;
+                        delta[token / W][token % W] = given >> token & 1u ? ld_shared_f32(at) : 0.0f;
+                    }
+                    named_bar_sync(1, 32 * Cfg::NUM_EPI_WARPS);   // the buffers are free again
+                }
+            }
+            auto add_delta = [&](float (&v)[W], int c) {
+                if (!adds) return;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    float d = delta[0][i];
+                    if constexpr (kAdapterTokens && Cfg::BN > W) d = c == 0 ? d : delta[Cfg::BN / W - 1][i];
+                    v[i] += d;
+                }
+            };
+            auto add_delta_bits = [&](uint32_t (&r)[W], int c) {
+                float v[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
+                add_delta(v, c);
+#pragma unroll
+                for (int i = 0; i < W; ++i) r[i] = __float_as_uint(v[i]);
+            };
             if constexpr (kPairOK) {
                 if (x.role == kRolePair) {
                     // The tile's two K halves meet in the first CTA of the pair: each
@@ -1756,6 +1749,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                             uint32_t r[W];
                             tmem_ld_row<W>(t_row + W * c, r);
                             tmem_ld_wait();
+                            if constexpr (kAdapterTokens) add_delta_bits(r, c);
                             const uint32_t dst = map_to_cta(stg + row_off + static_cast<uint32_t>(W * c) * 4u, 0);
 #pragma unroll
                             for (int i = 0; i < W; i += 4) st_cluster_v4(dst + 4u * i, r[i], r[i + 1], r[i + 2], r[i + 3]);
@@ -1784,7 +1778,6 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                                 acc[i + 2] = __uint_as_float(r[i + 2]) + q.z;
                                 acc[i + 3] = __uint_as_float(r[i + 3]) + q.w;
                             }
-                            if constexpr (kAdapterAdd) adapters_add<W>(ad, acc, row, row_ok, col0, p.N, lane);
                             epilogue_chunk<Cfg, EP>(p, acc, row, col0, row_ok, lane);
                         }
                     }
@@ -1943,7 +1936,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         float acc[W];
 #pragma unroll
                         for (int i = 0; i < W; ++i) acc[i] = acc_value<Cfg::ACC_F16>(r[i]);
-                        if constexpr (kAdapterAdd) adapters_add<W>(ad, acc, row, row_ok, col0, p.N, lane);
+                        if constexpr (kAdapterTokens) add_delta(acc, c);
                         epilogue_chunk<Cfg, EP>(p, acc, row, col0, row_ok, lane);
                     }
                 }
@@ -1962,6 +1955,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     uint32_t r[W];
                     tmem_ld_row<W>(t_row + W * c, r);
                     tmem_ld_wait();
+                    if constexpr (kAdapterTokens) add_delta_bits(r, c);
                     if constexpr (W == 32) {
                         stage_and_store_f32(&tmW, r, W * c, ws_row0, lane, stg, sbuf);
                     } else {
@@ -2030,9 +2024,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                             const int r = q / QUADS_PER_ROW;
                             const int col = (q - r * QUADS_PER_ROW) * 4;
                             const int grow = m0 + r, gcol = n0 + col;
-                            if (grow >= p.M || gcol >= p.N) continue;
-                            if constexpr (kAdapterAdd) adapters_add_quad(ad, acc[j], grow, gcol, p.N);
-                            epilogue_quad<Cfg, EP>(p, acc[j], grow, gcol);
+                            if (grow < p.M && gcol < p.N) epilogue_quad<Cfg, EP>(p, acc[j], grow, gcol);
                         }
                     }
                 }
@@ -2065,7 +2057,7 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     if (warp == 1) {
         __syncwarp();
         tc_fence_after_sync();
-        tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
+        tmem_dealloc<CG>(tmem_base, kTmemCols);
     }
 }
 

@@ -11,8 +11,9 @@ policy      the ratio's argument is off by b and eps |lp - old|, its exponential
             d = ref - lp is off by v = b + eps |d|; k's derivative is e^d - 1 and
             expm1 and the two roundings lose 4 eps (|e^d - 1| + |d|).  The slope is off
             by (q + 4 eps) |r A| and, c the coefficient, |c| (e^d v + 4 eps |e^d - 1|).
-preference  a reward is beta times a 64-bit sum: off by |beta| sum b, and one rounding; the
-            loss has a slope of at most 1 in m, and sigma of at most 1/4.
+preference  a reward is beta times a 64-bit sum: off by |beta| sum b, and one rounding; m
+            by both and a rounding; the loss has a slope of at most 1 in m, and sigma of
+            at most 1/4; the exponential, logarithm and quotient lose 8 eps each.
 gradients   the bound of the log-probabilities' gradient plus the slope's error
             times (1[j = y] + p_j) / temperature.
 """
@@ -266,7 +267,7 @@ def check_preference(tc, view, z, tokens, t, kind, lengths, seed, e=0.1, beta=0.
     def results(r):
         near(r.logprob, lp, bound_log(z, t, ref_logprobs(z, tokens, t)[2], lp), "logprob")
         near(r.reward, reward, bound + EPS * np.abs(reward) + 1e-37, "reward")
-        near(r.loss, loss, e_m + EPS * np.abs(loss) + 1e-37, "loss")
+        near(r.loss, loss, e_m + EPS * np.abs(reward[0::2] - reward[1::2]) + 16 * EPS * np.abs(loss) + 1e-37, "loss")
 
     results(tc.preference_loss(view, dev(tokens), dev(offsets), f32(ref), **kw))
     r = tc.preference_loss_grad(view, dev(tokens), dev(offsets), f32(w), f32(ref), dlogits=out, **kw)
@@ -278,7 +279,8 @@ def check_preference(tc, view, z, tokens, t, kind, lengths, seed, e=0.1, beta=0.
         for s, sign in ((2 * q, 1), (2 * q + 1, -1)):
             part = slice(offsets[s], offsets[s + 1])
             g[part] = sign * w[q] * slope[q] * given[part]
-            e_g[part] = given[part] * w[q] * (abs(beta) * e_m[q] / 4 + 4 * EPS * abs(slope[q]))
+            e_g[part] = given[part] * w[q] * (abs(beta) * (e_m[q] + EPS * abs(reward[2 * q] - reward[2 * q + 1])) / 4
+                                         + 24 * EPS * abs(beta))
     zero = np.zeros(T)
     check_gradient(r.dlogits, z, tokens, t, logp, zero, g, e_g, zero, kind)
     return r
