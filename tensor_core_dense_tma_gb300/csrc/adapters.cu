@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kRowThreads) hidden_rows_kernel(const RowArgs 
 // ---- host ------------------------------------------------------------------
 constexpr int64_t kMaxExtent = 0x7FFFF000;
 constexpr int64_t kMaxStride = int64_t(1) << 39;      // elements: below 2^40 bytes, what a tensor map takes
-constexpr int64_t kRowsMost = 32;                     // rows that hidden_rows_kernel takes
+constexpr int64_t kRowsMost = 64;                     // rows that hidden_rows_kernel takes
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 bool layout_ok(gemm_layout_t l) { return l == GEMM_ROW_MAJOR || l == GEMM_COL_MAJOR; }
 
@@ -233,12 +233,15 @@ gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* 
     h.part = part;
     h.rr = (h.rank + 15) / 16 * 16;
     h.a_mn = row ? 0u : 1u;
-    h.per_stage = row ? 128 / h.rr : h.rr <= 64 ? 2 : 1;
-    h.idesc = make_idesc(true, input_format(plan->in_dtype), false, !row, 128, h.rr);
+    h.per_stage = row && h.rr <= 32 ? 64 / h.rr : 1;
+    h.pitch = row ? h.rr : h.rr <= 64 ? 64 : 128;
+    h.idesc = make_idesc(true, input_format(plan->in_dtype), false, !row, 128, h.per_stage * h.pitch);
+    h.idesc_one = make_idesc(true, input_format(plan->in_dtype), false, !row, 128, h.rr);
     h.M = static_cast<int32_t>(M);
     h.k_blocks = static_cast<int32_t>((K + 63) / 64);
     h.splits = splits_of(plan, (M + 127) / 128, h.k_blocks, 4);
-    h.stages = tcdt::kAdapterSharedBytes / tcdt::kHiddenStage;
+    const int64_t ctas = (M + 127) / 128 * h.splits;
+    h.stages = tcdt::kAdapterSharedBytes / tcdt::hidden_stage_bytes(h.rr);
     h.hidden = static_cast<uint16_t*>(hidden);
     h.ldh = ldh;
     h.bf16 = bf16;
@@ -249,8 +252,7 @@ gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* 
         st = row ? encode_stack(plan, &h.tmA, a.down, K, a.rank, a.count, a.down_ld, a.down_stride, h.rr)
                  : encode_stack(plan, &h.tmA, a.down, a.rank, K, a.count, a.down_ld, a.down_stride, 64);
     if (st != GEMM_OK) return st;
-    return launch_tiles(plan, tcdt::hidden_tile_kernel, h, (M + 127) / 128 * h.splits,
-                        plan->adapters_prepared[0], s);
+    return launch_tiles(plan, tcdt::hidden_tile_kernel, h, ctas, plan->adapters_prepared[0], s);
 }
 
 }  // namespace
@@ -349,10 +351,9 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     f.part = part;
     f.idesc = make_idesc(true, input_format(plan->in_dtype), true, true, 128, 2 * part);
     f.M = M;
-    const int stage = tcdt::factor_stage_bytes(part);
-    f.stages = tcdt::kAdapterSharedBytes / stage;
-    if (f.stages > tcdt::kAdapterMaxStages) f.stages = tcdt::kAdapterMaxStages;
     f.splits = splits_of(plan, items, (M + 63) / 64, 4);
+    f.stages = tcdt::kAdapterSharedBytes / tcdt::factor_stage_bytes(part);
+    if (f.stages > tcdt::kAdapterMaxStages) f.stages = tcdt::kAdapterMaxStages;
     f.out_kind = out_dtype == GEMM_F32 ? 0u : out_dtype == GEMM_F16 ? 1u : 2u;
     f.status = plan->d_status;
     f.timeout_ns = plan->timeout_ns;

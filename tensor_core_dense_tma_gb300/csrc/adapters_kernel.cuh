@@ -13,7 +13,9 @@
 namespace tcdt {
 
 constexpr int kAdapterThreads = 192;                  // producer, MMA and four epilogue warps
-constexpr int kAdapterSharedBytes = 96 * 1024;        // of stages: two CTAs an SM
+// Shared memory of the stages, for two CTAs an SM: with one of twice as much, clusters of
+// eight found no eight free SMs together (8192 x 8192, rank 64: 31 us to 66).
+constexpr int kAdapterSharedBytes = 96 * 1024;
 constexpr int kAdapterMaxStages = 6;
 constexpr uint32_t kChunk = 8192;                     // 64 x 64 16-bit elements
 
@@ -95,10 +97,11 @@ struct HiddenArgs {
     const int32_t* index;
     const float* scale;
     int32_t count, rank, part;
-    int32_t rr;               // the rank in whole 16s: N of the MMAs
-    int32_t per_stage;        // adapters of a stage
+    int32_t rr;               // the rank in whole 16s
+    int32_t per_stage;        // adapters of a stage, whose columns lie side by side:
+    int32_t pitch;            // columns from one to the next (rr, or 64 or 128)
     uint32_t a_mn;            // 1: down factors are rank-contiguous
-    uint32_t idesc;
+    uint32_t idesc, idesc_one;    // N = per_stage * pitch, and for one adapter rr
     int32_t M, k_blocks, splits, stages;
     uint16_t* hidden;
     int64_t ldh;
@@ -107,91 +110,150 @@ struct HiddenArgs {
     uint64_t timeout_ns;
 };
 
-constexpr int kHiddenStage = 128 * 128 + 128 * 128;
+// A stage: a block of X, and the adapters' (8 KB: 4 of rank 16, 1 of rank 64).
+__host__ __device__ constexpr int hidden_stage_bytes(int rr) { return 128 * 128 + (rr <= 64 ? 8192 : 16384); }
 
-// A cluster of a.splits CTAs computes 128 rows.  All adapters of a tile
-// accumulate in the same columns of tensor memory, each in its own rows (MMAs
-// that leave the others as they are), so one pass over X serves any number; with more
-// than fit a stage, X comes again from L2 with the next ones.
-// 8192 x 8192 bf16, 4 adapters of rank 64: see the table of DESIGN.
+// A cluster of a.splits CTAs computes 128 rows.  The adapters of a stage have
+// columns of their own in tensor memory, up to 128 together, and a row takes those of
+// its adapter.  With more adapters than fit a stage, X comes again from L2 with
+// the next ones, which use the same columns in their own rows: MMAs that leave the
+// other rows as they are (those take some 200 cycles each, whatever their N; done
+// adapter by adapter, 2048 x 4096 with one adapter a tile took 0.45 us a block of
+// K, 16 us in all).
 __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __grid_constant__ HiddenArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ AdapterPipe q;
     __shared__ int list[128], listed;
-    __shared__ uint32_t off[128][4];          // rows that are not the adapter's
+    __shared__ uint32_t off[128][4];          // rows that are not of a group's adapters
+    __shared__ uint8_t slot[128];             // a row's adapter among those of its group
+    __shared__ float factor[128];             // its scale
+    __shared__ bool given[128];               // whether it has one
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int row0 = static_cast<int>(blockIdx.x / a.splits) * 128;
-    const uint32_t tmem_cols = a.rr <= 32 ? 32u : a.rr <= 64 ? 64u : 128u;
+    constexpr uint32_t kCols = 128;
     const bool bf16 = a.bf16 != 0;
+
+    const int kb0 = a.k_blocks * rank / a.splits, kb1 = a.k_blocks * (rank + 1) / a.splits;
+    auto stage_at = [&](int s) { return base + static_cast<uint32_t>(s * hidden_stage_bytes(a.rr)); };
 
     griddep_launch();
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_desc(&a.tmX);
             tma_prefetch_desc(&a.tmA);
             adapter_pipe_init(q, a.stages);
+            // the first blocks of X, before the adapters are known (0.6 us); a tile
+            // without adapters waits for them at its end
+            for (int i = 0; i < a.stages && i < kb1 - kb0; ++i) {
+                mbar_expect_tx(smem_addr(&q.full[i]), 128 * 128);
+                tma_load_2d(stage_at(i), &a.tmX, smem_addr(&q.full[i]), 64 * (kb0 + i), row0);
+            }
         }
-        AdapterWalk<128> walk(a.index, a.count, row0, a.M, lane);
+        __syncwarp();
+        AdapterWalk<128> walk;
+        walk.load(a.index, a.count, row0, a.M, lane);
         uint32_t m[4];
         int g, n = 0;
+        uint32_t rows[4] = {~0u, ~0u, ~0u, ~0u};
         while (walk.next(g, m)) {
-            if (lane == 0) {
-                list[n] = g;
+            const int at = n % a.per_stage;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) off[n][w] = m[w];
+            for (int w = 0; w < 4; ++w) {
+                rows[w] = at == 0 ? m[w] : rows[w] & m[w];
+                if (!(m[w] >> lane & 1u)) slot[32 * w + lane] = static_cast<uint8_t>(at);
+                if (lane == 0) off[n / a.per_stage][w] = rows[w];
             }
+            if (lane == 0) list[n] = g;
             ++n;
         }
         if (lane == 0) listed = n;
         __syncwarp();
     }
+    if (warp >= 2) {
+        // (here, not where they are used: two loads that wait for one another)
+        const int row = row0 + static_cast<int>(threadIdx.x) - 64;
+        const int g = row < a.M ? __ldg(a.index + row) : -1;
+        factor[threadIdx.x - 64] = g < 0 || g >= a.count ? 0.0f : a.scale ? __ldg(a.scale + g) : 1.0f;
+        given[threadIdx.x - 64] = g >= 0 && g < a.count;
+    }
     if (warp == 1) {
-        tmem_alloc<1>(smem_addr(&q.tmem), tmem_cols);
+        tmem_alloc<1>(smem_addr(&q.tmem), kCols);
         tmem_relinquish_alloc_permit<1>();
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = q.tmem;
-    const int n = listed;
-    const int kb0 = a.k_blocks * rank / a.splits, kb1 = a.k_blocks * (rank + 1) / a.splits;
+    const int n = warp_uniform<8>(listed);
+    const int early = min(a.stages, kb1 - kb0);        // blocks of X that are under way
     const int groups = (n + a.per_stage - 1) / a.per_stage;
     const uint32_t a_bytes = a.a_mn ? (a.rr <= 64 ? kChunk : 2 * kChunk) : static_cast<uint32_t>(a.rr) * 128u;
     const WaitCtx wctx{a.status, a.timeout_ns, &q.abort_flag};
-    auto stage_at = [&](int s) { return base + static_cast<uint32_t>(s) * kHiddenStage; };
     bool ok = true;
+    // The order of the steps: the first `early` stages take the first group of
+    // adapters of blocks kb0 .., whose X is on its way; then those blocks' other groups,
+    // and the other blocks.  (Counted, not divided: two divisions a step were half of the
+    // producer's time.)
+    const int steps = (kb1 - kb0) * groups;
+    struct Step {
+        int i = 0, kb, j = 0;
+    };
+    auto advance = [&](Step& s) {
+        if (++s.i < early) {
+            ++s.kb;
+        } else if (s.i == early && groups > 1) {
+            s.kb = kb0, s.j = 1;
+        } else if (++s.j >= groups) {
+            ++s.kb;
+            s.j = groups > 1 && s.kb < kb0 + early ? 1 : 0;
+        }
+    };
 
     if (warp == 0) {
         RingAt at;
-        int64_t issued = 0;
-        for (int kb = kb0; ok && kb < kb1; ++kb)
-            for (int j = 0; j < groups; ++j) {
-                if (!warp_wait_phase(smem_addr(&q.empty[at.stage]), at.phase ^ 1u, wctx, kSiteProducerEmpty)) {
-                    ok = false;
-                    break;
+        int issued = 0;
+        if (groups == 0) {
+            for (int i = 0; i < early; ++i) {
+                if (elect_one_sync()) mbar_arrive(smem_addr(&q.full[i]));
+                __syncwarp();
+            }
+            issued = early;
+            for (int i = 0; i < early; ++i) at.next(a.stages);
+            ok = false;               // nothing more: wait for them below
+        }
+        for (Step s{0, kb0, 0}; ok && s.i < steps; advance(s)) {
+            if (!warp_wait_phase(smem_addr(&q.empty[at.stage]), at.phase ^ 1u, wctx, kSiteProducerEmpty)) {
+                // (the early copies of X land all the same)
+                for (int k = s.i; k < early; ++k) {
+                    if (elect_one_sync()) mbar_arrive(smem_addr(&q.full[at.stage]));
+                    __syncwarp();
+                    ++issued;
+                    at.next(a.stages);
                 }
-                const uint32_t bar = smem_addr(&q.full[at.stage]), sx = stage_at(at.stage), sa = sx + 128 * 128;
-                const int first = j * a.per_stage, here = min(a.per_stage, n - first);
-                if (elect_one_sync()) {
-                    mbar_arrive_expect_tx(bar, 128 * 128 + here * a_bytes);
-                    tma_load_2d(sx, &a.tmX, bar, 64 * kb, row0);
-                    for (int i = 0; i < here; ++i) {
-                        const int g = list[first + i];
-                        const uint32_t dst = sa + i * a_bytes;
-                        if (a.a_mn) {
-                            tma_load_3d(dst, &a.tmA, bar, 0, 64 * kb, g);
-                            if (a.rr > 64) tma_load_3d(dst + kChunk, &a.tmA, bar, 64, 64 * kb, g);
-                        } else {
-                            tma_load_3d(dst, &a.tmA, bar, 64 * kb, 0, g);
-                        }
+                ok = false;
+                break;
+            }
+            const uint32_t bar = smem_addr(&q.full[at.stage]), sx = stage_at(at.stage), sa = sx + 128 * 128;
+            const int first = s.j * a.per_stage, here = min(a.per_stage, n - first);
+            if (elect_one_sync()) {
+                mbar_arrive_expect_tx(bar, (s.i < early ? 0u : 128u * 128u) + here * a_bytes);
+                if (s.i >= early) tma_load_2d(sx, &a.tmX, bar, 64 * s.kb, row0);
+                for (int e = 0; e < here; ++e) {
+                    const int g = list[first + e];
+                    const uint32_t dst = sa + e * a_bytes;
+                    if (a.a_mn) {
+                        tma_load_3d(dst, &a.tmA, bar, 0, 64 * s.kb, g);
+                        if (a.rr > 64) tma_load_3d(dst + kChunk, &a.tmA, bar, 64, 64 * s.kb, g);
+                    } else {
+                        tma_load_3d(dst, &a.tmA, bar, 64 * s.kb, 0, g);
                     }
                 }
-                __syncwarp();
-                ++issued;
-                at.next(a.stages);
             }
+            __syncwarp();
+            ++issued;
+            at.next(a.stages);
+        }
         if (!ok) {
             // wind down: let the copies already issued land before exiting
             for (int i = 0; i < a.stages && i < issued; ++i) {
@@ -202,36 +264,37 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
     } else if (warp == 1) {
         RingAt at;
         const uint32_t lbo = a.a_mn ? kChunk : 16u, kstep = a.a_mn ? 16u * 128u : 32u;
-        for (int kb = kb0; ok && kb < kb1; ++kb)
-            for (int j = 0; j < groups; ++j) {
-                if (!warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteMmaFull)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t sx = stage_at(at.stage), sa = sx + 128 * 128;
-                const int first = j * a.per_stage, here = min(a.per_stage, n - first);
-                if (elect_one_sync()) {
-                    for (int i = 0; i < here; ++i) {
-                        const uint32_t m[4] = {off[first + i][0], off[first + i][1], off[first + i][2], off[first + i][3]};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_f16_ss_rows<1>(tmem, smem_desc_sw128(sx + k * 32u, 16u, 1024u),
-                                                smem_desc_sw128(sa + i * a_bytes + k * kstep, lbo, 1024u), a.idesc, m,
-                                                kb != kb0 || k != 0 ? 1u : 0u);
-                    }
-                    umma_commit<1>(smem_addr(&q.empty[at.stage]));
-                }
-                __syncwarp();
-                at.next(a.stages);
+        for (Step s{0, kb0, 0}; s.i < steps; advance(s)) {
+            if (!warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteMmaFull)) {
+                ok = false;
+                break;
             }
+            tc_fence_after_sync();
+            const uint32_t sx = stage_at(at.stage), sa = sx + 128 * 128;
+            if (elect_one_sync()) {
+                const uint32_t m[4] = {off[s.j][0], off[s.j][1], off[s.j][2], off[s.j][3]};
+                const uint32_t idesc = n == 1 ? a.idesc_one : a.idesc;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t xdesc = smem_desc_sw128(sx + k * 32u, 16u, 1024u);
+                    const uint64_t adesc = smem_desc_sw128(sa + k * kstep, lbo, 1024u);
+                    const uint32_t more = s.kb != kb0 || k != 0 ? 1u : 0u;
+                    if (groups == 1) umma_f16_ss<1>(tmem, xdesc, adesc, idesc, more);
+                    else umma_f16_ss_rows<1>(tmem, xdesc, adesc, idesc, m, more);
+                }
+                umma_commit<1>(smem_addr(&q.empty[at.stage]));
+            }
+            __syncwarp();
+            at.next(a.stages);
+        }
         if (elect_one_sync()) umma_commit<1>(smem_addr(&q.acc));
         __syncwarp();
         if (!ok) wait_phase_drain(smem_addr(&q.acc), 0, 100000000ull);
     }
     __syncwarp();
-    // the four epilogue warps: this CTA's sums of 128 rows, in shared memory, rows rr + 4 apart
-    const int pitch = a.rr + 4;
+    // the four epilogue warps: this CTA's sums of 128 rows, in shared memory, rows 132 numbers apart
+    constexpr int kPitch = 128 + 4;
+    const int columns = n == 1 ? a.rr : min(n, a.per_stage) * a.pitch;
     float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_addr(smem_raw)));
     const int t = static_cast<int>(threadIdx.x) - 64;
     if (warp >= 2) {
@@ -239,13 +302,13 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
         if (ok && n > 0) {
             tc_fence_after_sync();
             const int quad = warp & 3, row = 32 * quad + lane;
-            for (int c = 0; c < a.rr; c += 16) {
+            for (int c = 0; c < columns; c += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * quad) << 16) + c, r);
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<uint4*>(sums + row * pitch + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                    *reinterpret_cast<uint4*>(sums + row * kPitch + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
             }
             tc_fence_before_sync();
         }
@@ -259,15 +322,13 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
         for (int i = t; i < rows * quads; i += 128) {
             const int row = rank * rows + i / quads, c = i % quads * 4;
             if (row0 + row >= a.M) continue;
-            const int g = __ldg(a.index + row0 + row);
             float v[4] = {};
-            if (g >= 0 && g < a.count && c < a.rr) {
-                const uint32_t from = smem_addr(sums + row * pitch + c);
+            if (given[row] && c < a.rr) {
+                const uint32_t from = smem_addr(sums + row * kPitch + slot[row] * a.pitch + c);
                 const float4 sum = a.splits > 1 ? cluster_sum4(from, a.splits) : ld_shared_v4f(from);
                 v[0] = sum.x, v[1] = sum.y, v[2] = sum.z, v[3] = sum.w;
-                const float scale = a.scale ? __ldg(a.scale + g) : 1.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = c + e < a.rank ? v[e] * scale : 0.0f;
+                for (int e = 0; e < 4; ++e) v[e] = c + e < a.rank ? v[e] * factor[row] : 0.0f;
             }
             uint16_t hi[4], lo[4];
 #pragma unroll
@@ -283,7 +344,7 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc<1>(tmem, tmem_cols);
+        tmem_dealloc<1>(tmem, kCols);
     }
 }
 
@@ -390,7 +451,8 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
             if (lane == 0) listed = n;
         }
         __syncthreads();
-        const int first = listed * rank / a.splits, last = listed * (rank + 1) / a.splits;
+        const int found = warp_uniform<11>(listed);
+        const int first = found * rank / a.splits, last = found * (rank + 1) / a.splits;
         if (warp == 0) {
             for (int i = first; ok && i < last; ++i) {
                 if (!warp_wait_phase(smem_addr(&q.empty[at.stage]), at.phase ^ 1u, wctx, kSiteProducerEmpty)) {

@@ -141,27 +141,36 @@ struct AdapterArgs {
 // The adapters of a tile's rows, each once, in the order of their first rows.
 // A warp's lane i holds rows i, 32 + i, ...; every warp that walks a tile sees
 // the same order.
-template <int ROWS>
+template <int ROWS, bool EACH = false>
 struct AdapterWalk {
     int idx[ROWS / 32];       // -1: none, or done
+    uint32_t given[ROWS / 32];    // rows that count: all of the tile's, or (EACH) those with an adapter
 
-    __device__ __forceinline__ AdapterWalk(const int32_t* index, int count, int row0, int M, int lane) {
+    __device__ __forceinline__ void load(const int32_t* index, int count, int row0, int M, int lane) {
 #pragma unroll
         for (int w = 0; w < ROWS / 32; ++w) {
             const int row = row0 + 32 * w + lane;
             const int g = row < M ? __ldg(index + row) : -1;
             idx[w] = g < count ? g : -1;
         }
+#pragma unroll
+        for (int w = 0; w < ROWS / 32; ++w)
+            given[w] = __ballot_sync(0xffffffffu, EACH ? idx[w] >= 0 : row0 + 32 * w + lane < M);
     }
     // The next adapter, and a bit for each row that it is not the adapter of.
+    // (What it returns comes from ballots alone: the loop over it is then known to be
+    // the same in all lanes, without which an MMA issued in it takes twice as long.)
     __device__ __forceinline__ bool next(int& g, uint32_t (&off)[ROWS / 32]) {
+        uint32_t any = 0;
         g = -1;
 #pragma unroll
         for (int w = 0; w < ROWS / 32; ++w) {
             const uint32_t left = __ballot_sync(0xffffffffu, idx[w] >= 0);
-            if (g < 0 && left) g = __shfl_sync(0xffffffffu, idx[w], __ffs(left) - 1);
+            const int first = __shfl_sync(0xffffffffu, idx[w], left ? __ffs(left) - 1 : 0);
+            if (!any && left) g = first;
+            any |= left;
         }
-        if (g < 0) return false;
+        if (!any) return false;
 #pragma unroll
         for (int w = 0; w < ROWS / 32; ++w) {
             const bool here = idx[w] == g;
@@ -171,6 +180,15 @@ struct AdapterWalk {
         return true;
     }
 };
+
+// x, which is the same in all lanes, in a form that the compiler knows to be.
+template <int BITS>
+__device__ __forceinline__ int warp_uniform(int x) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) v |= (__ballot_sync(0xffffffffu, x >> b & 1) & 1u) << b;
+    return static_cast<int>(v);
+}
 
 // A 16-bit value of the plan's type.
 __device__ __forceinline__ float adapter_value(uint32_t bits, bool bf16) {
@@ -1302,8 +1320,9 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         griddep_wait();      // h comes from the kernel before this one
                         constexpr int kRows = kAdapterTokens ? (Cfg::BN + 31) / 32 * 32 : Cfg::UMMA_M;
                         const int tokens = half ? Cfg::BN / 2 : Cfg::BN;
-                        AdapterWalk<kRows> walk(ad.index, ad.count, kAdapterTokens ? n0 : mb * Cfg::UMMA_M,
-                                                kAdapterTokens ? min(p.N, n0 + tokens) : p.M, lane);
+                        AdapterWalk<kRows> walk;
+                        walk.load(ad.index, ad.count, kAdapterTokens ? n0 : mb * Cfg::UMMA_M,
+                                  kAdapterTokens ? min(p.N, n0 + tokens) : p.M, lane);
                         const uint32_t u_tx = ad.u_mn ? static_cast<uint32_t>(b_chunks * 64 * 128)
                                               : half  ? Cfg::BN_CTA_HALF * 128u
                                                       : Cfg::BN_CTA * 128u;
@@ -1427,6 +1446,20 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 const uint32_t d_tmem = tmem_base + buf * Cfg::ACC_COLS;
                 const bool seeded = x.role == kRoleOwner;   // accumulate from the first MMA on
                 const uint32_t idesc = (Cfg::HALVES_OK && x.half >= 0) ? p.idesc_half : p.idesc;
+                // the rows' adapters are asked for here: after the K loop, whose MMAs
+                // still run then, their latency would be a pause of the tensor pipe
+                constexpr int kRows = kAdapterTokens ? (Cfg::BN + 31) / 32 * 32 : Cfg::UMMA_M;
+                AdapterWalk<kRows, kAdapterTokens> walk;
+                if constexpr (AD::kOn) {
+                    int mb, nb;
+                    tile_coords(p, x.tile, mb, nb);
+                    const bool half = Cfg::HALVES_OK && x.half >= 0;
+                    const int tokens = half ? Cfg::BN / 2 : Cfg::BN;
+                    const int n0 = nb * Cfg::BN + (half ? x.half * tokens : 0);
+                    if (x.kb1 == p.num_k_blocks)
+                        walk.load(ad.index, ad.count, kAdapterTokens ? n0 : mb * Cfg::UMMA_M,
+                                  kAdapterTokens ? min(p.N, n0 + tokens) : p.M, lane);
+                }
                 for (int kb = x.kb0; kb < x.kb1; ++kb) {
                     if (!warp_wait_phase(full_bar(stage), phase, wctx, kSiteMmaFull)) {
                         ok = false;
@@ -1458,15 +1491,8 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 if (!ok) break;
                 if constexpr (AD::kOn) {
                     if (x.kb1 == p.num_k_blocks) {
-                        int mb, nb;
-                        tile_coords(p, x.tile, mb, nb);
-                        constexpr int kRows = kAdapterTokens ? (Cfg::BN + 31) / 32 * 32 : Cfg::UMMA_M;
-                        const bool half = Cfg::HALVES_OK && x.half >= 0;
-                        const int tokens = half ? Cfg::BN / 2 : Cfg::BN;
-                        const int n0 = nb * Cfg::BN + (half ? x.half * tokens : 0);
-                        AdapterWalk<kRows> walk(ad.index, ad.count, kAdapterTokens ? n0 : mb * Cfg::UMMA_M,
-                                                kAdapterTokens ? min(p.N, n0 + tokens) : p.M, lane);
-                        const uint32_t idesc_u = half && kAdapterRows ? ad.idesc_half : ad.idesc;
+                        const uint32_t idesc_u =
+                            Cfg::HALVES_OK && x.half >= 0 && kAdapterRows ? ad.idesc_half : ad.idesc;
                         const uint32_t to = kAdapterTokens ? tmem_base + kDeltaCol * (1 + buf) : d_tmem;
                         const uint32_t u_lbo = ad.u_mn ? Cfg::MN_CHUNK_BYTES : 16u;
                         const uint32_t u_kstep = ad.u_mn ? 16u * 128u : 32u;
@@ -1476,8 +1502,14 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         for (int w = 0; w < 4 * CG; ++w) rows_off[w] = 0xFFFFFFFFu;
                         int g;
                         while (ok && walk.next(g, off)) {
+                            // all rows of a tile one adapter's (rows beyond M do not count; in
+                            // transposed tiles nor do those without one): ordinary MMAs
+                            uint32_t others = 0;
 #pragma unroll
-                            for (int w = 0; w < kRows / 32; ++w) rows_off[w] = off[w];
+                            for (int w = 0; w < kRows / 32; ++w) {
+                                rows_off[w] = off[w];
+                                others |= walk.given[w] & off[w];
+                            }
 #pragma unroll 1
                             for (int st = 0; st < steps; ++st) {
                                 if (!warp_wait_phase(full_bar(stage), phase, wctx, kSiteMmaFull)) {
@@ -1497,8 +1529,9 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                                         const uint64_t udesc = smem_desc_sw128(
                                             su + static_cast<uint32_t>((j & 63) >> 4) * u_kstep, u_lbo, 1024u);
                                         // (transposed: the adapter's first MMA sets its rows)
-                                        umma_f16_ss_rows<CG>(to, hdesc, udesc, idesc_u, rows_off,
-                                                             kAdapterTokens && st == 0 && k == 0 ? 0u : 1u);
+                                        const uint32_t more = kAdapterTokens && st == 0 && k == 0 ? 0u : 1u;
+                                        if (others) umma_f16_ss_rows<CG>(to, hdesc, udesc, idesc_u, rows_off, more);
+                                        else umma_f16_ss<CG>(to, hdesc, udesc, idesc_u, more);
                                     }
                                     umma_commit<CG>(empty_bar(stage), kPair);
                                 }
