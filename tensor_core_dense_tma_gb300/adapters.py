@@ -47,14 +47,14 @@ _calls: dict = {}     # the library's entry points and torch, filled on the firs
 
 
 def _lib():
-    if not _calls:
-        import torch
-        from . import load, DTYPE, GemmError
-        lib = load()
-        _calls.update(torch=torch, error=GemmError, run=lib.gemm_run_adapters, grad=lib.gemm_adapters_grad,
-                      codes={torch.float16: DTYPE["f16"], torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"]},
-                      types={"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32})
-    return _calls["torch"]
+    import torch
+    from . import load, DTYPE, GemmError
+    lib = load()
+    _calls.update(torch=torch, error=GemmError, run=lib.gemm_run_adapters, grad=lib.gemm_adapters_grad,
+                  codes={torch.float16: DTYPE["f16"], torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"]},
+                  types={"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}, empty=torch.empty,
+                  stream=torch._C._cuda_getCurrentRawStream, f32=torch.float32, i32=torch.int32)
+    return _calls
 
 
 def hidden_width(rank: int) -> int:
@@ -62,13 +62,23 @@ def hidden_width(rank: int) -> int:
     return 32 if rank <= 16 else 64 if rank <= 32 else 128 if rank <= 64 else 256
 
 
-def _row_ld(t, what: str, dev, dtype):
-    """Row stride of a row-major matrix of the plan's type on its device."""
-    if t.dim() != 2 or t.dtype != dtype or t.device != dev:
+# A decoding step's kernels take ten to thirty microseconds, so what follows looks at each
+# tensor once (an attribute of a tensor is 0.1 us, a call 0.2), and sorts out what
+# is wrong only once something is.
+
+def _refuse_matrix(t, what: str, di: int, dtype):
+    if t.dim() != 2 or t.dtype != dtype or t.get_device() != di:
         raise ValueError(f"{what} must be a 2-D {dtype} tensor on X's device")
+    raise ValueError(f"{what} must be row-major (strides {t.stride()})")
+
+
+def _row_ld(t, what: str, di: int, dtype) -> int:
+    """Row stride of a row-major matrix of the plan's type on device di."""
+    if t.dim() != 2 or t.dtype is not dtype or t.get_device() != di:
+        _refuse_matrix(t, what, di, dtype)
     (r, c), (s0, s1) = t.shape, t.stride()
-    if (c > 1 and s1 != 1) or (r > 1 and s0 < c):
-        raise ValueError(f"{what} must be row-major (strides {t.stride()})")
+    if (s1 != 1 and c > 1) or (s0 < c and r > 1):
+        _refuse_matrix(t, what, di, dtype)
     return s0 if r > 1 else -(-c // 8) * 8
 
 
@@ -85,96 +95,89 @@ def _order(r, c, s0, s1):
     return (s1, 1) if r <= 1 else None
 
 
-def _stack(t, what: str, dev, dtype, shape):
+def _stack(t, what: str, di: int, dtype, G, r, c):
     """(address, leading dimension, stride, layout) of a stack of matrices."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != dev or tuple(t.shape) != shape:
-        raise ValueError(f"{what} must be a {shape[0]} x {shape[1]} x {shape[2]} {dtype} tensor on X's device")
+    if t.dtype is not dtype or t.get_device() != di or t.shape != (G, r, c):
+        raise ValueError(f"{what} must be a {G} x {r} x {c} {dtype} tensor on X's device")
     s, s0, s1 = t.stride()
-    order = _order(shape[1], shape[2], s0, s1)
+    order = _order(r, c, s0, s1)
     if order is None:
         raise ValueError(f"{what} must have unit stride along one of its last two dimensions (strides {t.stride()})")
-    return t.data_ptr(), order[0], (s if shape[0] > 1 else 0), order[1]
+    return t.data_ptr(), order[0], (s if G > 1 else 0), order[1]
 
 
-def _adapters(down, up, index, scale, M, N, K, dev, dtype):
-    torch = _calls["torch"]
+def _adapters(down, up, index, scale, M, N, K, di, dtype):
     if down.dim() != 3 or up.dim() != 3:
         raise ValueError("down must be G x R x K, up G x N x R")
-    G, R = down.shape[0], down.shape[1]
+    G, R, _ = down.shape
     if not 1 <= R <= MAX_RANK:
         raise ValueError(f"the rank must be 1..{MAX_RANK}")
-    if index.dtype != torch.int32 or index.shape != (M,) or index.device != dev or (M > 1 and index.stride(0) != 1):
+    if index.dtype is not _calls["i32"] or index.shape != (M,) or index.get_device() != di or not index.is_contiguous():
         raise ValueError("index must be a contiguous int32 vector with one entry per row on X's device")
-    if scale is not None and (scale.dtype != torch.float32 or scale.shape != (G,) or scale.device != dev
-                              or (G > 1 and scale.stride(0) != 1)):
+    if scale is not None and (scale.dtype is not _calls["f32"] or scale.shape != (G,) or scale.get_device() != di
+                              or not scale.is_contiguous()):
         raise ValueError("scale must be a contiguous fp32 vector with one entry per adapter on X's device")
-    return Adapters(G, R, *_stack(down, "down", dev, dtype, (G, R, K)), *_stack(up, "up", dev, dtype, (G, N, R)),
-                    scale.data_ptr() if scale is not None else None, index.data_ptr())
+    return Adapters(G, R, *_stack(down, "down", di, dtype, G, R, K), *_stack(up, "up", di, dtype, G, N, R),
+                    None if scale is None else scale.data_ptr(), index.data_ptr())
 
 
-def _hidden(hidden, what, M, R, dev, dtype):
+def _hidden(hidden, what, M, R, dev, di, dtype):
     width = hidden_width(R)
     if hidden is None:
-        hidden = _calls["torch"].empty((M, width), dtype=dtype, device=dev)
-        return hidden, width
-    if tuple(hidden.shape) != (M, width):
+        return _calls["empty"]((M, width), dtype=dtype, device=dev), width
+    if hidden.shape != (M, width):
         raise ValueError(f"{what} must be {M} x {width}")
-    return hidden, _row_ld(hidden, what, dev, dtype)
-
-
-def _columns(B, K, what: str, dev, dtype):
-    """(N, leading dimension, layout) of the K x N matrix B."""
-    if B.dim() != 2 or B.dtype != dtype or B.device != dev:
-        raise ValueError(f"{what} must be a 2-D {dtype} tensor on X's device")
-    if B.shape[0] != K:
-        raise ValueError("inner dimensions differ")
-    order = _order(*B.shape, *B.stride())
-    if order is None:
-        raise ValueError(f"{what} must be row- or column-major (strides {B.stride()})")
-    return B.shape[1], *order
+    return hidden, _row_ld(hidden, what, di, dtype)
 
 
 def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, stream):
     """Plan.linear_adapters."""
-    torch = _lib()
-    dev, dtype = X.device, _calls["types"].get(plan.in_dtype)
-    if dtype not in (torch.float16, torch.bfloat16) or dev.type != "cuda" or X.dim() != 2:
+    calls = _calls or _lib()
+    types = calls["types"]
+    dtype, dev, di = types.get(plan.in_dtype), X.device, X.get_device()
+    if dtype is None or dtype is calls["f32"] or di < 0 or X.dim() != 2 or B.dim() != 2:
         raise ValueError("adapters take 2-D device tensors and an f16 or bf16 plan")
-    M, K = X.shape
-    ldx = _row_ld(X, "X", dev, dtype)
-    N, ldb, layout = _columns(B, K, "B", dev, dtype)
-    a = _adapters(down, up, index, scale, M, N, K, dev, dtype)
+    (M, K), (KB, N) = X.shape, B.shape
+    ldx = _row_ld(X, "X", di, dtype)
+    if B.dtype is not dtype or B.get_device() != di:
+        raise ValueError(f"B must be a 2-D {dtype} tensor on X's device")
+    if KB != K:
+        raise ValueError("inner dimensions differ")
+    order = _order(K, N, *B.stride())
+    if order is None:
+        raise ValueError(f"B must be row- or column-major (strides {B.stride()})")
+    a = _adapters(down, up, index, scale, M, N, K, di, dtype)
     if D is None:
-        D = torch.empty((M, N), dtype=_calls["types"][out_dtype or plan.in_dtype], device=dev)
+        out = types[out_dtype or plan.in_dtype]
+        D = calls["empty"]((M, N), dtype=out, device=dev)
         ldd = N
     else:
-        if out_dtype is not None and D.dtype != _calls["types"][out_dtype]:
+        out = D.dtype
+        if out_dtype is not None and out is not types[out_dtype]:
             raise ValueError("D must have the output type")
         d0, d1 = D.stride() if D.dim() == 2 else (0, 0)
-        if D.dtype not in _calls["codes"] or D.shape != (M, N) or D.device != dev or (N > 1 and d1 != 1) or \
-                (M > 1 and d0 < N):
+        if out not in calls["codes"] or D.shape != (M, N) or D.get_device() != di or (d1 != 1 and N > 1) or \
+                (d0 < N and M > 1):
             raise ValueError("D must be a row-major M x N matrix on X's device")
         ldd = d0 if M > 1 else N
-    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or bias.device != dev
-                             or (N > 1 and bias.stride(0) != 1)):
+    if bias is not None and (bias.dtype is not calls["f32"] or bias.shape != (N,) or bias.get_device() != di
+                             or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous fp32 vector of length N on X's device")
-    hidden, ldh = _hidden(hidden, "hidden", M, a.rank, dev, dtype)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    st = _calls["run"](plan.handle, X.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, ldx, ldb, ldd, layout,
-                       _calls["codes"][D.dtype], bias.data_ptr() if bias is not None else None, ctypes.byref(a),
-                       hidden.data_ptr(), ldh, stream)
+    hidden, ldh = _hidden(hidden, "hidden", M, a.rank, dev, di, dtype)
+    st = calls["run"](plan.handle, X.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, ldx, order[0], ldd, order[1],
+                      calls["codes"][out], None if bias is None else bias.data_ptr(), ctypes.byref(a),
+                      hidden.data_ptr(), ldh, calls["stream"](di) if stream is None else stream)
     if st != 0:
-        raise _calls["error"](st, "gemm_run_adapters")
+        raise calls["error"](st, "gemm_run_adapters")
     return D, hidden
 
 
-def _gradient(t, dtype, dev, shape, what):
+def _gradient(t, dtype, dev, di, shape, what):
     """(tensor, leading dimension, stride) of an output stack, allocated if not given."""
     G, rows, cols = shape
     if t is None:
-        return _calls["torch"].empty(shape, dtype=dtype, device=dev), cols, rows * cols
-    if tuple(t.shape) != shape or t.device != dev:
+        return _calls["empty"](shape, dtype=dtype, device=dev), cols, rows * cols
+    if t.shape != shape or t.get_device() != di:
         raise ValueError(f"{what} must be a {G} x {rows} x {cols} tensor on X's device")
     s, s0, s1 = t.stride()
     if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols) or (G > 1 and s < (rows - 1) * s0 + cols):
@@ -184,31 +187,31 @@ def _gradient(t, dtype, dev, shape, what):
 
 def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up, stream):
     """Plan.linear_adapters_grad."""
-    torch = _lib()
-    dev, dtype = X.device, _calls["types"].get(plan.in_dtype)
+    calls = _calls or _lib()
+    dtype, dev, di = calls["types"].get(plan.in_dtype), X.device, X.get_device()
     if X.dim() != 2 or dY.dim() != 2 or B.dim() != 2 or down.dim() != 3 or up.dim() != 3:
         raise ValueError("X, dY and B must be 2-D, down and up 3-D tensors")
-    (M, K), N, G, R = X.shape, dY.shape[1], down.shape[0], down.shape[1]
-    if dY.shape[0] != M or B.shape != (K, N):
+    (M, K), (MY, N), (G, R, _) = X.shape, dY.shape, down.shape
+    if MY != M or B.shape != (K, N):
         raise ValueError("dY must be M x N, B K x N")
-    ldx = _row_ld(X, "X", dev, dtype)
-    lddy = _row_ld(dY, "dY", dev, dtype)
-    hidden, ldh = _hidden(hidden, "hidden", M, R, dev, dtype)
+    ldx = _row_ld(X, "X", di, dtype)
+    lddy = _row_ld(dY, "dY", di, dtype)
+    hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
     like = d_down if d_down is not None else d_up
     out = dtype if like is None else like.dtype
-    if out not in (torch.float32, dtype) or (d_up is not None and d_up.dtype != out):
+    if out not in (calls["f32"], dtype) or (d_up is not None and d_up.dtype is not out):
         raise ValueError("d_down and d_up must both be fp32 or both of the plan's type")
-    d_down, down_ld, down_stride = _gradient(d_down, out, dev, (G, R, K), "d_down")
-    d_up, up_ld, up_stride = _gradient(d_up, out, dev, (G, N, R), "d_up")
+    d_down, down_ld, down_stride = _gradient(d_down, out, dev, di, (G, R, K), "d_down")
+    d_up, up_ld, up_stride = _gradient(d_up, out, dev, di, (G, N, R), "d_up")
     # dX is the same product the other way round, and leaves p as its hidden rows
-    p = torch.empty_strided((M, hidden_width(R)), (ldh, 1), dtype=dtype, device=dev)
-    dX, _ = linear(plan, dY, B.t(), up.transpose(1, 2), down.transpose(1, 2), index, scale, dX, None, p, None, stream)
+    p = calls["torch"].empty_strided((M, hidden_width(R)), (ldh, 1), dtype=dtype, device=dev)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        stream = calls["stream"](di)
+    dX, _ = linear(plan, dY, B.t(), up.transpose(1, 2), down.transpose(1, 2), index, scale, dX, None, p, None, stream)
     a = Adapters(G, R, None, 0, 0, 0, None, 0, 0, 0, None, index.data_ptr())
-    st = _calls["grad"](plan.handle, X.data_ptr(), dY.data_ptr(), M, N, K, ldx, lddy, ctypes.byref(a),
-                        hidden.data_ptr(), p.data_ptr(), ldh, _calls["codes"][out], d_down.data_ptr(), down_ld,
-                        down_stride, d_up.data_ptr(), up_ld, up_stride, stream)
+    st = calls["grad"](plan.handle, X.data_ptr(), dY.data_ptr(), M, N, K, ldx, lddy, ctypes.byref(a),
+                       hidden.data_ptr(), p.data_ptr(), ldh, calls["codes"][out], d_down.data_ptr(), down_ld,
+                       down_stride, d_up.data_ptr(), up_ld, up_stride, stream)
     if st != 0:
-        raise _calls["error"](st, "gemm_adapters_grad")
+        raise calls["error"](st, "gemm_adapters_grad")
     return AdaptersGrad(dX, d_down, d_up)

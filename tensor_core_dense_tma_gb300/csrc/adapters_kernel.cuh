@@ -26,11 +26,12 @@ struct AdapterPipe {
     int abort_flag, drained;
 };
 
-__device__ __forceinline__ void adapter_pipe_init(AdapterPipe& q, int stages) {
+// empty: arrivals that give a stage back.
+__device__ __forceinline__ void adapter_pipe_init(AdapterPipe& q, int stages, uint32_t empty) {
     for (int i = 0; i < stages; ++i) {
         mbar_init(smem_addr(&q.full[i]), 1);
         mbar_init(smem_addr(&q.ready[i]), 4);
-        mbar_init(smem_addr(&q.empty[i]), 1);
+        mbar_init(smem_addr(&q.empty[i]), empty);
     }
     mbar_init(smem_addr(&q.acc), 1);
     q.abort_flag = 0;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
     if (warp == 0) {
         if (lane == 0) {
             tma_prefetch_desc(&a.tmA);
-            adapter_pipe_init(q, a.stages);
+            adapter_pipe_init(q, a.stages, 1);
             // the first blocks of X, before the adapters are known (0.6 us); a tile
             // without adapters waits for them at its end
             for (int i = 0; i < a.stages && i < kb1 - kb0; ++i) {
@@ -317,25 +318,37 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
     if (a.splits > 1) cluster_sync_all();
     else __syncthreads();
     if (warp >= 2) {
-        // this CTA's share of the rows: sums of all ranges in their order, four columns a thread
-        const int rows = 128 / a.splits, quads = a.part / 4;
-        for (int i = t; i < rows * quads; i += 128) {
-            const int row = rank * rows + i / quads, c = i % quads * 4;
-            if (row0 + row >= a.M) continue;
-            float v[4] = {};
-            if (given[row] && c < a.rr) {
-                const uint32_t from = smem_addr(sums + row * kPitch + slot[row] * a.pitch + c);
-                const float4 sum = a.splits > 1 ? cluster_sum4(from, a.splits) : ld_shared_v4f(from);
-                v[0] = sum.x, v[1] = sum.y, v[2] = sum.z, v[3] = sum.w;
+        // this CTA's share of the rows: sums of all ranges in their order, four columns a
+        // thread, two times four under way together
+        const int rows = 128 / a.splits, quads = a.part / 4, total = rows * quads;
+        const int shift = a.part <= 16 ? 2 : a.part <= 32 ? 3 : a.part <= 64 ? 4 : 5;      // of quads
+        for (int i0 = t; i0 < total; i0 += 256) {
+            float4 sum[2];
+            int row[2], c[2];
+            bool here[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = c + e < a.rank ? v[e] * factor[row] : 0.0f;
+            for (int k = 0; k < 2; ++k) {
+                const int i = i0 + 128 * k;
+                here[k] = i < total;
+                row[k] = rank * rows + (here[k] ? i >> shift : 0), c[k] = (i & (quads - 1)) * 4;
+                sum[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (here[k] && given[row[k]] && c[k] < a.rr) {
+                    const uint32_t from = smem_addr(sums + row[k] * kPitch + slot[row[k]] * a.pitch + c[k]);
+                    sum[k] = a.splits > 1 ? cluster_sum4(from, a.splits) : ld_shared_v4f(from);
+                }
             }
-            uint16_t hi[4], lo[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) adapter_split(v[e], bf16, hi[e], lo[e]);
-            uint16_t* out = a.hidden + (row0 + row) * a.ldh + c;
-            *reinterpret_cast<uint2*>(out) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(out + a.part) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            for (int k = 0; k < 2; ++k) {
+                if (!here[k] || row0 + row[k] >= a.M) continue;
+                const float v[4] = {sum[k].x, sum[k].y, sum[k].z, sum[k].w};
+                uint16_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    adapter_split(c[k] + e < a.rank ? v[e] * factor[row[k]] : 0.0f, bf16, hi[e], lo[e]);
+                uint16_t* out = a.hidden + (row0 + row[k]) * a.ldh + c[k];
+                *reinterpret_cast<uint2*>(out) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2*>(out + a.part) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            }
         }
     }
     __syncwarp();
@@ -404,7 +417,7 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&f.tmX);
         tma_prefetch_desc(&f.tmH);
-        adapter_pipe_init(q, a.stages);
+        adapter_pipe_init(q, a.stages, 5);
     }
     if (warp == 1) {
         tmem_alloc<1>(smem_addr(&q.tmem), tmem_cols);
@@ -419,6 +432,7 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
     RingAt at;
     bool ok = true;
     int64_t used = 0;                    // stages that this CTA has gone through
+    uint32_t mixed = 0;                  // the phases of the `ready` barriers, which tiles with other rows alone use
 
     for (int64_t w0 = 0; w0 * 64 < a.M; w0 += kFactorWindow) {
         const int tiles = static_cast<int>(min(static_cast<int64_t>(kFactorWindow), (a.M + 63) / 64 - w0));
@@ -473,8 +487,12 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
             }
         } else if (warp == 1) {
             for (int i = first; ok && i < last; ++i) {
-                if (!warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteMmaFull) ||
-                    !warp_wait_phase(smem_addr(&q.ready[at.stage]), at.phase, wctx, kSiteMmaFull)) {
+                bool got = warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteMmaFull);
+                if (got && list[i] & 0x8000) {
+                    got = warp_wait_phase(smem_addr(&q.ready[at.stage]), mixed >> at.stage & 1u, wctx, kSiteMmaFull);
+                    mixed ^= 1u << at.stage;
+                }
+                if (!got) {
                     ok = false;
                     break;
                 }
@@ -493,6 +511,7 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
             }
         } else {
             for (int i = first; ok && i < last; ++i) {
+                // (every stage is waited for, so that none is mistaken for a later one)
                 if (!warp_wait_phase(smem_addr(&q.full[at.stage]), at.phase, wctx, kSiteEpilogueAccFull)) {
                     ok = false;
                     break;
@@ -507,9 +526,10 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
                             for (int b = 0; b < 64; b += 16) st_shared_v4(s + c * kChunk + b, 0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&q.ready[at.stage]));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&q.ready[at.stage]));
+                if (lane == 0) mbar_arrive(smem_addr(&q.empty[at.stage]));
                 ++used;
                 at.next(a.stages);
             }
@@ -560,7 +580,7 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
     // joined and stored, an equal share by each CTA, in the order of the output's memory
     const bool by_rank = f.sr == 1;            // consecutive in memory: rank, else columns
     const int total = a.rank * 128, share = (total + a.splits - 1) / a.splits;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = rank * share + threadIdx.x; i < min(total, (rank + 1) * share); i += kAdapterThreads) {
         const int r = by_rank ? i % a.rank : i / 128, c = by_rank ? i / a.rank : i % 128;
         if (col0 + c >= f.columns) continue;

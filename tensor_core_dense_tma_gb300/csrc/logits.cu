@@ -1050,10 +1050,12 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             const float shift = nothing ? 0.f : -log2_S;
             const uint64_t m2 = pair(-s.m, -s.m), shift2 = pair(shift, shift);
             const uint64_t ga2 = pair(nothing ? 0.f : ga, nothing ? 0.f : ga), gb2 = pair(gb, gb);
-            auto gradient = [&](uint64_t x2) {
+            // without a term of the entropy p_j's factor is the same for all of a row
+            const bool plain = OP == kPolicy && a.bonus == 0.f;
+            auto gradient = [&](uint64_t x2, bool plain) {
                 uint64_t l2 = fma2(add2(x2, m2), c2, shift2);
                 uint64_t g2 = ga2;
-                if constexpr (OP != kDistill) {
+                if (OP != kDistill && !plain) {
                     l2 = max_nan2(l2, -200.f);
                     g2 = fma2(gb2, l2, ga2);
                 }
@@ -1074,15 +1076,19 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                 const bool inside = take(seg, b, true, q);
                 const int v0 = b * kChunk + tid;
                 uint4* at = reinterpret_cast<uint4*>(out + seg.first) + v0;
-                if (inside && whole) {
+                auto store_whole = [&](bool plain) {
 #pragma unroll
                     for (int k = 0; k < kUnroll; ++k) {
                         uint64_t x[kPer / 2];
                         Ele<E>::pairs(q[k], x);
 #pragma unroll
-                        for (int e = 0; e < kPer / 2; ++e) x[e] = gradient(x[e]);
+                        for (int e = 0; e < kPer / 2; ++e) x[e] = gradient(x[e], plain);
                         __stcs(at + k * kThreads, Ele<E>::pack_pairs(x));
                     }
+                };
+                if (inside && whole) {
+                    if (OP == kPolicy && plain) store_whole(true);
+                    else store_whole(false);
                 } else {
 #pragma unroll
                     for (int k = 0; k < kUnroll; ++k) {
@@ -1091,7 +1097,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                         uint64_t x[kPer / 2];
                         Ele<E>::pairs(q[k], x);
 #pragma unroll
-                        for (int e = 0; e < kPer / 2; ++e) x[e] = gradient(x[e]);
+                        for (int e = 0; e < kPer / 2; ++e) x[e] = gradient(x[e], plain);
                         if (whole) {
                             at[k * kThreads] = Ele<E>::pack_pairs(x);
                         } else {
@@ -1108,7 +1114,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             }
             if (tid < kPer && !zeros) {
                 float x0, x1;
-                unpair(gradient(pair(x_head, x_tail)), x0, x1);
+                unpair(gradient(pair(x_head, x_tail), plain), x0, x1);
                 if (tid < seg.head) out[tid] = Ele<E>::round(x0);
                 if (tid < seg.tail) out[seg.after + tid] = Ele<E>::round(x1);
             }

@@ -274,23 +274,37 @@ def distill_topk_grad(logits, teacher_tokens, teacher_logits, weight, *, tempera
     return loss, dlogits
 
 
-def _policy_args(logits, tokens, old_logprob, advantage, ref_logprob, clip, kl, entropy_bonus):
-    """The rows' size and type, and the arguments from the tokens to the policy."""
+def _vectors(dtype, n: int, device, **vs):
+    """Addresses of contiguous device vectors (None: None), looked at once each;
+    what is wrong is said once something is."""
+    size, di, out = (n,), device.index, []
+    for what, v in vs.items():
+        if v is None:
+            out.append(None)
+        elif v.dtype is dtype and v.shape == size and v.get_device() == di and v.is_contiguous():
+            out.append(v.data_ptr())
+        else:
+            raise ValueError(f"{what} must be a contiguous {dtype} vector of length {n} on the logits' device")
+    return out
+
+
+def _policy_args(logits, tokens, old_logprob, advantage, weight, ref_logprob, clip, kl, entropy_bonus):
+    """The arguments from the device to the tokens, the policy, the weights' address and the outputs."""
     import torch
     T, V, ld = _matrix(logits, "logits")
     dev = logits.device
-    code = _dtype(logits)
     if tokens is None or old_logprob is None or advantage is None:
         raise ValueError("tokens, old_logprob and advantage must be given")
     if kl != 0 and ref_logprob is None:
         raise ValueError("a KL term needs ref_logprob")
     low, high = clip
-    tok = _vector(tokens, T, torch.int64, dev, "tokens")
-    policy = _Policy(_vector(old_logprob, T, torch.float32, dev, "old_logprob"),
-                     _vector(advantage, T, torch.float32, dev, "advantage"),
-                     _vector(ref_logprob, T, torch.float32, dev, "ref_logprob"), low, high, kl, entropy_bonus)
-    out = [torch.empty((T,), dtype=torch.float32, device=dev) for _ in range(4)]
-    return (T, V, ld), dev, (dev.index, code, logits.data_ptr(), T, V, ld, tok), policy, out
+    tok, = _vectors(torch.int64, T, dev, tokens=tokens)
+    old, adv, ref, w = _vectors(torch.float32, T, dev, old_logprob=old_logprob, advantage=advantage,
+                                ref_logprob=ref_logprob, weight=weight)
+    new = torch.empty_like
+    out = new(old_logprob), new(old_logprob), new(old_logprob), new(old_logprob)
+    return (dev.index, _dtype(logits), logits.data_ptr(), T, V, ld, tok), \
+        _Policy(old, adv, ref, low, high, kl, entropy_bonus), w, out
 
 
 def policy_loss(logits, tokens, old_logprob, advantage, ref_logprob=None, *, clip=(0.2, 0.2), kl: float = 0.0,
@@ -300,11 +314,12 @@ def policy_loss(logits, tokens, old_logprob, advantage, ref_logprob=None, *, cli
     r = exp(logprob - old_logprob) and A the advantage (fp32 vectors).
     ref_logprob gives the KL term against a reference policy.  A row with a
     token outside 0..V-1 has zeros and is not read (logits_policy)."""
-    _, dev, rows, policy, out = _policy_args(logits, tokens, old_logprob, advantage, ref_logprob, clip, kl,
-                                             entropy_bonus)
-    _call("logits_policy", *rows, temperature, ctypes.byref(policy), *(v.data_ptr() for v in out),
-          _stream(stream, dev))
-    return PolicyLoss(*out)
+    rows, policy, _, out = _policy_args(logits, tokens, old_logprob, advantage, None, ref_logprob, clip, kl,
+                                        entropy_bonus)
+    loss, lp, k, ent = out
+    _call("logits_policy", *rows, temperature, ctypes.byref(policy), loss.data_ptr(), lp.data_ptr(), k.data_ptr(),
+          ent.data_ptr(), _stream(stream, logits.device))
+    return PolicyLoss(loss, lp, k, ent)
 
 
 def policy_loss_grad(logits, tokens, old_logprob, advantage, weight, ref_logprob=None, *, clip=(0.2, 0.2),
@@ -313,34 +328,37 @@ def policy_loss_grad(logits, tokens, old_logprob, advantage, weight, ref_logprob
     """policy_loss and the gradient for the logits of sum(weight * loss), in
     one kernel (logits_policy_grad).  Rows without a token or of weight 0 have
     gradients of zeros.  dlogits may be the logits themselves."""
-    import torch
     if weight is None:
         raise ValueError("weight must be given")
-    (T, _, _), dev, rows, policy, out = _policy_args(logits, tokens, old_logprob, advantage, ref_logprob, clip, kl,
-                                                     entropy_bonus)
-    w = _vector(weight, T, torch.float32, dev, "weight")
+    rows, policy, w, out = _policy_args(logits, tokens, old_logprob, advantage, weight, ref_logprob, clip, kl,
+                                        entropy_bonus)
     dlogits, ldd = _gradient(dlogits, logits)
-    _call("logits_policy_grad", *rows, temperature, ctypes.byref(policy), w, *(v.data_ptr() for v in out),
-          dlogits.data_ptr(), ldd, _stream(stream, dev))
-    return PolicyLossGrad(*out, dlogits)
+    loss, lp, k, ent = out
+    _call("logits_policy_grad", *rows, temperature, ctypes.byref(policy), w, loss.data_ptr(), lp.data_ptr(),
+          k.data_ptr(), ent.data_ptr(), dlogits.data_ptr(), ldd, _stream(stream, logits.device))
+    return PolicyLossGrad(loss, lp, k, ent, dlogits)
 
 
-def _preference_args(logits, tokens, offsets, ref_logprob, beta, smoothing):
+def _preference_args(logits, tokens, offsets, weight, ref_logprob, beta, smoothing):
+    """The arguments from the device to the tokens, the preference, the weights' address and the outputs."""
     import torch
     T, V, ld = _matrix(logits, "logits")
     dev = logits.device
-    code = _dtype(logits)
     if tokens is None or offsets is None:
         raise ValueError("tokens and offsets must be given")
-    tok = _vector(tokens, T, torch.int64, dev, "tokens")
     if offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
         raise ValueError("offsets must have an entry for each sequence of a pair and one more")
-    pairs = (offsets.shape[0] - 1) // 2
-    preference = _Preference(_vector(offsets, offsets.shape[0], torch.int64, dev, "offsets"), pairs,
-                             _vector(ref_logprob, T, torch.float32, dev, "ref_logprob"), beta, smoothing)
+    ends = offsets.shape[0]
+    pairs = ends // 2
     f32 = torch.float32
-    out = [torch.empty((n,), dtype=f32, device=dev) for n in (pairs, 2 * pairs, T)]
-    return pairs, T, dev, (dev.index, code, logits.data_ptr(), T, V, ld, tok), preference, out
+    tok, = _vectors(torch.int64, T, dev, tokens=tokens)
+    at, = _vectors(torch.int64, ends, dev, offsets=offsets)
+    ref, = _vectors(f32, T, dev, ref_logprob=ref_logprob)
+    w, = _vectors(f32, pairs, dev, weight=weight)
+    new = torch.empty
+    out = new((pairs,), dtype=f32, device=dev), new((2 * pairs,), dtype=f32, device=dev), new((T,), dtype=f32, device=dev)
+    return (dev.index, _dtype(logits), logits.data_ptr(), T, V, ld, tok), _Preference(at, pairs, ref, beta, smoothing), \
+        w, out
 
 
 def preference_loss(logits, tokens, offsets, ref_logprob=None, *, beta: float = 0.1, smoothing: float = 0.0,
@@ -351,10 +369,11 @@ def preference_loss(logits, tokens, offsets, ref_logprob=None, *, beta: float = 
     times the sum of logprob - ref_logprob over its rows whose token (int64) is
     in 0..V-1, the loss -(1 - smoothing) log sigma(m) - smoothing log sigma(-m)
     of the rewards' difference m (logits_preference)."""
-    _, _, dev, rows, preference, out = _preference_args(logits, tokens, offsets, ref_logprob, beta, smoothing)
-    _call("logits_preference", *rows, temperature, ctypes.byref(preference), *(v.data_ptr() for v in out),
-          _stream(stream, dev))
-    return PreferenceLoss(*out)
+    rows, preference, _, out = _preference_args(logits, tokens, offsets, None, ref_logprob, beta, smoothing)
+    loss, reward, lp = out
+    _call("logits_preference", *rows, temperature, ctypes.byref(preference), loss.data_ptr(), reward.data_ptr(),
+          lp.data_ptr(), _stream(stream, logits.device))
+    return PreferenceLoss(loss, reward, lp)
 
 
 def preference_loss_grad(logits, tokens, offsets, weight, ref_logprob=None, *, beta: float = 0.1,
@@ -367,10 +386,10 @@ def preference_loss_grad(logits, tokens, offsets, weight, ref_logprob=None, *, b
     import torch
     if weight is None:
         raise ValueError("weight must be given")
-    pairs, T, dev, rows, preference, out = _preference_args(logits, tokens, offsets, ref_logprob, beta, smoothing)
-    w = _vector(weight, pairs, torch.float32, dev, "weight")
+    rows, preference, w, out = _preference_args(logits, tokens, offsets, weight, ref_logprob, beta, smoothing)
     dlogits, ldd = _gradient(dlogits, logits)
-    work = torch.empty((T, 4), dtype=torch.float32, device=dev)
-    _call("logits_preference_grad", *rows, temperature, ctypes.byref(preference), w, *(v.data_ptr() for v in out),
-          dlogits.data_ptr(), ldd, work.data_ptr(), _stream(stream, dev))
-    return PreferenceLossGrad(*out, dlogits)
+    loss, reward, lp = out
+    work = torch.empty((4 * rows[3],), dtype=torch.float32, device=logits.device)
+    _call("logits_preference_grad", *rows, temperature, ctypes.byref(preference), w, loss.data_ptr(),
+          reward.data_ptr(), lp.data_ptr(), dlogits.data_ptr(), ldd, work.data_ptr(), _stream(stream, logits.device))
+    return PreferenceLossGrad(loss, reward, lp, dlogits)
