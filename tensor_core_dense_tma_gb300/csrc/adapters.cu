@@ -195,12 +195,15 @@ gemm_status_t launch_tiles(gemm_plan* plan, void (*kernel)(Args), const Args& a,
     cfg.blockDim = dim3(tcdt::kAdapterThreads, 1, 1);
     cfg.dynamicSmemBytes = most;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // (they start while the kernel before them ends, and wait for it themselves)
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.splits > 1 ? 1 : 0;
+    cfg.numAttrs = a.splits > 1 ? 2 : 1;
     return launched(plan, cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
@@ -238,8 +241,9 @@ gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* 
     h.idesc = make_idesc(true, input_format(plan->in_dtype), false, !row, 128, h.per_stage * h.pitch);
     h.idesc_one = make_idesc(true, input_format(plan->in_dtype), false, !row, 128, h.rr);
     h.M = static_cast<int32_t>(M);
-    h.k_blocks = static_cast<int32_t>((K + 63) / 64);
-    h.splits = splits_of(plan, (M + 127) / 128, h.k_blocks, 4);
+    const int64_t step = 64 * tcdt::hidden_blocks(h.rr);
+    h.k_steps = static_cast<int32_t>((K + step - 1) / step);
+    h.splits = splits_of(plan, (M + 127) / 128, h.k_steps, 2);
     const int64_t ctas = (M + 127) / 128 * h.splits;
     h.stages = tcdt::kAdapterSharedBytes / tcdt::hidden_stage_bytes(h.rr);
     h.hidden = static_cast<uint16_t*>(hidden);
@@ -351,7 +355,9 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     f.part = part;
     f.idesc = make_idesc(true, input_format(plan->in_dtype), true, true, 128, 2 * part);
     f.M = M;
-    f.splits = splits_of(plan, items, (M + 63) / 64, 4);
+    // (an adapter has about its share of the tiles: 1000 rows of three adapters, 75 items, 9 us
+    // with one CTA each, 13 with four, 19 with eight; 4096 of one, 64 items: 27, 17, 27)
+    f.splits = splits_of(plan, items, (M + 63) / 64 / a.count, 8);
     f.stages = tcdt::kAdapterSharedBytes / tcdt::factor_stage_bytes(part);
     if (f.stages > tcdt::kAdapterMaxStages) f.stages = tcdt::kAdapterMaxStages;
     f.out_kind = out_dtype == GEMM_F32 ? 0u : out_dtype == GEMM_F16 ? 1u : 2u;

@@ -103,7 +103,7 @@ struct HiddenArgs {
     int32_t pitch;            // columns from one to the next (rr, or 64 or 128)
     uint32_t a_mn;            // 1: down factors are rank-contiguous
     uint32_t idesc, idesc_one;    // N = per_stage * pitch, and for one adapter rr
-    int32_t M, k_blocks, splits, stages;
+    int32_t M, k_steps, splits, stages;
     uint16_t* hidden;
     int64_t ldh;
     uint32_t bf16;
@@ -111,8 +111,16 @@ struct HiddenArgs {
     uint64_t timeout_ns;
 };
 
-// A stage: a block of X, and the adapters' (8 KB: 4 of rank 16, 1 of rank 64).
-__host__ __device__ constexpr int hidden_stage_bytes(int rr) { return 128 * 128 + (rr <= 64 ? 8192 : 16384); }
+// A stage: two blocks of X and the adapters' of both (8 KB each: 4 of rank 16, 1 of
+// rank 64), or, beyond rank 64, one.  (Its two waits and the election cost the
+// producer as much as its copies: with one block a stage the loop took 680 cycles a
+// block, whatever was in flight.)
+__host__ __device__ constexpr int hidden_blocks(int rr) { return rr <= 64 ? 2 : 1; }
+constexpr int kHiddenBlock = 128 * 128;      // of X, 64 columns
+__host__ __device__ constexpr int hidden_adapter_bytes(int rr) { return rr <= 64 ? 8192 : 16384; }
+__host__ __device__ constexpr int hidden_stage_bytes(int rr) {
+    return hidden_blocks(rr) * (kHiddenBlock + hidden_adapter_bytes(rr));
+}
 
 // A cluster of a.splits CTAs computes 128 rows.  The adapters of a stage have
 // columns of their own in tensor memory, up to 128 together, and a row takes those of
@@ -136,19 +144,32 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
     constexpr uint32_t kCols = 128;
     const bool bf16 = a.bf16 != 0;
 
-    const int kb0 = a.k_blocks * rank / a.splits, kb1 = a.k_blocks * (rank + 1) / a.splits;
+    // (steps of one or two blocks; beyond K both operands read as zeros)
+    const int blocks = hidden_blocks(a.rr);
+    const int kb0 = a.k_steps * rank / a.splits, kb1 = a.k_steps * (rank + 1) / a.splits;
     auto stage_at = [&](int s) { return base + static_cast<uint32_t>(s * hidden_stage_bytes(a.rr)); };
 
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&a.tmX);
+        tma_prefetch_desc(&a.tmA);
+        adapter_pipe_init(q, a.stages, 1);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(smem_addr(&q.tmem), kCols);
+        tmem_relinquish_alloc_permit<1>();
+    }
+    // what is before this kernel in the stream has ended; the product may start
+    griddep_wait();
     griddep_launch();
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_desc(&a.tmA);
-            adapter_pipe_init(q, a.stages, 1);
             // the first blocks of X, before the adapters are known (0.6 us); a tile
             // without adapters waits for them at its end
             for (int i = 0; i < a.stages && i < kb1 - kb0; ++i) {
-                mbar_expect_tx(smem_addr(&q.full[i]), 128 * 128);
-                tma_load_2d(stage_at(i), &a.tmX, smem_addr(&q.full[i]), 64 * (kb0 + i), row0);
+                mbar_expect_tx(smem_addr(&q.full[i]), blocks * kHiddenBlock);
+                for (int b = 0; b < blocks; ++b)
+                    tma_load_2d(stage_at(i) + b * kHiddenBlock, &a.tmX, smem_addr(&q.full[i]),
+                                64 * ((kb0 + i) * blocks + b), row0);
             }
         }
         __syncwarp();
@@ -178,17 +199,13 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
         factor[threadIdx.x - 64] = g < 0 || g >= a.count ? 0.0f : a.scale ? __ldg(a.scale + g) : 1.0f;
         given[threadIdx.x - 64] = g >= 0 && g < a.count;
     }
-    if (warp == 1) {
-        tmem_alloc<1>(smem_addr(&q.tmem), kCols);
-        tmem_relinquish_alloc_permit<1>();
-    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = q.tmem;
     const int n = warp_uniform<8>(listed);
-    const int early = min(a.stages, kb1 - kb0);        // blocks of X that are under way
-    const int groups = (n + a.per_stage - 1) / a.per_stage;
+    const int early = min(a.stages, kb1 - kb0);        // steps whose X is under way
+    const int groups = n <= a.per_stage ? (n > 0 ? 1 : 0) : (n + a.per_stage - 1) / a.per_stage;
     const uint32_t a_bytes = a.a_mn ? (a.rr <= 64 ? kChunk : 2 * kChunk) : static_cast<uint32_t>(a.rr) * 128u;
     const WaitCtx wctx{a.status, a.timeout_ns, &q.abort_flag};
     bool ok = true;
@@ -235,19 +252,24 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
                 ok = false;
                 break;
             }
-            const uint32_t bar = smem_addr(&q.full[at.stage]), sx = stage_at(at.stage), sa = sx + 128 * 128;
-            const int first = s.j * a.per_stage, here = min(a.per_stage, n - first);
+            const uint32_t bar = smem_addr(&q.full[at.stage]), sx = stage_at(at.stage), sa = sx + blocks * kHiddenBlock;
+            const int first = s.j * a.per_stage, here = min(a.per_stage, n - first), k0 = 64 * blocks * s.kb;
             if (elect_one_sync()) {
-                mbar_arrive_expect_tx(bar, (s.i < early ? 0u : 128u * 128u) + here * a_bytes);
-                if (s.i >= early) tma_load_2d(sx, &a.tmX, bar, 64 * s.kb, row0);
+                mbar_arrive_expect_tx(bar, (s.i < early ? 0u : blocks * kHiddenBlock) + blocks * here * a_bytes);
+                if (s.i >= early)
+                    for (int b = 0; b < blocks; ++b)
+                        tma_load_2d(sx + b * kHiddenBlock, &a.tmX, bar, k0 + 64 * b, row0);
                 for (int e = 0; e < here; ++e) {
                     const int g = list[first + e];
                     const uint32_t dst = sa + e * a_bytes;
-                    if (a.a_mn) {
-                        tma_load_3d(dst, &a.tmA, bar, 0, 64 * s.kb, g);
-                        if (a.rr > 64) tma_load_3d(dst + kChunk, &a.tmA, bar, 64, 64 * s.kb, g);
-                    } else {
-                        tma_load_3d(dst, &a.tmA, bar, 64 * s.kb, 0, g);
+                    for (int b = 0; b < blocks; ++b) {
+                        const uint32_t to = dst + b * hidden_adapter_bytes(a.rr);
+                        if (a.a_mn) {
+                            tma_load_3d(to, &a.tmA, bar, 0, k0 + 64 * b, g);
+                            if (a.rr > 64) tma_load_3d(to + kChunk, &a.tmA, bar, 64, k0 + 64 * b, g);
+                        } else {
+                            tma_load_3d(to, &a.tmA, bar, k0 + 64 * b, 0, g);
+                        }
                     }
                 }
             }
@@ -271,17 +293,20 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
                 break;
             }
             tc_fence_after_sync();
-            const uint32_t sx = stage_at(at.stage), sa = sx + 128 * 128;
+            const uint32_t sx = stage_at(at.stage), sa = sx + blocks * kHiddenBlock;
             if (elect_one_sync()) {
                 const uint32_t m[4] = {off[s.j][0], off[s.j][1], off[s.j][2], off[s.j][3]};
                 const uint32_t idesc = n == 1 ? a.idesc_one : a.idesc;
+                for (int b = 0; b < blocks; ++b) {
+                    const uint32_t xb = sx + b * kHiddenBlock, ab = sa + b * hidden_adapter_bytes(a.rr);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t xdesc = smem_desc_sw128(sx + k * 32u, 16u, 1024u);
-                    const uint64_t adesc = smem_desc_sw128(sa + k * kstep, lbo, 1024u);
-                    const uint32_t more = s.kb != kb0 || k != 0 ? 1u : 0u;
-                    if (groups == 1) umma_f16_ss<1>(tmem, xdesc, adesc, idesc, more);
-                    else umma_f16_ss_rows<1>(tmem, xdesc, adesc, idesc, m, more);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t xdesc = smem_desc_sw128(xb + k * 32u, 16u, 1024u);
+                        const uint64_t adesc = smem_desc_sw128(ab + k * kstep, lbo, 1024u);
+                        const uint32_t more = s.kb != kb0 || b != 0 || k != 0 ? 1u : 0u;
+                        if (groups == 1) umma_f16_ss<1>(tmem, xdesc, adesc, idesc, more);
+                        else umma_f16_ss_rows<1>(tmem, xdesc, adesc, idesc, m, more);
+                    }
                 }
                 umma_commit<1>(smem_addr(&q.empty[at.stage]));
             }
@@ -384,7 +409,7 @@ struct FactorGradArgs {
 };
 
 constexpr int kFactorWindow = 1024;       // tiles of 64 rows looked through at once
-constexpr int kFactorPitch = 129;         // of the sums in shared memory: both orders of reading free of conflicts
+constexpr int kFactorPitch = 132;         // of the sums in shared memory
 
 __host__ __device__ constexpr int factor_stage_bytes(int part) { return 2 * 8192 + (part <= 32 ? 1 : part / 32) * 8192; }
 
@@ -423,6 +448,7 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
         tmem_alloc<1>(smem_addr(&q.tmem), tmem_cols);
         tmem_relinquish_alloc_permit<1>();
     }
+    griddep_wait();       // what is before this kernel in the stream has ended
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -436,22 +462,30 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
 
     for (int64_t w0 = 0; w0 * 64 < a.M; w0 += kFactorWindow) {
         const int tiles = static_cast<int>(min(static_cast<int64_t>(kFactorWindow), (a.M + 63) / 64 - w0));
-        // eight tiles a warp at a time, so that their loads overlap
-        for (int t0 = warp * 8; t0 < tiles; t0 += 6 * 8) {
-            int x[8][2];
+        // a tile a thread, its 64 entries in loads that are all under way together
+        for (int t = threadIdx.x; t < tiles; t += kAdapterThreads) {
+            const int64_t row = (w0 + t) * 64;
+            const int32_t* from = a.index + row;
+            bool any = false, all = true;
+            if (row + 64 <= a.M && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+                int4 x[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 16; ++i) x[i] = __ldg(reinterpret_cast<const int4*>(from) + i);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t row = (w0 + t0 + i) * 64 + 32 * h + lane;
-                    x[i][h] = t0 + i < tiles && row < a.M ? __ldg(a.index + row) : g;
+                for (int i = 0; i < 16; ++i) {
+                    any |= x[i].x == g || x[i].y == g || x[i].z == g || x[i].w == g;
+                    all &= x[i].x == g && x[i].y == g && x[i].z == g && x[i].w == g;
                 }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool all = __all_sync(0xffffffffu, x[i][0] == g && x[i][1] == g);
-                const bool any = __any_sync(0xffffffffu, x[i][0] == g || x[i][1] == g);
-                if (lane == 0 && t0 + i < tiles) holds[t0 + i] = all ? 2 : any ? 1 : 0;
+            } else {
+                const int n = static_cast<int>(min(a.M - row, static_cast<int64_t>(64)));
+#pragma unroll 32
+                for (int i = 0; i < 64; ++i) {
+                    const bool here = i < n && __ldg(from + i) == g;
+                    any |= here;
+                    all &= here || i >= n;
+                }
             }
+            holds[t] = any ? all ? 2 : 1 : 0;
         }
         __syncthreads();
         if (warp == 0) {
@@ -577,18 +611,58 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
     }
     if (a.splits > 1) cluster_sync_all();
     else __syncthreads();
-    // joined and stored, an equal share by each CTA, in the order of the output's memory
-    const bool by_rank = f.sr == 1;            // consecutive in memory: rank, else columns
-    const int total = a.rank * 128, share = (total + a.splits - 1) / a.splits;
-#pragma unroll 4
+    // joined and stored, an equal share by each CTA: eight elements that are neighbours in
+    // memory a thread (of a row of d_down, of a column's values in d_up), in 16-byte stores
+    // where they can be
+    const bool by_rank = f.sr == 1 && f.sc != 1;
+    const int total = by_rank ? (a.rank + 7) / 8 * 128 : a.rank * 16, share = (total + a.splits - 1) / a.splits;
+    const int esz = a.out_kind == 0 ? 4 : 2;
+    const bool units = ((reinterpret_cast<uintptr_t>(f.out) | static_cast<uintptr_t>(f.stride * esz) |
+                         static_cast<uintptr_t>((by_rank ? f.sc : f.sr) * esz)) & 15) == 0;
     for (int i = rank * share + threadIdx.x; i < min(total, (rank + 1) * share); i += kAdapterThreads) {
-        const int r = by_rank ? i % a.rank : i / 128, c = by_rank ? i / a.rank : i % 128;
+        const int r = by_rank ? i / 128 * 8 : i / 16, c = by_rank ? i % 128 : i % 16 * 8;
+        const int n = by_rank ? min(8, a.rank - r) : min(8, f.columns - col0 - c);
         if (col0 + c >= f.columns) continue;
         const uint32_t from = smem_addr(sums + r * kFactorPitch + c);
-        const float v = a.splits > 1 ? cluster_sum(from, a.splits) : ld_shared_f32(from);
-        const int64_t o = g * f.stride + r * f.sr + (col0 + c) * f.sc;
-        if (a.out_kind == 0) static_cast<float*>(f.out)[o] = v;
-        else static_cast<uint16_t*>(f.out)[o] = adapter_bits(v, a.out_kind == 2);
+        float v[8];
+        if (by_rank) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t at_e = from + (e < n ? e : 0) * (kFactorPitch * 4u);
+                v[e] = a.splits > 1 ? cluster_sum(at_e, a.splits) : ld_shared_f32(at_e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const float4 x = a.splits > 1 ? cluster_sum4(from + 4u * e, a.splits) : ld_shared_v4f(from + 4u * e);
+                v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
+            }
+        }
+        const int64_t o = g * f.stride + r * f.sr + (col0 + c) * f.sc, step = by_rank ? f.sr : f.sc;
+        if (a.out_kind == 0) {
+            float* out = static_cast<float*>(f.out) + o;
+            if (units && n == 8) {
+                reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) out[e * step] = v[e];
+            }
+        } else {
+            uint16_t* out = static_cast<uint16_t*>(f.out) + o;
+            uint16_t x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = adapter_bits(v[e], a.out_kind == 2);
+            if (units && n == 8) {
+                *reinterpret_cast<uint4*>(out) = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16,
+                                                            x[6] | x[7] << 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) out[e * step] = x[e];
+            }
+        }
     }
     __syncwarp();
     if (a.splits > 1) cluster_sync_all();

@@ -368,6 +368,35 @@ def test_streams_and_graphs(tc):
         p.close(), q.close()
 
 
+def test_graph_after_other_work(plans):
+    """A call captured behind a memset, a copy and kernels that make its inputs."""
+    plan = plans["bf16"]
+    for M in (9, 300):
+        c = Case(M, 264, 520, 16, 3, "bf16", seed=11, index="mixed")
+        src = c.X.clone()
+        X, index = torch.empty((M, 520), dtype=torch.bfloat16, device="cuda"), c.index.clone()
+        args = (c.B, c.down, c.up, index, c.scale)
+        want = plan.linear_adapters(2 * src, *args)
+        g, D = torch.cuda.CUDAGraph(), torch.empty((M, 264), dtype=torch.bfloat16, device="cuda")
+        side = torch.zeros(1 << 20, device="cuda")
+        with torch.cuda.graph(g):
+            X.copy_(src)
+            side.zero_()
+            plan.linear_adapters(X, *args, D)
+            X.copy_(src)
+            X.mul_(2)
+            D2, h2 = plan.linear_adapters(X, *args)
+            X.zero_()
+            side.zero_()
+            D3, _ = plan.linear_adapters(X, *args)
+        for _ in range(3):
+            X.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(D2, want[0]) and torch.equal(h2, want[1]) and not D3.any()
+            assert torch.equal(D, plan.linear_adapters(src.contiguous(), *args)[0])
+
+
 def test_pinned_and_tuned_configurations(tc):
     """A plan that is pinned to a configuration or division, or tuned, computes the same."""
     c = Case(700, 1030, 1000, 24, 5, "bf16", seed=12, index="mixed", whole=True, bias=True)
