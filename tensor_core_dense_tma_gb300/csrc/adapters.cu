@@ -251,6 +251,9 @@ gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* 
     h.bf16 = bf16;
     h.status = plan->d_status;
     h.timeout_ns = plan->timeout_ns;
+#ifdef TCDT_FAULT_INJECTION
+    h.fi_skip_load = plan->fi_skip_load;
+#endif
     gemm_status_t st = encode_map(plan, &h.tmX, X, K, M, ldx, 64, 128, plan->in_dtype);
     if (st == GEMM_OK)
         st = row ? encode_stack(plan, &h.tmA, a.down, K, a.rank, a.count, a.down_ld, a.down_stride, h.rr)
@@ -363,6 +366,9 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     f.out_kind = out_dtype == GEMM_F32 ? 0u : out_dtype == GEMM_F16 ? 1u : 2u;
     f.status = plan->d_status;
     f.timeout_ns = plan->timeout_ns;
+#ifdef TCDT_FAULT_INJECTION
+    f.fi_skip_load = plan->fi_skip_load;
+#endif
     return launch_tiles(plan, tcdt::factor_grad_kernel, f, items * f.splits, plan->adapters_prepared[1],
                         static_cast<cudaStream_t>(stream));
 }

@@ -109,6 +109,9 @@ struct HiddenArgs {
     uint32_t bf16;
     int* status;
     uint64_t timeout_ns;
+#ifdef TCDT_FAULT_INJECTION
+    int64_t fi_skip_load;     // test builds only: this step's copies (counted per CTA) do not start
+#endif
 };
 
 // A stage: two blocks of X and the adapters' of both (8 KB each: 4 of rank 16, 1 of
@@ -259,6 +262,9 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
                 if (s.i >= early)
                     for (int b = 0; b < blocks; ++b)
                         tma_load_2d(sx + b * kHiddenBlock, &a.tmX, bar, k0 + 64 * b, row0);
+#ifdef TCDT_FAULT_INJECTION
+                if (issued != a.fi_skip_load)
+#endif
                 for (int e = 0; e < here; ++e) {
                     const int g = list[first + e];
                     const uint32_t dst = sa + e * a_bytes;
@@ -406,6 +412,9 @@ struct FactorGradArgs {
     uint32_t out_kind;        // 0 fp32, 1 fp16, 2 bf16
     int* status;
     uint64_t timeout_ns;
+#ifdef TCDT_FAULT_INJECTION
+    int64_t fi_skip_load;     // test builds only: as in HiddenArgs
+#endif
 };
 
 constexpr int kFactorWindow = 1024;       // tiles of 64 rows looked through at once
@@ -440,8 +449,10 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
     const uint32_t stage_bytes = static_cast<uint32_t>(factor_stage_bytes(a.part));
     const uint32_t tmem_cols = 2u * static_cast<uint32_t>(a.part);
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&f.tmX);
-        tma_prefetch_desc(&f.tmH);
+        if (a.M > 0) {        // (without rows there are no maps)
+            tma_prefetch_desc(&f.tmX);
+            tma_prefetch_desc(&f.tmH);
+        }
         adapter_pipe_init(q, a.stages, 5);
     }
     if (warp == 1) {
@@ -511,6 +522,9 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
                 const int row = static_cast<int>((w0 + (list[i] & 0x7FFF)) * 64);
                 if (elect_one_sync()) {
                     mbar_arrive_expect_tx(bar, stage_bytes);
+#ifdef TCDT_FAULT_INJECTION
+                    if (used != a.fi_skip_load)
+#endif
                     tma_load_2d(sx, &f.tmX, bar, col0, row);
                     tma_load_2d(sx + kChunk, &f.tmX, bar, col0 + 64, row);
                     for (int c = 0; c < chunks; ++c) tma_load_2d(sh + c * kChunk, &f.tmH, bar, 64 * c, row);

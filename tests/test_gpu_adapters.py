@@ -413,11 +413,58 @@ def test_pinned_and_tuned_configurations(tc):
         plan.force_division("auto")
         plan.autotune(c.X, c.B, out_dtype="bf16")
         check_forward(plan, c, whole=True)
-        for config in ("single_128x64", ):
-            plan.force_config(config)
+        plan.clear_tuning()
+        one = Case(11, 1030, 1000, 24, 5, "bf16", seed=12, index="mixed", whole=True)
+        for config, x in (("single_128x64", few), ("single_128x64", one), ("single_128x16", one)):
+            for splits in (0, 1, 2, 3):
+                plan.force_config(config, splits)
+                check_forward(plan, x, whole=True)
+        plan.force_config("auto")
+        for division in ("whole", "split", "pair_split", "halves"):
+            plan.force_division(division)
+            if division != "halves":
+                check_forward(plan, one, whole=True)
             check_forward(plan, few, whole=True)
         torch.cuda.synchronize()
         assert plan.device_status() == 0
+
+
+@pytest.mark.parametrize("division", ["early_split", "stream_k"])
+def test_captured_early_partials(tc, division):
+    """Divisions whose units leave partial sums for one another, captured: each replay uses its own."""
+    c = Case(5200, 3840 if division == "early_split" else 5120, 520, 16, 5, "bf16", seed=13, index="runs", whole=True)
+    with tc.Plan("bf16", 0) as plan:
+        plan.force_division(division)
+        want = check_forward(plan, c, whole=True)[0].clone()
+        g, X, D = torch.cuda.CUDAGraph(), c.X.clone(), torch.empty_like(want)
+        # (the stride of the clone's rows is the columns': whole 16-byte units here)
+        with torch.cuda.graph(g):
+            plan.linear_adapters(X, *c.args(), D)
+        other = torch.randint(-2, 3, X.shape, device="cuda").to(X.dtype)
+        for _ in range(3):
+            X.copy_(other)
+            g.replay()
+            X.copy_(c.X)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(D, want)
+        assert plan.device_status() == 0
+
+
+def test_long_index(plans):
+    """More rows than one look at the index takes (65536)."""
+    c = Case(70001, 8, 24, 4, 3, "f16", seed=14, index="runs", whole=True, runs=9)
+    check_backward(plans["f16"], c, whole=True, out="f32")
+
+
+def test_unaligned_index(plans):
+    """An index that starts anywhere on 4 bytes."""
+    c = Case(700, 136, 264, 16, 3, "bf16", seed=15, index="runs", whole=True)
+    for shift in (1, 2, 3):
+        buf = torch.full((704 + shift,), 2, dtype=torch.int32, device="cuda")
+        buf[shift:shift + 700] = c.index
+        c.index = buf[shift:shift + 700]
+        check_backward(plans["bf16"], c, whole=True, out="f32")
 
 
 def test_empty(plans):
