@@ -107,6 +107,8 @@ def _stack(t, what: str, di: int, dtype, G, r, c):
 
 
 def _adapters(down, up, index, scale, M, N, K, di, dtype):
+    """G, R, the fields of gemm_adapters_t that describe down and up, and the
+    addresses of scale and index."""
     if down.dim() != 3 or up.dim() != 3:
         raise ValueError("down must be G x R x K, up G x N x R")
     G, R, _ = down.shape
@@ -117,8 +119,8 @@ def _adapters(down, up, index, scale, M, N, K, di, dtype):
     if scale is not None and (scale.dtype is not _calls["f32"] or scale.shape != (G,) or scale.get_device() != di
                               or not scale.is_contiguous()):
         raise ValueError("scale must be a contiguous fp32 vector with one entry per adapter on X's device")
-    return Adapters(G, R, *_stack(down, "down", di, dtype, G, R, K), *_stack(up, "up", di, dtype, G, N, R),
-                    None if scale is None else scale.data_ptr(), index.data_ptr())
+    return (G, R, _stack(down, "down", di, dtype, G, R, K), _stack(up, "up", di, dtype, G, N, R),
+            None if scale is None else scale.data_ptr(), index.data_ptr())
 
 
 def _hidden(hidden, what, M, R, dev, di, dtype):
@@ -130,6 +132,31 @@ def _hidden(hidden, what, M, R, dev, di, dtype):
     return hidden, _row_ld(hidden, what, di, dtype)
 
 
+def _weights(B, di: int, dtype, K, N):
+    """(leading dimension, layout) of the K x N matrix B."""
+    if B.dtype is not dtype or B.get_device() != di:
+        raise ValueError(f"B must be a 2-D {dtype} tensor on X's device")
+    order = _order(K, N, *B.stride())
+    if order is None:
+        raise ValueError(f"B must be row- or column-major (strides {B.stride()})")
+    return order
+
+
+def _result(D, what: str, M, N, di: int, dev, wanted, own):
+    """(D, its type, its row stride); allocated if not given, of the type that is wanted or the plan's own."""
+    if D is None:
+        out = wanted or own
+        return _calls["empty"]((M, N), dtype=out, device=dev), out, N
+    out = D.dtype
+    if wanted is not None and out is not wanted:
+        raise ValueError(f"{what} must have the output type")
+    d0, d1 = D.stride() if D.dim() == 2 else (0, 0)
+    if out not in _calls["codes"] or D.shape != (M, N) or D.get_device() != di or (d1 != 1 and N > 1) or \
+            (d0 < N and M > 1):
+        raise ValueError(f"{what} must be a row-major matrix of the result's size on X's device")
+    return D, out, (d0 if M > 1 else N)
+
+
 def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, stream):
     """Plan.linear_adapters."""
     calls = _calls or _lib()
@@ -139,31 +166,16 @@ def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, strea
         raise ValueError("adapters take 2-D device tensors and an f16 or bf16 plan")
     (M, K), (KB, N) = X.shape, B.shape
     ldx = _row_ld(X, "X", di, dtype)
-    if B.dtype is not dtype or B.get_device() != di:
-        raise ValueError(f"B must be a 2-D {dtype} tensor on X's device")
     if KB != K:
         raise ValueError("inner dimensions differ")
-    order = _order(K, N, *B.stride())
-    if order is None:
-        raise ValueError(f"B must be row- or column-major (strides {B.stride()})")
-    a = _adapters(down, up, index, scale, M, N, K, di, dtype)
-    if D is None:
-        out = types[out_dtype or plan.in_dtype]
-        D = calls["empty"]((M, N), dtype=out, device=dev)
-        ldd = N
-    else:
-        out = D.dtype
-        if out_dtype is not None and out is not types[out_dtype]:
-            raise ValueError("D must have the output type")
-        d0, d1 = D.stride() if D.dim() == 2 else (0, 0)
-        if out not in calls["codes"] or D.shape != (M, N) or D.get_device() != di or (d1 != 1 and N > 1) or \
-                (d0 < N and M > 1):
-            raise ValueError("D must be a row-major M x N matrix on X's device")
-        ldd = d0 if M > 1 else N
+    order = _weights(B, di, dtype, K, N)
+    G, R, lower, upper, scales, at = _adapters(down, up, index, scale, M, N, K, di, dtype)
+    D, out, ldd = _result(D, "D", M, N, di, dev, None if out_dtype is None else types[out_dtype], dtype)
     if bias is not None and (bias.dtype is not calls["f32"] or bias.shape != (N,) or bias.get_device() != di
                              or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous fp32 vector of length N on X's device")
-    hidden, ldh = _hidden(hidden, "hidden", M, a.rank, dev, di, dtype)
+    hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
+    a = Adapters(G, R, *lower, *upper, scales, at)
     st = calls["run"](plan.handle, X.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, ldx, order[0], ldd, order[1],
                       calls["codes"][out], None if bias is None else bias.data_ptr(), ctypes.byref(a),
                       hidden.data_ptr(), ldh, calls["stream"](di) if stream is None else stream)
@@ -189,13 +201,16 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
     """Plan.linear_adapters_grad."""
     calls = _calls or _lib()
     dtype, dev, di = calls["types"].get(plan.in_dtype), X.device, X.get_device()
-    if X.dim() != 2 or dY.dim() != 2 or B.dim() != 2 or down.dim() != 3 or up.dim() != 3:
-        raise ValueError("X, dY and B must be 2-D, down and up 3-D tensors")
-    (M, K), (MY, N), (G, R, _) = X.shape, dY.shape, down.shape
+    if dtype is None or dtype is calls["f32"] or di < 0 or X.dim() != 2 or dY.dim() != 2 or B.dim() != 2:
+        raise ValueError("adapters take 2-D device tensors and an f16 or bf16 plan")
+    (M, K), (MY, N) = X.shape, dY.shape
     if MY != M or B.shape != (K, N):
         raise ValueError("dY must be M x N, B K x N")
     ldx = _row_ld(X, "X", di, dtype)
     lddy = _row_ld(dY, "dY", di, dtype)
+    ldb, layout = _weights(B, di, dtype, K, N)
+    G, R, lower, upper, scales, at = _adapters(down, up, index, scale, M, N, K, di, dtype)
+    dX, x_type, lddx = _result(dX, "dX", M, K, di, dev, None, dtype)
     hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
     like = d_down if d_down is not None else d_up
     out = dtype if like is None else like.dtype
@@ -203,15 +218,19 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
         raise ValueError("d_down and d_up must both be fp32 or both of the plan's type")
     d_down, down_ld, down_stride = _gradient(d_down, out, dev, di, (G, R, K), "d_down")
     d_up, up_ld, up_stride = _gradient(d_up, out, dev, di, (G, N, R), "d_up")
-    # dX is the same product the other way round, and leaves p as its hidden rows
     p = calls["torch"].empty_strided((M, hidden_width(R)), (ldh, 1), dtype=dtype, device=dev)
     if stream is None:
         stream = calls["stream"](di)
-    dX, _ = linear(plan, dY, B.t(), up.transpose(1, 2), down.transpose(1, 2), index, scale, dX, None, p, None, stream)
-    a = Adapters(G, R, None, 0, 0, 0, None, 0, 0, 0, None, index.data_ptr())
-    st = calls["grad"](plan.handle, X.data_ptr(), dY.data_ptr(), M, N, K, ldx, lddy, ctypes.byref(a),
-                       hidden.data_ptr(), p.data_ptr(), ldh, calls["codes"][out], d_down.data_ptr(), down_ld,
-                       down_stride, d_up.data_ptr(), up_ld, up_stride, stream)
+    # dX is the same product the other way round (a matrix's transpose is the same memory in
+    # the other order), and leaves p as its hidden rows
+    a = Adapters(G, R, *upper[:3], 1 - upper[3], *lower[:3], 1 - lower[3], scales, at)
+    this, other, kept, mine = X.data_ptr(), dY.data_ptr(), hidden.data_ptr(), p.data_ptr()
+    st = calls["run"](plan.handle, other, B.data_ptr(), dX.data_ptr(), M, K, N, lddy, ldb, lddx, 1 - layout,
+                      calls["codes"][x_type], None, ctypes.byref(a), mine, ldh, stream)
+    if st == 0:
+        st = calls["grad"](plan.handle, this, other, M, N, K, ldx, lddy, ctypes.byref(a), kept, mine, ldh,
+                           calls["codes"][out], d_down.data_ptr(), down_ld, down_stride, d_up.data_ptr(), up_ld,
+                           up_stride, stream)
     if st != 0:
-        raise calls["error"](st, "gemm_adapters_grad")
+        raise calls["error"](st, "gemm_run_adapters or gemm_adapters_grad")
     return AdaptersGrad(dX, d_down, d_up)
