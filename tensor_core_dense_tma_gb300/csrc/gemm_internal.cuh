@@ -294,16 +294,18 @@ inline gemm_status_t encode_map(gemm_plan* plan, CUtensorMap* map, const void* p
 // 3-D tensor map over a stack of matrices of 16-bit elements, `outer` rows of `inner`
 // contiguous elements each, 128-byte swizzle, zero fill outside.
 inline gemm_status_t encode_stack(gemm_plan* plan, CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer,
-                                  uint64_t count, uint64_t ld, uint64_t stride, uint32_t box_outer) {
+                                  uint64_t count, uint64_t ld, uint64_t stride, uint32_t box_outer,
+                                  uint32_t box_inner = 64) {
     // (a stack of one has no stride of its own, but the map wants one)
     const cuuint64_t dims[3] = {inner, outer, count};
     const cuuint64_t strides[2] = {ld * 2, (count > 1 ? stride : ld) * 2};
-    const cuuint32_t box[3] = {64, box_outer, 1};
+    const cuuint32_t box[3] = {box_inner, box_outer, 1};     // 64: 128-byte swizzle, 16: 32-byte swizzle
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUtensorMapDataType dt =
         plan->in_dtype == GEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUresult r = plan->encode(map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                    box_inner == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
@@ -541,7 +543,9 @@ gemm_status_t fill_adapters(gemm_plan* plan, tcdt::AdapterArgs& ad, const Proble
         encode_map(plan, &ad.tmH, a.hidden, 2 * a.part, rows, a.ldh, 64, tokens ? Cfg::BN : Cfg::BM, plan->in_dtype);
     if (st != GEMM_OK) return st;
     if (mn) return encode_stack(plan, &ad.tmU, a.up, channels, a.rank, a.count, a.up_ld, a.up_stride, 64);
-    st = encode_stack(plan, &ad.tmU, a.up, a.rank, channels, a.count, a.up_ld, a.up_stride, tokens ? 128 : Cfg::BN_CTA);
+    ad.packed = tokens && a.part == 16 ? 1u : 0u;
+    st = encode_stack(plan, &ad.tmU, a.up, a.rank, channels, a.count, a.up_ld, a.up_stride, tokens ? 128 : Cfg::BN_CTA,
+                      ad.packed ? 16 : 64);
     if (st == GEMM_OK && !tokens && Cfg::HALVES_OK)
         st = encode_stack(plan, &ad.tmUh, a.up, a.rank, channels, a.count, a.up_ld, a.up_stride, Cfg::BN_CTA_HALF);
     return st;

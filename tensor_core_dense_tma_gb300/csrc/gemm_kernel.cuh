@@ -135,6 +135,8 @@ struct AdapterArgs {
     int32_t count, rank;
     int32_t part;             // columns of h's high parts (and of its low ones)
     uint32_t u_mn;            // 1: U is N-contiguous
+    uint32_t packed;          // 1: (transposed tiles, rank up to 16, U rank-contiguous) four adapters a step,
+                              //    U in boxes of 16 columns x 128 channels
     uint32_t idesc, idesc_half;
 };
 
@@ -1332,6 +1334,40 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         const int steps = adapter_steps(ad), blocks = ad.part <= 64 ? 1 : 2;
                         uint32_t off[kRows / 32];
                         int g;
+                        if constexpr (kAdapterTokens) {
+                            // up to four adapters a step (one after another took 400 cycles each, 16 x
+                            // 8192 x 8192 with 16 of rank 16 3 us)
+                            bool more = ad.packed != 0;
+                            while (ok && more) {
+                                int four[4], n = 0;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    four[i] = 0;
+                                    if (more) more = walk.next(four[i], off);
+                                    n += more;
+                                }
+                                if (n == 0) break;
+                                if (!warp_wait_phase(empty_bar(stage), phase ^ 1u, wctx, kSiteProducerEmpty)) {
+                                    ok = false;
+                                    break;
+                                }
+                                const uint32_t sa = base + stage * Cfg::STAGE_BYTES;
+                                const uint32_t fb_local = full_bar(stage);
+                                if (elect_one_sync()) {
+                                    mbar_arrive_expect_tx(fb_local, static_cast<uint32_t>(n) * 4096u + Cfg::BN * 128u);
+                                    tma_load_2d(sa + Cfg::A_BYTES, &ad.tmH, fb_local, 0, n0);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        if (i < n) tma_load_3d(sa + 4096u * i, &ad.tmU, fb_local, 0, m0, four[i]);
+                                }
+                                __syncwarp();
+                                ++issued;
+                                if (++stage == Cfg::STAGES) {
+                                    stage = 0;
+                                    phase ^= 1u;
+                                }
+                            }
+                        }
                         while (ok && walk.next(g, off)) {
 #pragma unroll 1
                             for (int st = 0; st < steps; ++st) {
@@ -1501,6 +1537,43 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 #pragma unroll
                         for (int w = 0; w < 4 * CG; ++w) rows_off[w] = 0xFFFFFFFFu;
                         int g;
+                        if constexpr (kAdapterTokens) {
+                            bool more = ad.packed != 0;
+                            while (ok && more) {
+                                uint32_t left = 0;
+#pragma unroll
+                                for (int w = 0; w < kRows / 32; ++w) left |= __ballot_sync(0xffffffffu, walk.idx[w] >= 0);
+                                if (!left) break;
+                                if (!warp_wait_phase(full_bar(stage), phase, wctx, kSiteMmaFull)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after_sync();
+                                const uint32_t su = base + stage * Cfg::STAGE_BYTES;
+                                const uint32_t sh = su + Cfg::A_BYTES;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    if (more) more = walk.next(g, off);
+                                    if (!more) continue;
+#pragma unroll
+                                    for (int w = 0; w < kRows / 32; ++w) rows_off[w] = off[w];
+                                    if (elect_one_sync()) {
+                                        const uint64_t udesc = smem_desc_sw32(su + 4096u * i);
+                                        umma_f16_ss_rows<CG>(to, smem_desc_sw128(sh, 16u, 1024u), udesc, idesc_u, rows_off,
+                                                             0u);
+                                        umma_f16_ss_rows<CG>(to, smem_desc_sw128(sh + 32u, 16u, 1024u), udesc, idesc_u,
+                                                             rows_off, 1u);
+                                    }
+                                    __syncwarp();
+                                }
+                                if (elect_one_sync()) umma_commit<CG>(empty_bar(stage), kPair);
+                                __syncwarp();
+                                if (++stage == Cfg::STAGES) {
+                                    stage = 0;
+                                    phase ^= 1u;
+                                }
+                            }
+                        }
                         while (ok && walk.next(g, off)) {
                             // all rows of a tile one adapter's (rows beyond M do not count; in
                             // transposed tiles nor do those without one): ordinary MMAs

@@ -499,7 +499,7 @@ __device__ __forceinline__ void tmem_ld_wait() {
 //   [32,46) stride-dimension byte offset >> 4
 //   [46,48) descriptor version, 1 on sm_100-family
 //   [49,52) base offset (0: tiles are 1024-byte aligned)
-//   [61,64) swizzle mode, 2 = 128-byte swizzle
+//   [61,64) swizzle mode, 2 = 128-byte swizzle, 6 = 32-byte swizzle
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo_bytes,
                                                     uint32_t sbo_bytes) {
@@ -509,6 +509,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
     d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
     d |= 1ull << 46;
     d |= 2ull << 61;
+    return d;
+}
+
+// The same for rows of 32 bytes with the 32-byte swizzle (mode 6), 8-row groups
+// 256 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= 1ull << 16;
+    d |= static_cast<uint64_t>(256u >> 4) << 32;
+    d |= 1ull << 46;
+    d |= 6ull << 61;
     return d;
 }
 
