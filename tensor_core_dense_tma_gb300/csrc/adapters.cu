@@ -113,7 +113,15 @@ __global__ void __launch_bounds__(kRowThreads) hidden_rows_kernel(const RowArgs 
 // ---- host ------------------------------------------------------------------
 constexpr int64_t kMaxExtent = 0x7FFFF000;
 constexpr int64_t kMaxStride = int64_t(1) << 39;      // elements: below 2^40 bytes, what a tensor map takes
-constexpr int64_t kRowsMost = 64;                     // rows that hidden_rows_kernel takes
+
+// Whether hidden_rows_kernel makes h (down factors K-contiguous): it reads X and A from
+// L2 again for every row, so its time goes with rows x rank x K, while
+// hidden_tile_kernel takes 6 us and more for anything, and more again where a tile's rows
+// have many adapters.  Measured (us), rows / tiles with 4 and with 64 adapters in turn:
+// K = 8192, rank 16: 16 rows 2.9 / 14, 40; 64 rows 3.4 / 14, 146; 256 rows 8.4 / 15, 146
+// (10 where each tile has one); rank 64, 4 adapters: 64 rows 8.6 / 26, 128 rows 14 / 26 (11
+// where each tile has one).  256 x 16 x 8192 and 64 x 64 x 8192 are 2^25.
+bool by_rows(int64_t M, int part, int64_t K) { return M <= 65535 && M * part <= (int64_t(1) << 25) / K; }
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 bool layout_ok(gemm_layout_t l) { return l == GEMM_ROW_MAJOR || l == GEMM_COL_MAJOR; }
 
@@ -220,7 +228,7 @@ gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* 
     const bool row = a.down_layout == GEMM_ROW_MAJOR;
     const int part = part_of(a.rank);
     const uint32_t bf16 = plan->in_dtype == GEMM_BF16 ? 1u : 0u;
-    if (row && M <= kRowsMost) {
+    if (row && by_rows(M, part, K)) {
         const RowArgs r{static_cast<const uint16_t*>(X), ldx, K, static_cast<const uint16_t*>(a.down), a.down_ld,
                         a.down_stride, a.index, a.scale, static_cast<int32_t>(a.count), static_cast<int32_t>(a.rank), part,
                         static_cast<uint16_t*>(hidden), ldh, bf16};

@@ -23,7 +23,7 @@ constexpr uint32_t kChunk = 8192;                     // 64 x 64 16-bit elements
 struct AdapterPipe {
     uint64_t full[kAdapterMaxStages], ready[kAdapterMaxStages], empty[kAdapterMaxStages], acc;
     uint32_t tmem;
-    int abort_flag, drained;
+    int abort_flag;
 };
 
 // empty: arrivals that give a stage back.

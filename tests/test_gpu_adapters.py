@@ -498,7 +498,8 @@ def test_refusals(tc, plans):
         a = dict(ok, **kw)
         with pytest.raises(ValueError):
             plan.linear_adapters(a.pop("X"), a.pop("B"), a.pop("down"), a.pop("up"), a.pop("index"), a.pop("scale"), **a)
-    for kw in (dict(X=z(4, 65)[:, 1:]), dict(B=z(64, 33)[:, :32]), dict(down=z(2, 8, 65)[:, :, :64]), dict(down=z(2, 8, 72)[:, :, 4:68]), dict(up=z(2, 32, 9)[:, :, :8])):
+    for kw in (dict(X=z(4, 65)[:, 1:]), dict(B=z(64, 33)[:, :32]), dict(down=z(2, 8, 65)[:, :, :64]),
+               dict(down=z(2, 8, 72)[:, :, 4:68]), dict(up=z(2, 32, 9)[:, :, :8])):
         a = dict(ok, **kw)
         with pytest.raises(tc.GemmError) as e:
             plan.linear_adapters(*[a[k] for k in ("X", "B", "down", "up", "index", "scale")])
