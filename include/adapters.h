@@ -41,7 +41,8 @@
  * X, W, down, up, dD and hidden start on 16-byte boundaries and so do
  * their rows and an adapter's factors (GEMM_ERR_MISALIGNED); one plan is
  * used by one stream at a time; a wait inside a kernel that ran out is in
- * gemm_plan_device_status.  Nothing is allocated, so calls may be captured.
+ * gemm_plan_device_status.  D, hidden and the gradients overlap no input and not one
+ * another.  Nothing is allocated, so calls may be captured.
  */
 #ifndef TCDT_ADAPTERS_H
 #define TCDT_ADAPTERS_H

@@ -129,9 +129,10 @@ __host__ __device__ constexpr int hidden_stage_bytes(int rr) {
 // columns of their own in tensor memory, up to 128 together, and a row takes those of
 // its adapter.  With more adapters than fit a stage, X comes again from L2 with
 // the next ones, which use the same columns in their own rows: MMAs that leave the
-// other rows as they are (those take some 200 cycles each, whatever their N; done
-// adapter by adapter, 2048 x 4096 with one adapter a tile took 0.45 us a block of
-// K, 16 us in all).
+// other rows as they are.  (An MMA costs some 95 cycles to issue however narrow it is:
+// one for all adapters of a stage, not one each.)  8192 x 8192, rank 64, four
+// adapters: 30 us (134 MB, 20 at the copy rate); 2048 x 4096, rank 32: 9.5, of which 5
+// are start and end; 200 to 256 x 8192 with 64 adapters of rank 16 in turn 146.
 __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __grid_constant__ HiddenArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ AdapterPipe q;
@@ -427,7 +428,8 @@ __host__ __device__ constexpr int factor_stage_bytes(int part) { return 2 * 8192
 // evenly.  Both operands are read as they lie (the sum runs over their rows, so
 // both are MN-major).  In a tile that has other rows too, the epilogue warps
 // zero those of both operands in shared memory first: zeros in h alone would let an
-// infinity in x through.
+// infinity in x through.  Both factors of 4096 x 4096 x 4096, rank 16: 16 us (67 MB, 10 at
+// the copy rate); 8192 x 4096 x 4096, rank 64, four adapters: 31 (134 MB, 20).
 __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __grid_constant__ FactorGradArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ AdapterPipe q;

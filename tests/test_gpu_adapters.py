@@ -467,6 +467,66 @@ def test_unaligned_index(plans):
         check_backward(plans["bf16"], c, whole=True, out="f32")
 
 
+def test_offsets_past_32_bits(plans):
+    """Factors, rows and gradients more than 2^31 elements apart."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    far = (1 << 31) + 64
+    bufs = [torch.empty((2 * far + 4096,), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+
+    def spread(t, buf, stride):
+        v = torch.as_strided(buf, t.shape, stride, 8)
+        v.copy_(t)
+        return v
+
+    c = Case(200, 136, 264, 16, 2, "bf16", seed=16, index="mixed", whole=True)
+    c.down = spread(c.down, bufs[0], (far, 264, 1))
+    c.up = spread(c.up, bufs[1], (far, 16, 1))
+    check_forward(plans["bf16"], c, "f32", whole=True)
+    check_backward(plans["bf16"], c, whole=True, out="f32")
+    few = Case(3, 136, 264, 16, 2, "bf16", seed=16, index="mixed", whole=True)
+    few.down, few.up = c.down, c.up
+    check_forward(plans["bf16"], few, "f32", whole=True)
+    # rows of X, of hidden, of D and of a gradient far apart
+    near_X, few.down, few.up = few.X[:2].clone(), c.down.clone(), c.up.clone()
+    few.M, few.X, few.index, few.dY = 2, spread(near_X, bufs[0], (far, 1)), few.index[:2].contiguous(), few.dY[:2]
+    D = torch.as_strided(bufs[1], (2, 136), (far, 1), 1)
+    hidden = torch.as_strided(bufs[1], (2, 32), (far, 1), 1024)
+    want = plans["bf16"].linear_adapters(padded(near_X.double(), "bf16"), *few.args())
+    got = plans["bf16"].linear_adapters(few.X, *few.args(), D, hidden=hidden)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    a = plans["bf16"].linear_adapters_grad(few.dY, few.B, few.X, hidden, few.down, few.up, few.index, few.scale)
+    d_down = torch.as_strided(bufs[1], (2, 16, 264), (far, 264, 1), 2048)
+    b = plans["bf16"].linear_adapters_grad(few.dY, few.B, few.X, hidden, few.down, few.up, few.index, few.scale, d_down=d_down)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_at_once(tc):
+    """Two plans on two streams at the same time, time and again: the same bits as alone."""
+    cases = [Case(M, 1032, 2056, 16, 7, "bf16", seed=17, index="mixed") for M in (33, 900)]
+    ps = [tc.Plan("bf16", 0) for _ in cases]
+
+    def calls(p, c):
+        D, hidden = p.linear_adapters(c.X, *c.args())
+        return (D, hidden, *p.linear_adapters_grad(c.dY, c.B, c.X, hidden, c.down, c.up, c.index, c.scale))
+
+    want = [calls(p, c) for p, c in zip(ps, cases)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    for _ in range(5):
+        got = []
+        for p, c, s in zip(ps, cases, streams):
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    r = calls(p, c)
+                got.append(r)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for a, b in zip(got, want) for x, y in zip(a, b))
+    for p in ps:
+        assert p.device_status() == 0
+        p.close()
+
+
 def test_empty(plans):
     plan = plans["bf16"]
     z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")      # noqa: E731
