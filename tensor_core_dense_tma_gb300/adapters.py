@@ -6,6 +6,10 @@ computation is the library's kernels on the given (or current) stream.  A
 stack of factors is G x R x K (``down``) or G x N x R (``up``), with unit stride
 along either of its last two dimensions: ``up.transpose(1, 2)`` is a ``down``
 for the backward direction without a copy.
+
+What a call returns belongs to torch's current stream; with another ``stream``
+order the two, as for any tensor used on a second stream.  Its own buffers it
+sees to itself.
 """
 from __future__ import annotations
 
@@ -219,8 +223,12 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
     d_down, down_ld, down_stride = _gradient(d_down, out, dev, di, (G, R, K), "d_down")
     d_up, up_ld, up_stride = _gradient(d_up, out, dev, di, (G, N, R), "d_up")
     p = calls["torch"].empty_strided((M, hidden_width(R)), (ldh, 1), dtype=dtype, device=dev)
+    current = calls["stream"](di)
     if stream is None:
-        stream = calls["stream"](di)
+        stream = current
+    elif stream != current:
+        # p goes back to the current stream's memory when this returns
+        p.record_stream(calls["torch"].cuda.ExternalStream(stream, device=dev))
     # dX is the same product the other way round (a matrix's transpose is the same memory in
     # the other order), and leaves p as its hidden rows
     a = Adapters(G, R, *upper[:3], 1 - upper[3], *lower[:3], 1 - lower[3], scales, at)

@@ -14,7 +14,7 @@ have such rows too, or the gradient be given with the logits' stride: a gradient
 row that starts elsewhere within 16 bytes than its logits is stored element by
 element (2048 x 65537 bf16 282 us, with equal rows 96).
 
-What a call allocates belongs to torch's current stream; with another
+What a call returns belongs to torch's current stream; with another
 ``stream`` order the two, as for any tensor used on a second stream.
 """
 from __future__ import annotations
@@ -390,6 +390,9 @@ def preference_loss_grad(logits, tokens, offsets, weight, ref_logprob=None, *, b
     dlogits, ldd = _gradient(dlogits, logits)
     loss, reward, lp = out
     work = torch.empty((4 * rows[3],), dtype=torch.float32, device=logits.device)
+    if stream is not None and stream != _stream(None, logits.device):
+        # work goes back to the current stream's memory when this returns
+        work.record_stream(torch.cuda.ExternalStream(stream, device=logits.device))
     _call("logits_preference_grad", *rows, temperature, ctypes.byref(preference), w, loss.data_ptr(),
           reward.data_ptr(), lp.data_ptr(), dlogits.data_ptr(), ldd, work.data_ptr(), _stream(stream, logits.device))
     return PreferenceLossGrad(loss, reward, lp, dlogits)

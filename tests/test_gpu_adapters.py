@@ -501,6 +501,26 @@ def test_offsets_past_32_bits(plans):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_given_stream(plans):
+    """`stream` another than the current one, which takes what memory it can get
+    meanwhile: the call's own buffer is not among it."""
+    plan = plans["bf16"]
+    c = Case(300, 264, 520, 16, 3, "bf16", seed=18, index="mixed")
+    _, hidden = plan.linear_adapters(c.X, *c.args())
+    args = (c.dY, c.B, c.X, hidden, c.down, c.up, c.index, c.scale)
+    want = plan.linear_adapters_grad(*args)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = plan.linear_adapters_grad(*args, stream=s.cuda_stream)
+        for _ in range(8):
+            torch.full((300, 32), float("nan"), dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_two_at_once(tc):
     """Two plans on two streams at the same time, time and again: the same bits as alone."""
     cases = [Case(M, 1032, 2056, 16, 7, "bf16", seed=17, index="mixed") for M in (33, 900)]

@@ -416,6 +416,25 @@ def test_streams_and_graphs(tc):      # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(r, want))
 
 
+def test_given_stream(tc):      # noqa: F811
+    """`stream` another than the current one, which takes what memory it can get
+    meanwhile: the call's own buffer is not among it."""
+    view, _ = make(200, 5000, "bf16", seed=6)
+    tok = torch.arange(200, device="cuda")
+    o, w = torch.tensor([0, 90, 200], device="cuda"), torch.ones(1, device="cuda")
+    want = tc.preference_loss_grad(view, tok, o, w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = tc.preference_loss_grad(view, tok, o, w, stream=s.cuda_stream)
+        for _ in range(8):
+            torch.full((800,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_empty_calls(tc):      # noqa: F811
     z = torch.empty((0, 100), device="cuda")
     e, i = torch.empty(0, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
