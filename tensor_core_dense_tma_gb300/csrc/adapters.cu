@@ -115,13 +115,16 @@ constexpr int64_t kMaxExtent = 0x7FFFF000;
 constexpr int64_t kMaxStride = int64_t(1) << 39;      // elements: below 2^40 bytes, what a tensor map takes
 
 // Whether hidden_rows_kernel makes h (down factors K-contiguous): it reads X and A from
-// L2 again for every row, so its time goes with rows x rank x K, while
-// hidden_tile_kernel takes 6 us and more for anything, and more again where a tile's rows
-// have many adapters.  Measured (us), rows / tiles with 4 and with 64 adapters in turn:
-// K = 8192, rank 16: 16 rows 2.9 / 14, 40; 64 rows 3.4 / 14, 146; 256 rows 8.4 / 15, 146
-// (10 where each tile has one); rank 64, 4 adapters: 64 rows 8.6 / 26, 128 rows 14 / 26 (11
-// where each tile has one).  256 x 16 x 8192 and 64 x 64 x 8192 are 2^25.
-bool by_rows(int64_t M, int part, int64_t K) { return M <= 65535 && M * part <= (int64_t(1) << 25) / K; }
+// L2 again for every row, so its time goes with rows x rank x K, whatever the rows'
+// adapters are, while hidden_tile_kernel takes 6 to 11 us where a tile has one adapter and
+// many times that where it has many.  Measured (us), rows / tiles of one adapter / of 64 in
+// turn: K = 8192, rank 16: 64 rows 3.4 / 9.5 / 146, 256 rows 8.5 / 9.7 / 146, 512 rows 14 /
+// 9.8 / 147; rank 64: 64 rows 8.9 / 11 / 330, 128 rows 15 / 11 / 331, 256 rows 28 / 11 /
+// 336; K = 4096, rank 16: 256 rows 6.4 / 7.8, 512 rows 10.8 / 7.8.  2^25 is 256 x 16 x 8192;
+// up to 128 rows, most likely tokens of different requests, twice that.
+bool by_rows(int64_t M, int part, int64_t K) {
+    return M <= 65535 && M * part <= (int64_t(1) << (M <= 128 ? 26 : 25)) / K;
+}
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 bool layout_ok(gemm_layout_t l) { return l == GEMM_ROW_MAJOR || l == GEMM_COL_MAJOR; }
 
