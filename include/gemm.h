@@ -39,7 +39,9 @@
  * stream) and synchronises nothing; results are visible after the caller
  * synchronises the stream.  A plan holds device state (a status word,
  * split-K partials and counters, early-partial flags) and must not be used
- * from two streams at once, nor from two host threads at once.
+ * from two streams at once, nor from two host threads at once.  Calls on
+ * device buffers may be captured in a graph (a larger gemm_run_i8 only after a
+ * call of its size); a replay counts as a call of its plan.
  *
  * Alignment ("CUDA算子优化(5)：WMMA矩阵乘法", load_matrix_sync: ldm a
  * multiple of 16 bytes): A and B must start on 16-byte boundaries and

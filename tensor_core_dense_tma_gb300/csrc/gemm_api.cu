@@ -432,12 +432,29 @@ gemm_status_t describe_impl(const gemm_plan* plan, int64_t M, int64_t N, int64_t
                             gemm_layout_t layoutB, gemm_dtype_t accum_dtype, gemm_dtype_t out_dtype, char* buf,
                             int64_t len);
 
+// Early partials and stream-K tell one launch's flags from another's by a tag.  All
+// replays of a captured launch have the same one, so what a replay finds is what the one before
+// it left: a captured launch of theirs clears the flags first.
+gemm_status_t clear_captured_flags(gemm_plan* plan, const Choice& ch, cudaStream_t s) {
+    if (!ch.early) return GEMM_OK;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess ||
+        (capture != cudaStreamCaptureStatusNone &&
+         cudaMemsetAsync(plan->d_flags, 0, kNumCounters * sizeof(unsigned), s) != cudaSuccess)) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
 // Launch one chosen configuration (arguments already validated, M, N, K > 0).
 gemm_status_t run_choice(gemm_plan* plan, const Choice& ch, const void* A, const void* B, const void* C, void* D,
                          int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
                          gemm_layout_t layoutA, gemm_layout_t layoutB, gemm_dtype_t accum_dtype,
                          gemm_dtype_t out_dtype, float alpha, float beta, const gemm_epilogue_t* ep,
                          cudaStream_t s) {
+    const gemm_status_t st = clear_captured_flags(plan, ch, s);
+    if (st != GEMM_OK) return st;
     const Problem pr = make_problem(ch.swap, A, B, M, N, K, lda, ldb, layoutA, layoutB, ep);
     const int slot = out_slot(accum_dtype, out_dtype);
     const int in_kind = input_kind(plan->in_dtype);
@@ -503,6 +520,8 @@ gemm_status_t run_keep_nan(gemm_plan* plan, const void* A, const void* B, void* 
         plan->forced_division = division;
         if (!valid) return GEMM_ERR_UNSUPPORTED;
     }
+    const gemm_status_t st = clear_captured_flags(plan, ch, s);
+    if (st != GEMM_OK) return st;
     const Problem pr = make_problem(ch.swap, A, B, M, N, K, lda, ldb, GEMM_ROW_MAJOR, GEMM_COL_MAJOR, ep);
     return launch_pair256_ep_nan(plan, out_slot(GEMM_F32, out), ch, pr, D, ldd, s);
 }
@@ -511,16 +530,7 @@ gemm_status_t choose_adapters(gemm_plan* plan, int64_t M, int64_t N, int64_t K, 
                               gemm_dtype_t out, cudaStream_t s, Choice* ch) {
     bool valid = true;
     *ch = select_choice(plan, M, N, K, GEMM_ROW_MAJOR, layoutW, GEMM_F32, out, &valid, nullptr);
-    if (!valid) return GEMM_ERR_UNSUPPORTED;
-    if (!ch->early) return GEMM_OK;
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess ||
-        (capture != cudaStreamCaptureStatusNone &&
-         cudaMemsetAsync(plan->d_flags, 0, kNumCounters * sizeof(unsigned), s) != cudaSuccess)) {
-        cudaGetLastError();
-        return GEMM_ERR_CUDA;
-    }
-    return GEMM_OK;
+    return valid ? clear_captured_flags(plan, *ch, s) : GEMM_ERR_UNSUPPORTED;
 }
 
 gemm_status_t launch_adapters(gemm_plan* plan, const Choice& ch, const void* X, const void* W, void* D, int64_t M,
