@@ -731,7 +731,7 @@ class Plan:
                              stream=None) -> AdaptersGrad:
         """Gradients of sum(dY * linear_adapters(...)) for X, down and up: B, X, down,
         up, index and scale as given to that call, hidden as it returned it
-        (gemm_run_adapters, gemm_adapters_grad).  d_down and d_up are of the
+        (None without rows or adapters; gemm_run_adapters, gemm_adapters_grad).  d_down and d_up are of the
         plan's type unless given as fp32; an adapter without rows has zeros."""
         return _adapters.linear_grad(self, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up, stream)
 

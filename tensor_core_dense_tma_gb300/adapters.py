@@ -214,6 +214,8 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
     lddy = _row_ld(dY, "dY", di, dtype)
     ldb, layout = _weights(B, di, dtype, K, N)
     G, R, lower, upper, scales, at = _adapters(down, up, index, scale, M, N, K, di, dtype)
+    if hidden is None and M and G:
+        raise ValueError("hidden must be what linear_adapters returned")
     dX, x_type, lddx = _result(dX, "dX", M, K, di, dev, None, dtype)
     hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
     like = d_down if d_down is not None else d_up
