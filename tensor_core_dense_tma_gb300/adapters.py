@@ -8,13 +8,15 @@ along either of its last two dimensions: ``up.transpose(1, 2)`` is a ``down``
 for the backward direction without a copy.
 
 What a call returns belongs to torch's current stream; with another ``stream``
-order the two, as for any tensor used on a second stream.  Its own buffers it
-sees to itself.
+order the two, as for any tensor used on a second stream.  A result that is not
+looked at (``hidden`` where one serves) may be dropped at once.
 """
 from __future__ import annotations
 
 import ctypes
 from typing import NamedTuple
+
+from .logits import _stream
 
 __all__ = ["AdaptersGrad", "MAX_RANK"]
 
@@ -174,15 +176,20 @@ def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, strea
         raise ValueError("inner dimensions differ")
     order = _weights(B, di, dtype, K, N)
     G, R, lower, upper, scales, at = _adapters(down, up, index, scale, M, N, K, di, dtype)
+    given = D, hidden
     D, out, ldd = _result(D, "D", M, N, di, dev, None if out_dtype is None else types[out_dtype], dtype)
     if bias is not None and (bias.dtype is not calls["f32"] or bias.shape != (N,) or bias.get_device() != di
                              or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous fp32 vector of length N on X's device")
     hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
     a = Adapters(G, R, *lower, *upper, scales, at)
+    if stream is None:
+        stream = calls["stream"](di)
+    else:
+        _stream(stream, dev, *[t for t, g in zip((D, hidden), given) if g is None])
     st = calls["run"](plan.handle, X.data_ptr(), B.data_ptr(), D.data_ptr(), M, N, K, ldx, order[0], ldd, order[1],
                       calls["codes"][out], None if bias is None else bias.data_ptr(), ctypes.byref(a),
-                      hidden.data_ptr(), ldh, calls["stream"](di) if stream is None else stream)
+                      hidden.data_ptr(), ldh, stream)
     if st != 0:
         raise calls["error"](st, "gemm_run_adapters")
     return D, hidden
@@ -216,6 +223,7 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
     G, R, lower, upper, scales, at = _adapters(down, up, index, scale, M, N, K, di, dtype)
     if hidden is None and M and G:
         raise ValueError("hidden must be what linear_adapters returned")
+    given = dX, d_down, d_up
     dX, x_type, lddx = _result(dX, "dX", M, K, di, dev, None, dtype)
     hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
     like = d_down if d_down is not None else d_up
@@ -225,12 +233,10 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
     d_down, down_ld, down_stride = _gradient(d_down, out, dev, di, (G, R, K), "d_down")
     d_up, up_ld, up_stride = _gradient(d_up, out, dev, di, (G, N, R), "d_up")
     p = calls["torch"].empty_strided((M, hidden_width(R)), (ldh, 1), dtype=dtype, device=dev)
-    current = calls["stream"](di)
     if stream is None:
-        stream = current
-    elif stream != current:
-        # p goes back to the current stream's memory when this returns
-        p.record_stream(calls["torch"].cuda.ExternalStream(stream, device=dev))
+        stream = calls["stream"](di)
+    else:
+        _stream(stream, dev, p, *[t for t, g in zip((dX, d_down, d_up), given) if g is None])
     # dX is the same product the other way round (a matrix's transpose is the same memory in
     # the other order), and leaves p as its hidden rows
     a = Adapters(G, R, *upper[:3], 1 - upper[3], *lower[:3], 1 - lower[3], scales, at)

@@ -15,7 +15,8 @@ row that starts elsewhere within 16 bytes than its logits is stored element by
 element (2048 x 65537 bf16 282 us, with equal rows 96).
 
 What a call returns belongs to torch's current stream; with another
-``stream`` order the two, as for any tensor used on a second stream.
+``stream`` order the two, as for any tensor used on a second stream.  A result that
+is not looked at may be dropped at once.
 """
 from __future__ import annotations
 
@@ -139,14 +140,16 @@ def _vector(v, n: int, dtype, device, what: str):
 
 
 def _gradient(dlogits, logits):
+    """(gradient, its row stride, the same if it was allocated here)."""
     import torch
     T, V = logits.shape
+    own = None
     if dlogits is None:
         unit = 16 // logits.element_size()
-        dlogits = torch.empty((T, -(-V // unit) * unit), dtype=logits.dtype, device=logits.device)[:, :V]
+        own = dlogits = torch.empty((T, -(-V // unit) * unit), dtype=logits.dtype, device=logits.device)[:, :V]
     elif dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.device != logits.device:
         raise ValueError("dlogits must have the logits' shape, type and device")
-    return dlogits, _matrix(dlogits, "dlogits")[2]
+    return dlogits, _matrix(dlogits, "dlogits")[2], own
 
 
 def _outputs(T: int, dev, first: bool):
@@ -172,11 +175,19 @@ def _call(name: str, *args):
         raise GemmError(st, name)
 
 
-def _stream(stream, device):
-    if stream is not None:
-        return stream
+def _stream(stream, device, *own):
+    """The stream of a call: the given or the current one.  The memory of its `own` tensors (those it
+    allocated, of the current stream's; None: none) goes back there once nobody holds them, say an output that
+    the caller does not look at; with a given stream, not before what is on that one now has ended."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)    # current_stream() takes 2 us to make an object
+    current = torch._C._cuda_getCurrentRawStream(device.index)    # current_stream() takes 2 us to make an object
+    if stream is None or stream == current:
+        return current
+    other = torch.cuda.ExternalStream(stream, device=device)
+    for t in own:
+        if t is not None:
+            t.record_stream(other)
+    return stream
 
 
 def token_logprobs(logits, tokens=None, top: int = 0, *, temperature: float = 1.0, stream=None) -> TokenLogprobs:
@@ -196,7 +207,7 @@ def token_logprobs(logits, tokens=None, top: int = 0, *, temperature: float = 1.
     top_tok = torch.empty((T, top), dtype=torch.int64, device=dev)
     _call("logits_logprobs", dev.index, code, logits.data_ptr(), T, V, ld, tok, temperature, top,
           lp.data_ptr() if lp is not None else None, entropy.data_ptr(), lse.data_ptr(), top_lp.data_ptr(),
-          top_tok.data_ptr(), _stream(stream, dev))
+          top_tok.data_ptr(), _stream(stream, dev, lp, entropy, lse, top_lp, top_tok))
     return TokenLogprobs(lp, entropy, lse, top_lp, top_tok)
 
 
@@ -214,11 +225,11 @@ def token_logprobs_grad(logits, tokens=None, grad_logprob=None, grad_entropy=Non
     h = _vector(grad_entropy, T, torch.float32, dev, "grad_entropy")
     if grad_logprob is not None and tokens is None:
         raise ValueError("grad_logprob needs tokens")
-    dlogits, ldd = _gradient(dlogits, logits)
+    dlogits, ldd, own = _gradient(dlogits, logits)
     lp, entropy, lse = _outputs(T, dev, tokens is not None)
     _call("logits_logprobs_grad", dev.index, code, logits.data_ptr(), T, V, ld, tok, temperature, g, h,
           lp.data_ptr() if lp is not None else None, entropy.data_ptr(), lse.data_ptr(), dlogits.data_ptr(), ldd,
-          _stream(stream, dev))
+          _stream(stream, dev, lp, entropy, lse, own))
     return TokenLogprobsGrad(lp, entropy, lse, dlogits)
 
 
@@ -250,7 +261,7 @@ def distill_topk(logits, teacher_tokens, teacher_logits, *, temperature: float =
     teacher = _teacher(teacher_tokens, teacher_logits, T, dev)
     _, loss, lse = _outputs(T, dev, False)
     _call("logits_distill", dev.index, code, logits.data_ptr(), T, V, ld, *teacher, temperature, loss.data_ptr(),
-          lse.data_ptr(), _stream(stream, dev))
+          lse.data_ptr(), _stream(stream, dev, loss, lse))
     return loss, lse
 
 
@@ -267,10 +278,10 @@ def distill_topk_grad(logits, teacher_tokens, teacher_logits, weight, *, tempera
     if weight is None:
         raise ValueError("weight must be given")
     w = _vector(weight, T, torch.float32, dev, "weight")
-    dlogits, ldd = _gradient(dlogits, logits)
+    dlogits, ldd, own = _gradient(dlogits, logits)
     loss = torch.empty((T,), dtype=torch.float32, device=dev)
     _call("logits_distill_grad", dev.index, code, logits.data_ptr(), T, V, ld, *teacher, temperature, w,
-          loss.data_ptr(), None, dlogits.data_ptr(), ldd, _stream(stream, dev))
+          loss.data_ptr(), None, dlogits.data_ptr(), ldd, _stream(stream, dev, loss, own))
     return loss, dlogits
 
 
@@ -318,7 +329,7 @@ def policy_loss(logits, tokens, old_logprob, advantage, ref_logprob=None, *, cli
                                         entropy_bonus)
     loss, lp, k, ent = out
     _call("logits_policy", *rows, temperature, ctypes.byref(policy), loss.data_ptr(), lp.data_ptr(), k.data_ptr(),
-          ent.data_ptr(), _stream(stream, logits.device))
+          ent.data_ptr(), _stream(stream, logits.device, *out))
     return PolicyLoss(loss, lp, k, ent)
 
 
@@ -332,10 +343,10 @@ def policy_loss_grad(logits, tokens, old_logprob, advantage, weight, ref_logprob
         raise ValueError("weight must be given")
     rows, policy, w, out = _policy_args(logits, tokens, old_logprob, advantage, weight, ref_logprob, clip, kl,
                                         entropy_bonus)
-    dlogits, ldd = _gradient(dlogits, logits)
+    dlogits, ldd, own = _gradient(dlogits, logits)
     loss, lp, k, ent = out
     _call("logits_policy_grad", *rows, temperature, ctypes.byref(policy), w, loss.data_ptr(), lp.data_ptr(),
-          k.data_ptr(), ent.data_ptr(), dlogits.data_ptr(), ldd, _stream(stream, logits.device))
+          k.data_ptr(), ent.data_ptr(), dlogits.data_ptr(), ldd, _stream(stream, logits.device, *out, own))
     return PolicyLossGrad(loss, lp, k, ent, dlogits)
 
 
@@ -372,7 +383,7 @@ def preference_loss(logits, tokens, offsets, ref_logprob=None, *, beta: float = 
     rows, preference, _, out = _preference_args(logits, tokens, offsets, None, ref_logprob, beta, smoothing)
     loss, reward, lp = out
     _call("logits_preference", *rows, temperature, ctypes.byref(preference), loss.data_ptr(), reward.data_ptr(),
-          lp.data_ptr(), _stream(stream, logits.device))
+          lp.data_ptr(), _stream(stream, logits.device, *out))
     return PreferenceLoss(loss, reward, lp)
 
 
@@ -387,12 +398,10 @@ def preference_loss_grad(logits, tokens, offsets, weight, ref_logprob=None, *, b
     if weight is None:
         raise ValueError("weight must be given")
     rows, preference, w, out = _preference_args(logits, tokens, offsets, weight, ref_logprob, beta, smoothing)
-    dlogits, ldd = _gradient(dlogits, logits)
+    dlogits, ldd, own = _gradient(dlogits, logits)
     loss, reward, lp = out
     work = torch.empty((4 * rows[3],), dtype=torch.float32, device=logits.device)
-    if stream is not None and stream != _stream(None, logits.device):
-        # work goes back to the current stream's memory when this returns
-        work.record_stream(torch.cuda.ExternalStream(stream, device=logits.device))
     _call("logits_preference_grad", *rows, temperature, ctypes.byref(preference), w, loss.data_ptr(),
-          reward.data_ptr(), lp.data_ptr(), dlogits.data_ptr(), ldd, work.data_ptr(), _stream(stream, logits.device))
+          reward.data_ptr(), lp.data_ptr(), dlogits.data_ptr(), ldd, work.data_ptr(),
+          _stream(stream, logits.device, *out, work, own))
     return PreferenceLossGrad(loss, reward, lp, dlogits)

@@ -20,3 +20,57 @@ def test_gradient_without_hidden(plans):      # noqa: F811
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
     g = plan.linear_adapters_grad(c.dY[:0], c.B, c.X[:0], None, c.down, c.up, none, c.scale)
     assert g.dX.shape == (0, 520) and not g.d_down.any() and not g.d_up.any()
+
+
+def dropped(call, pick, want, fill):
+    """call(stream) on a stream that is busy, all of its results dropped but pick's, the current stream's next
+    allocations in the memory that this frees; pick's results as wanted, and what was allocated as filled."""
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = pick(call(s.cuda_stream))
+        later = [torch.full_like(t, 3) for t in fill for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert all(bool((t == 3).all()) for t in later)
+
+
+@pytest.mark.parametrize("M", [4, 300])
+def test_serving_on_a_given_stream(plans, M):      # noqa: F811
+    """A caller that wants D alone drops the hidden rows while both kernels are still to run."""
+    plan = plans["bf16"]
+    c = Case(M, 264, 520, 16, 3, "bf16", seed=41, index="mixed")
+    D, hidden = plan.linear_adapters(c.X, *c.args())
+    dropped(lambda s: plan.linear_adapters(c.X, *c.args(), stream=s), lambda r: r[:1], [D], [hidden])
+    dropped(lambda s: plan.linear_adapters(c.X, *c.args(), stream=s), lambda r: r[1:], [hidden], [D])
+
+
+def test_gradient_on_a_given_stream(plans):      # noqa: F811
+    """The same of a caller that does not want dX."""
+    plan = plans["bf16"]
+    c = Case(300, 264, 520, 16, 3, "bf16", seed=42, index="mixed")
+    _, hidden = plan.linear_adapters(c.X, *c.args())
+    args = (c.dY, c.B, c.X, hidden, c.down, c.up, c.index, c.scale)
+    want = plan.linear_adapters_grad(*args)
+    dropped(lambda s: plan.linear_adapters_grad(*args, stream=s), lambda r: r[1:], want[1:], [want.dX])
+
+
+def test_losses_on_a_given_stream(tc):      # noqa: F811
+    """One result of each operator on logits kept."""
+    g = torch.Generator(device="cuda").manual_seed(43)
+    z = torch.randn((64, 5000), generator=g, device="cuda")
+    t = torch.randint(0, 5000, (64,), generator=g, device="cuda")
+    old, adv = torch.randn((2, 64), generator=g, device="cuda").unbind()
+    at, w = torch.tensor([0, 20, 64], device="cuda"), torch.ones(1, device="cuda")
+    r = tc.token_logprobs(z, t, top=4)
+    for name, args, kw in (("token_logprobs", (t,), dict(top=4)), ("token_logprobs_grad", (t, adv, old), {}),
+                           ("distill_topk", (r.top_token, r.top_logprob), {}),
+                           ("distill_topk_grad", (r.top_token, r.top_logprob, adv), {}),
+                           ("policy_loss", (t, old, adv), {}), ("policy_loss_grad", (t, old, adv, adv), {}),
+                           ("preference_loss", (t, at), {}), ("preference_loss_grad", (t, at, w), {})):
+        call = lambda s=None: getattr(tc, name)(z, *args, stream=s, **kw)      # noqa: E731, B023
+        want = call()
+        for i in range(len(want)):
+            dropped(call, lambda r, i=i: [r[i]], [want[i]], [t for k, t in enumerate(want) if k != i])
