@@ -87,8 +87,11 @@ gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void *X, const void *W, 
 
 /* d_down[g * down_stride + r * down_ld + k] and d_up[g * up_stride + n * up_ld + r],
  * of all `count` adapters (zeros for one without rows), from X (M x K), dD
- * (M x N), both row-major, h and p.  Of `adapters` count, rank and index are
- * used.  Either of d_down and d_up may be NULL, with what only it needs. */
+ * (M x N), both row-major, h and p.  The adapters' gradients lie one after
+ * another, or their rows in turn (down_ld >= (count - 1) down_stride + K); in a
+ * stack whose matrices overlap their CTAs would write the same memory
+ * (GEMM_ERR_INVALID_ARG).  Of `adapters` count, rank and index are used.
+ * Either of d_down and d_up may be NULL, with what only it needs. */
 gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void *X, const void *dD, int64_t M, int64_t N, int64_t K,
                                  int64_t ldx, int64_t lddd, const gemm_adapters_t *adapters, const void *h,
                                  const void *p, int64_t ldh, gemm_dtype_t out_dtype, void *d_down, int64_t down_ld,

@@ -173,10 +173,17 @@ gemm_status_t check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld
     return aligned(p, 16) && ld % 8 == 0 ? GEMM_OK : GEMM_ERR_MISALIGNED;
 }
 
-gemm_status_t check_gradient(int64_t count, int64_t ld, int64_t stride, int64_t inner) {
-    if (count == 0) return GEMM_OK;
+// A stack that is written: its matrices do not overlap, lying one after another or row by row in turn.
+gemm_status_t check_gradient(int64_t count, int64_t rows, int64_t inner, int64_t ld, int64_t stride) {
+    if (count == 0 || rows == 0 || inner == 0) return GEMM_OK;
     if (ld < inner || stride < 0) return GEMM_ERR_INVALID_ARG;
-    return ld >= kMaxStride || stride >= kMaxStride ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+    if (ld >= kMaxStride || stride >= kMaxStride) return GEMM_ERR_UNSUPPORTED;
+    // whether n rows of `inner` at distances of `step` end before `next`
+    auto fits = [&](int64_t n, int64_t step, int64_t next) {
+        return next >= inner && (n == 1 || (step > 0 && n - 1 <= (next - inner) / step));
+    };
+    return count == 1 || fits(rows, ld, stride) || (stride >= inner && fits(count, stride, ld)) ? GEMM_OK
+                                                                                               : GEMM_ERR_INVALID_ARG;
 }
 
 gemm_status_t launched(gemm_plan* plan, cudaError_t e) {
@@ -334,12 +341,12 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     if (d_down) {
         st = check_matrix(X, M, K, ldx);
         if (st == GEMM_OK) st = check_matrix(p, M, 2 * part, ldh);
-        if (st == GEMM_OK) st = check_gradient(a.count, down_ld, down_stride, K);
+        if (st == GEMM_OK) st = check_gradient(a.count, a.rank, K, down_ld, down_stride);
     }
     if (d_up && st == GEMM_OK) {
         st = check_matrix(dD, M, N, lddd);
         if (st == GEMM_OK) st = check_matrix(h, M, 2 * part, ldh);
-        if (st == GEMM_OK) st = check_gradient(a.count, up_ld, up_stride, a.rank);
+        if (st == GEMM_OK) st = check_gradient(a.count, N, a.rank, up_ld, up_stride);
     }
     if (st != GEMM_OK) return st;
     const uintptr_t esz = out_dtype == GEMM_F32 ? 4 : 2;

@@ -74,3 +74,42 @@ def test_losses_on_a_given_stream(tc):      # noqa: F811
         want = call()
         for i in range(len(want)):
             dropped(call, lambda r, i=i: [r[i]], [want[i]], [t for k, t in enumerate(want) if k != i])
+
+
+def test_gradients_that_overlap(tc, plans):      # noqa: F811
+    """The C entry point on output stacks whose matrices share memory: refused before anything is launched; stacks
+    of another order, where each element has a place of its own, are written."""
+    plan = plans["bf16"]
+    lib, Adapters = tc.load(), tc._adapters.Adapters
+    c = Case(300, 264, 520, 16, 3, "bf16", seed=44, index="mixed")
+    _, hidden = plan.linear_adapters(c.X, *c.args())
+    want = plan.linear_adapters_grad(c.dY, c.B, c.X, hidden, c.down, c.up, c.index, c.scale)
+    p = torch.empty_like(hidden)
+    G, R, K, N = 3, 16, 520, 264
+    a = Adapters(G, R, c.up.data_ptr(), c.up.stride(1), c.up.stride(0), 1, c.down.data_ptr(), c.down.stride(1),
+                 c.down.stride(0), 1, c.scale.data_ptr(), c.index.data_ptr())      # the way back's: each in the other's place
+    dX = torch.empty((300, K), dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    assert lib.gemm_run_adapters(plan.handle, c.dY.data_ptr(), c.B.data_ptr(), dX.data_ptr(), 300, K, N, c.dY.stride(0),
+                                 c.B.stride(1), K, 0, 1, None, tc._adapters.ctypes.byref(a), p.data_ptr(), 32, s) == 0
+    d_down = torch.full((G * R * K + 99,), 7.0, dtype=torch.bfloat16, device="cuda")
+    d_up = torch.full((G * N * R + 99,), 7.0, dtype=torch.bfloat16, device="cuda")
+
+    def grad(down_ld, down_stride, up_ld, up_stride, parts=3):
+        return lib.gemm_adapters_grad(plan.handle, c.X.data_ptr(), c.dY.data_ptr(), 300, N, K, c.X.stride(0),
+                                      c.dY.stride(0), tc._adapters.ctypes.byref(a), hidden.data_ptr(), p.data_ptr(), 32, 1,
+                                      d_down.data_ptr() if parts & 1 else None, down_ld, down_stride,
+                                      d_up.data_ptr() if parts & 2 else None, up_ld, up_stride, s)
+
+    for bad in ((K, 0, R, N * R), (K, R * K - 1, R, N * R), (K, K, R, N * R), (G * K, K - 1, R, N * R),
+                (G * K - 1, K, R, N * R), (K, R * K, R, 0), (K, R * K, R, N * R - 1), (K, R * K, G * R - 1, R)):
+        assert tc.STATUS[grad(*bad)] == "GEMM_ERR_INVALID_ARG", bad
+    torch.cuda.synchronize()
+    assert bool((d_down == 7).all()) and bool((d_up == 7).all())
+    assert grad(K, 0, R, N * R, 2) == 0                        # the other's strides count for nothing
+    for down, up_ in (((K, R * K), (R, N * R)), ((G * K, K), (G * R, R)), ((G * K + 2, K), (R, N * R + 3))):
+        d_down.fill_(7), d_up.fill_(7)
+        assert grad(*down, *up_) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(torch.as_strided(d_down, (G, R, K), (down[1], down[0], 1)), want.d_down)
+        assert torch.equal(torch.as_strided(d_up, (G, N, R), (up_[1], up_[0], 1)), want.d_up)
