@@ -71,7 +71,9 @@ extern "C" {
  *               NaN) are no alternatives: places that are left hold -inf and -1.
  * tokens may be NULL (then logprob is not written); each of logprob, entropy
  * and lse may be NULL; top is 0..LOGITS_MAX_TOP and the two top arrays may be
- * NULL when it is 0.  temperature is a positive finite number. */
+ * NULL when it is 0.  temperature is a positive finite number.
+ * Every operator's logprob of equal logits is the same number (calls with few rows, or with a
+ * gradient, may divide a row otherwise and differ in the last bit). */
 gemm_status_t logits_logprobs(int device, gemm_dtype_t dtype, const void *logits, int64_t T, int64_t V, int64_t ld,
                               const int64_t *tokens, float temperature, int top, float *logprob, float *entropy,
                               float *lse, float *top_logprob, int64_t *top_token, void *stream);

@@ -70,7 +70,7 @@ struct Args {
     int cluster, rows, slots;     // CTAs of a row, rows of a CTA, chunks of the ring
     int per;                      // vectors of a segment
     float c, inv_t, t;            // log2(e) / temperature, 1 / temperature, temperature
-    float c_rest;                 // what c lacks, as a part of it
+    float c_rest;                 // what c lacks, as a part of it (see log_sum)
     const int64_t* tokens;        // [T], or teacher tokens [T][ldt]
     // log-probabilities
     int top;
@@ -368,6 +368,20 @@ __device__ __forceinline__ void raise_max(Stats& s, float m, float c) {
     s.m = m;
 }
 
+// What ex2.approx lacks on average, relatively: measured over all floats of a range, 4.95e-8 to
+// 5.06e-8 in each of -10 .. -9 to -2 .. -1, 2.5e-8 in -1 .. -1/2, 2.0e-8 in -1/4 .. 0, nothing at 0.
+constexpr float kEx2Lacks = 5.0e-8f;
+
+// raise_max for a sum that is joined with others.  Every value goes through several exponentials on its
+// way into the row's sum, its own and those that scale it to the maximum of the warp, the block and the
+// cluster, all off to one side: what the factor lacks (and `more`) is put back, before the product is
+// rounded (afterwards, below half a unit of S, it would be lost).
+__device__ __forceinline__ void raise_joined(Stats& s, float m, float c, float more) {
+    const float S = s.S, d = max_nan((s.m - m) * c, -1e4f);
+    raise_max(s, m, c);
+    s.S = fmaf(S, ex2(d), s.S * fmaf(fminf(-d, 1.f), kEx2Lacks, more));
+}
+
 // Two floats in a register pair, and the packed arithmetic on them.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
     uint64_t v;
@@ -424,30 +438,41 @@ __device__ __forceinline__ float warp_sum(float x, int width) {
 }
 
 template <bool ENTROPY>
-__device__ __forceinline__ Stats warp_join(Stats s, int width, float c) {
-    raise_max(s, warp_max(s.m), c);
+__device__ __forceinline__ Stats warp_join(Stats s, int width, float c, float more = 0.f) {
+    // (of a distillation's sums no one adds up thousands)
+    if constexpr (ENTROPY) raise_joined(s, warp_max(s.m), c, more);
+    else raise_max(s, warp_max(s.m), c);
     s.S = warp_sum(s.S, width);
     if constexpr (ENTROPY) s.U = warp_sum(s.U, width);
     return s;
 }
 
-// log p of a logit z.  Not ln 2 times the base-2 logarithm: scaled by c, a
-// finite z near the type's lowest value would overflow to -inf.
-__device__ __forceinline__ float log_p(float z, float m, float log2_S, float inv_t) {
-    return fmaf(z - m, inv_t, -kLn2 * log2_S);
+// The logarithm of a row's sum S of e^((z - m) / t), in two parts.  Callers add up thousands of
+// log-probabilities, where an error to one side adds up and one to either side does not:
+//  * lg2.approx is off by up to 2^-22 to one side for long stretches.  So S = 2^e f, f in
+//    3/4 .. 3/2, and ln 2 is split after Cody and Waite: e times its first 12 bits is
+//    exact, logf(f) and what is left are below 0.41, where a unit is 2^-25;
+//  * c = log2(e) / t, rounded to fp32, is a part c_rest too small, the same in every
+//    exponent: S lacks c_rest ln 2 times U, the sum of 2^u u.
+struct LogSum {
+    float hi, lo;
+};
+constexpr float kLn2First = 2839.f / 4096.f, kLn2Rest = static_cast<float>(0.6931471805599453 - 2839.0 / 4096.0);
+
+__device__ __forceinline__ LogSum log_sum(float S, float U, float c_rest) {
+    const int bits = __float_as_int(S), e = (bits - 0x3F400000) >> 23;
+    const float f = __int_as_float(bits - e * (1 << 23)), n = static_cast<float>(e);
+    return {n * kLn2First, logf(f) + fmaf(n, kLn2Rest, c_rest * kLn2 * __fdividef(U, S)) + (S - S)};      // a NaN stays one
 }
 
-// log p of a logit z for sums over thousands of rows, where an error to one side adds
-// up and one to either side does not: a logarithm in 64 bits (lg2.approx is off by up
-// to 2^-22 to one side for long stretches), one rounding, and what ex2.approx lacks on
-// average.  Over 2^22 arguments in each of thirteen ranges from -26 to 0 its
-// mean relative error is -5.0e-8 to -5.1e-8 (and exactly 0 at the maximum, the 1 in S).
-// A reward over 512 rows of 131072 bf16 logits: relative error 1.2e-5 without, 7e-7 with.
-constexpr double kEx2Mean = -5.07e-8;
-
-__device__ __forceinline__ float log_p_unbiased(float z, float m, float S, float t) {
-    const double lacks = kEx2Mean * (1.0 - 1.0 / static_cast<double>(S));
-    return static_cast<float>(static_cast<double>(z - m) / t - log(static_cast<double>(S)) + lacks);
+// log p of a logit z.  Not ln 2 times the base-2 logarithm: scaled by c, a
+// finite z near the type's lowest value would overflow to -inf.
+__device__ __forceinline__ float log_p(float z, float m, const LogSum& l, float t, float inv_t) {
+    const float d = z - m, q = d * inv_t;
+    // what q lacks (inv_t's own rounding is the same in all rows); the logarithm is put together first,
+    // as its last bits differ from row to row and those of 16-bit logits over t hardly do
+    const float rest = isinf(q) ? 0.f : fmaf(-q, t, d) * inv_t;
+    return q - (l.hi + (l.lo - rest));
 }
 
 // Order of alternatives: larger logit first, equal ones by the lowest token.
@@ -698,10 +723,11 @@ __device__ __forceinline__ void select_top(TopState& t, const Segment<E>& seg, u
 template <typename E, int OP, bool GRAD, bool TOP>
 __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args a) {
     constexpr int kPer = Ele<E>::kPer;
-    constexpr bool kEntropy = OP == kLogprobs || OP == kPolicy;
+    constexpr bool kEntropy = OP != kDistill;
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
     __shared__ Exchange inbox[kMaxCluster], all;
+    __shared__ LogSum row_log;
     __shared__ bool heard;                               // of every CTA of the row
     __shared__ volatile int gave_up;                     // on a copy
     __shared__ __align__(8) uint64_t full_bar[kSlotsMost], empty_bar[kSlotsMost], inbox_bar;
@@ -883,7 +909,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         float bucket_max = -INFINITY, bucket_second = -INFINITY;     // of its chunks' maxima
         int bucket_batch = 0;
         Stats s = empty_stats();
-        const uint64_t c2 = pair(a.c, a.c), c_rest2 = pair(a.c_rest, a.c_rest);
+        const uint64_t c2 = pair(a.c, a.c);
         {
             uint64_t m2 = pair(-s.m, -s.m), S2 = 0, U2 = 0;
             auto raise = [&](float m) {
@@ -898,12 +924,6 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             };
             auto add = [&](uint64_t x2) {
                 uint64_t u2 = mul2(add2(x2, m2), c2);
-                // (a preference sums thousands of these: c's own rounding, 2^-26 of u ~ -12, would
-                // be the same in all of them)
-                if constexpr (OP == kScore) {
-                    u2 = max_nan2(u2, -200.f);
-                    u2 = fma2(u2, c_rest2, u2);
-                }
                 if constexpr (kEntropy) u2 = max_nan2(u2, -200.f);
                 const uint64_t e2 = ex2_2(u2);
                 S2 = add2(S2, e2);
@@ -946,7 +966,8 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
 
         // joined over the block by warp 0; the teacher's softmax and the
         // segment's part of a distillation loss are warp 1's
-        s = warp_join<kEntropy>(s, 32, a.c);
+        // (of a thread's elements all but its maximum, 1 of S, went through ex2)
+        s = warp_join<kEntropy>(s, 32, a.c, s.S > 1.f ? kEx2Lacks - __fdividef(kEx2Lacks, s.S) : 0.f);
         if (lane == 0) warp_stats[warp] = s;
         sync_threads();
         if (warp == 0) {
@@ -1014,6 +1035,8 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             __syncwarp();
             if (lane == 0) {
                 all = {s, l, sum_P};
+                // (for all threads of a policy loss: computed by each of them it took 2 % longer)
+                if constexpr (OP == kPolicy) row_log = log_sum(s.S, s.U, a.c_rest);
                 if constexpr (TOP) heard = arrived;
             }
         }
@@ -1023,9 +1046,10 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         const bool nothing = s.S == 0.f;
         const float log2_S = lg2(s.S);
         const float entropy = nothing ? 0.f : kLn2 * (log2_S - s.U / s.S);
+        auto log_of_row = [&] { return OP == kPolicy ? row_log : log_sum(s.S, s.U, a.c_rest); };
         PolicyLoss policy{};
         if constexpr (OP == kPolicy) {
-            const float logprob = nothing ? -INFINITY : log_p(z_token, s.m, log2_S, a.inv_t);
+            const float logprob = nothing ? -INFINITY : log_p(z_token, s.m, row_log, a.t, a.inv_t);
             policy = policy_loss(a, r, logprob);
             if (a.bonus != 0.f) policy.loss = fmaf(-a.bonus, entropy, policy.loss);
         }
@@ -1033,11 +1057,10 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             if (a.lse) a.lse[r] = nothing ? -INFINITY : fmaf(s.m, a.inv_t, kLn2 * log2_S);
             if constexpr (OP != kDistill) {
                 if (a.logprob)
-                    a.logprob[r] = token < 0      ? 0.f
-                                   : nothing      ? -INFINITY
-                                   : OP == kScore ? log_p_unbiased(z_token, s.m, s.S, a.t)
-                                                  : log_p(z_token, s.m, log2_S, a.inv_t);
-                if (kEntropy && a.entropy) a.entropy[r] = entropy;
+                    a.logprob[r] = token < 0 ? 0.f
+                                   : nothing ? -INFINITY
+                                             : log_p(z_token, s.m, log_of_row(), a.t, a.inv_t);
+                if (a.entropy) a.entropy[r] = entropy;
                 if constexpr (OP == kPolicy) {
                     a.loss[r] = policy.loss;
                     if (a.kl) a.kl[r] = policy.kl;
@@ -1193,6 +1216,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                     sync_threads();
                     keys = top->cand;
                 }
+                const LogSum l = log_of_row();
                 for (int i = tid; i < lists * n; i += kThreads) {
                     const uint64_t k = keys[i];
                     if (!k) continue;
@@ -1209,7 +1233,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                     }
                     if (place < n) {
                         const float z = from_ordered(static_cast<uint32_t>(k >> 32));
-                        a.top_logprob[r * n + place] = log_p(z, s.m, log2_S, a.inv_t);
+                        a.top_logprob[r * n + place] = log_p(z, s.m, l, a.t, a.inv_t);
                         a.top_token[r * n + place] = static_cast<int64_t>(~static_cast<uint32_t>(k));
                     }
                 }
