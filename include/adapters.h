@@ -72,6 +72,7 @@ typedef struct {
     gemm_layout_t up_layout;
     const float *scale;        /* [count], or NULL (ones) */
     const int32_t *index;      /* [M] */
+    int64_t ldp;               /* gemm_adapters_grad: row stride of p, 0 for ldh */
 } gemm_adapters_t;
 
 /* Columns of `hidden`: 2 P, P = 16, 32, 64 or 128, the smallest that holds the
@@ -90,7 +91,7 @@ gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void *X, const void *W, 
  * (M x N), both row-major, h and p.  The adapters' gradients lie one after
  * another, or their rows in turn (down_ld >= (count - 1) down_stride + K); in a
  * stack whose matrices overlap their CTAs would write the same memory
- * (GEMM_ERR_INVALID_ARG).  Of `adapters` count, rank and index are used.
+ * (GEMM_ERR_INVALID_ARG).  Of `adapters` count, rank, index and ldp are used.
  * Either of d_down and d_up may be NULL, with what only it needs. */
 gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void *X, const void *dD, int64_t M, int64_t N, int64_t K,
                                  int64_t ldx, int64_t lddd, const gemm_adapters_t *adapters, const void *h,

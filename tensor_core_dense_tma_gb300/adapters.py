@@ -34,7 +34,8 @@ class Adapters(ctypes.Structure):
     _fields_ = [("count", ctypes.c_int64), ("rank", ctypes.c_int64), ("down", ctypes.c_void_p),
                 ("down_ld", ctypes.c_int64), ("down_stride", ctypes.c_int64), ("down_layout", ctypes.c_int),
                 ("up", ctypes.c_void_p), ("up_ld", ctypes.c_int64), ("up_stride", ctypes.c_int64),
-                ("up_layout", ctypes.c_int), ("scale", ctypes.c_void_p), ("index", ctypes.c_void_p)]
+                ("up_layout", ctypes.c_int), ("scale", ctypes.c_void_p), ("index", ctypes.c_void_p),
+                ("ldp", ctypes.c_int64)]
 
 
 def declare(lib: ctypes.CDLL) -> None:
@@ -232,17 +233,18 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
         raise ValueError("d_down and d_up must both be fp32 or both of the plan's type")
     d_down, down_ld, down_stride = _gradient(d_down, out, dev, di, (G, R, K), "d_down")
     d_up, up_ld, up_stride = _gradient(d_up, out, dev, di, (G, N, R), "d_up")
-    p = calls["torch"].empty_strided((M, hidden_width(R)), (ldh, 1), dtype=dtype, device=dev)
+    ldp = hidden_width(R)
+    p = calls["empty"]((M, ldp), dtype=dtype, device=dev)
     if stream is None:
         stream = calls["stream"](di)
     else:
         _stream(stream, dev, p, *[t for t, g in zip((dX, d_down, d_up), given) if g is None])
     # dX is the same product the other way round (a matrix's transpose is the same memory in
     # the other order), and leaves p as its hidden rows
-    a = Adapters(G, R, *upper[:3], 1 - upper[3], *lower[:3], 1 - lower[3], scales, at)
+    a = Adapters(G, R, *upper[:3], 1 - upper[3], *lower[:3], 1 - lower[3], scales, at, ldp)
     this, other, kept, mine = X.data_ptr(), dY.data_ptr(), hidden.data_ptr(), p.data_ptr()
     st = calls["run"](plan.handle, other, B.data_ptr(), dX.data_ptr(), M, K, N, lddy, ldb, lddx, 1 - layout,
-                      calls["codes"][x_type], None, ctypes.byref(a), mine, ldh, stream)
+                      calls["codes"][x_type], None, ctypes.byref(a), mine, ldp, stream)
     if st == 0:
         st = calls["grad"](plan.handle, this, other, M, N, K, ldx, lddy, ctypes.byref(a), kept, mine, ldh,
                            calls["codes"][out], d_down.data_ptr(), down_ld, down_stride, d_up.data_ptr(), up_ld,

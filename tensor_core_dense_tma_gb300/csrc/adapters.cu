@@ -338,9 +338,10 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     if (out_dtype != GEMM_F32 && out_dtype != plan->in_dtype) return GEMM_ERR_UNSUPPORTED;
     const gemm_adapters_t& a = *adapters;
     const int part = part_of(a.rank);
+    const int64_t ldp = a.ldp ? a.ldp : ldh;
     if (d_down) {
         st = check_matrix(X, M, K, ldx);
-        if (st == GEMM_OK) st = check_matrix(p, M, 2 * part, ldh);
+        if (st == GEMM_OK) st = check_matrix(p, M, 2 * part, ldp);
         if (st == GEMM_OK) st = check_gradient(a.count, a.rank, K, down_ld, down_stride);
     }
     if (d_up && st == GEMM_OK) {
@@ -361,11 +362,11 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     if (!on.ok) return GEMM_ERR_CUDA;
     const void* left[2] = {X, dD};
     const void* right[2] = {p, h};
-    const int64_t columns[2] = {K, N}, ld[2] = {ldx, lddd};
+    const int64_t columns[2] = {K, N}, ld[2] = {ldx, lddd}, ld_right[2] = {ldp, ldh};
     for (int i = 0; i < 2 && M > 0; ++i) {
         if (f.f[i].blocks == 0) continue;
         st = encode_map(plan, &f.f[i].tmX, left[i], columns[i], M, ld[i], 64, 64, plan->in_dtype);
-        if (st == GEMM_OK) st = encode_map(plan, &f.f[i].tmH, right[i], 2 * part, M, ldh, 64, 64, plan->in_dtype);
+        if (st == GEMM_OK) st = encode_map(plan, &f.f[i].tmH, right[i], 2 * part, M, ld_right[i], 64, 64, plan->in_dtype);
         if (st != GEMM_OK) return st;
     }
     f.f[0].out = d_down, f.f[0].stride = down_stride, f.f[0].sr = down_ld, f.f[0].sc = 1;

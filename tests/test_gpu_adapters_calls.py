@@ -113,3 +113,25 @@ def test_gradients_that_overlap(tc, plans):      # noqa: F811
         torch.cuda.synchronize()
         assert torch.equal(torch.as_strided(d_down, (G, R, K), (down[1], down[0], 1)), want.d_down)
         assert torch.equal(torch.as_strided(d_up, (G, N, R), (up_[1], up_[0], 1)), want.d_up)
+
+
+@pytest.mark.parametrize("kind,R", [("bf16", 16), ("f16", 40)])
+def test_hidden_in_a_wide_buffer(plans, kind, R):      # noqa: F811
+    """hidden as a slice of a buffer for many layers: the call's own rows are not as wide, and results the same."""
+    plan = plans[kind]
+    c = Case(3000, 136, 264, R, 3, kind, seed=45, index="mixed")
+    _, hidden = plan.linear_adapters(c.X, *c.args())
+    args = (c.dY, c.B, c.X)
+    rest = (c.down, c.up, c.index, c.scale)
+    want = plan.linear_adapters_grad(*args, hidden, *rest)
+    wide = torch.full((3000, 64 * hidden.shape[1]), float("nan"), dtype=c.X.dtype, device="cuda")
+    part = wide[:, 8:8 + hidden.shape[1]]
+    assert torch.equal(plan.linear_adapters(c.X, *c.args(), hidden=part)[1], hidden) and bool(wide[:, :8].isnan().all())
+    out = [torch.empty_like(t) for t in want]
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    got = plan.linear_adapters_grad(*args, part, *rest, *out[:1], d_down=out[1], d_up=out[2])
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before <= 2 * hidden.numel() * hidden.element_size() + (2 << 20)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
