@@ -29,8 +29,16 @@
  * h and p are handed on as `hidden`: M rows of P = gemm_adapters_hidden_width(rank) / 2
  * high parts, the values rounded to the plan's type, and P low parts, what that
  * rounding lost (columns from the rank on are 0): 16 bits would be the
- * only rounding before D's own, the two parts together keep 16 (bf16) or 22 (fp16)
- * bits.  fp16 values are to be within its range.
+ * only rounding before D's own, the two parts together keep 16 (bf16) or up to 22 (fp16)
+ * bits.
+ *
+ * fp16 values are to be within its range, 65504 at most; and its low parts end at 2^-24, so
+ * that a value is off by up to 2^-25 however small it is: one of 1e-3 keeps 15 bits, one of
+ * 1e-5 eight.  In D and dX that is 2^-25 of a row's sum of |U| or |A|, but p = s U^T dD is that
+ * small itself while U is near 0, or where dD comes from a mean, and then d_down is as far
+ * off.  With `wide`, on fp16 plans, rows have 3 P columns: low parts, high parts, and what the high
+ * parts lost times 2^11, which gemm_adapters_grad takes instead of the low ones: 22 bits from
+ * 2^-14 on, off by 2^-36 below.
  *
  * Types.  X, W, down, up, dD and hidden are of the plan's type, GEMM_F16 or
  * GEMM_BF16; scale and bias fp32; D and the two gradients GEMM_F32 or the plan's
@@ -73,9 +81,11 @@ typedef struct {
     const float *scale;        /* [count], or NULL (ones) */
     const int32_t *index;      /* [M] */
     int64_t ldp;               /* gemm_adapters_grad: row stride of p, 0 for ldh */
+    int32_t wide;              /* 1: gemm_run_adapters's hidden, gemm_adapters_grad's p is wide (fp16 plans) */
+    int32_t wide_h;            /* 1: gemm_adapters_grad's h is */
 } gemm_adapters_t;
 
-/* Columns of `hidden`: 2 P, P = 16, 32, 64 or 128, the smallest that holds the
+/* Columns of `hidden` (not wide): 2 P, P = 16, 32, 64 or 128, the smallest that holds the
  * rank; 0 for a rank out of range. */
 int64_t gemm_adapters_hidden_width(int64_t rank);
 
@@ -91,7 +101,8 @@ gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void *X, const void *W, 
  * (M x N), both row-major, h and p.  The adapters' gradients lie one after
  * another, or their rows in turn (down_ld >= (count - 1) down_stride + K); in a
  * stack whose matrices overlap their CTAs would write the same memory
- * (GEMM_ERR_INVALID_ARG).  Of `adapters` count, rank, index and ldp are used.
+ * (GEMM_ERR_INVALID_ARG).  Of `adapters` count, rank, index, ldp, wide and
+ * wide_h are used.
  * Either of d_down and d_up may be NULL, with what only it needs. */
 gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void *X, const void *dD, int64_t M, int64_t N, int64_t K,
                                  int64_t ldx, int64_t lddd, const gemm_adapters_t *adapters, const void *h,

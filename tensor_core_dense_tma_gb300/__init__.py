@@ -723,7 +723,8 @@ class Plan:
         M x K, B K x N in either order, down G x R x K, up G x N x R (R <= 128, either of
         the last two dimensions contiguous), scale G fp32 numbers, bias N.  D is of
         the plan's type unless out_dtype or D says otherwise.  hidden (M rows, as
-        gemm_adapters_hidden_width says, allocated if not given) is what
+        gemm_adapters_hidden_width says, allocated if not given; on an "f16" plan it may be given with
+        half as many columns more, for values far below 1e-3, see adapters.h) is what
         linear_adapters_grad wants of the forward pass."""
         return _adapters.linear(self, X, B, down, up, index, scale, D, bias, hidden, out_dtype, stream)
 

@@ -35,7 +35,7 @@ class Adapters(ctypes.Structure):
                 ("down_ld", ctypes.c_int64), ("down_stride", ctypes.c_int64), ("down_layout", ctypes.c_int),
                 ("up", ctypes.c_void_p), ("up_ld", ctypes.c_int64), ("up_stride", ctypes.c_int64),
                 ("up_layout", ctypes.c_int), ("scale", ctypes.c_void_p), ("index", ctypes.c_void_p),
-                ("ldp", ctypes.c_int64)]
+                ("ldp", ctypes.c_int64), ("wide", ctypes.c_int32), ("wide_h", ctypes.c_int32)]
 
 
 def declare(lib: ctypes.CDLL) -> None:
@@ -60,7 +60,8 @@ def _lib():
     _calls.update(torch=torch, error=GemmError, run=lib.gemm_run_adapters, grad=lib.gemm_adapters_grad,
                   codes={torch.float16: DTYPE["f16"], torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"]},
                   types={"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}, empty=torch.empty,
-                  stream=torch._C._cuda_getCurrentRawStream, f32=torch.float32, i32=torch.int32)
+                  stream=torch._C._cuda_getCurrentRawStream, f32=torch.float32, f16=torch.float16,
+                  i32=torch.int32)
     return _calls
 
 
@@ -130,13 +131,15 @@ def _adapters(down, up, index, scale, M, N, K, di, dtype):
             None if scale is None else scale.data_ptr(), index.data_ptr())
 
 
-def _hidden(hidden, what, M, R, dev, di, dtype):
+def _hidden(hidden, M, R, dev, di, dtype):
+    """(hidden, its row stride, whether it is wide); allocated if not given."""
     width = hidden_width(R)
     if hidden is None:
-        return _calls["empty"]((M, width), dtype=dtype, device=dev), width
-    if hidden.shape != (M, width):
-        raise ValueError(f"{what} must be {M} x {width}")
-    return hidden, _row_ld(hidden, what, di, dtype)
+        return _calls["empty"]((M, width), dtype=dtype, device=dev), width, 0
+    wide = 1 if dtype is _calls["f16"] and hidden.shape == (M, width // 2 * 3) else 0
+    if not wide and hidden.shape != (M, width):
+        raise ValueError(f"hidden must be {M} x {width}" + (f" or {M} x {width // 2 * 3}" if dtype is _calls["f16"] else ""))
+    return hidden, _row_ld(hidden, "hidden", di, dtype), wide
 
 
 def _weights(B, di: int, dtype, K, N):
@@ -182,8 +185,8 @@ def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, strea
     if bias is not None and (bias.dtype is not calls["f32"] or bias.shape != (N,) or bias.get_device() != di
                              or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous fp32 vector of length N on X's device")
-    hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
-    a = Adapters(G, R, *lower, *upper, scales, at)
+    hidden, ldh, wide = _hidden(hidden, M, R, dev, di, dtype)
+    a = Adapters(G, R, *lower, *upper, scales, at, 0, wide)
     if stream is None:
         stream = calls["stream"](di)
     else:
@@ -226,14 +229,16 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
         raise ValueError("hidden must be what linear_adapters returned")
     given = dX, d_down, d_up
     dX, x_type, lddx = _result(dX, "dX", M, K, di, dev, None, dtype)
-    hidden, ldh = _hidden(hidden, "hidden", M, R, dev, di, dtype)
+    hidden, ldh, wide = _hidden(hidden, M, R, dev, di, dtype)
     like = d_down if d_down is not None else d_up
     out = dtype if like is None else like.dtype
     if out not in (calls["f32"], dtype) or (d_up is not None and d_up.dtype is not out):
         raise ValueError("d_down and d_up must both be fp32 or both of the plan's type")
     d_down, down_ld, down_stride = _gradient(d_down, out, dev, di, (G, R, K), "d_down")
     d_up, up_ld, up_stride = _gradient(d_up, out, dev, di, (G, N, R), "d_up")
-    ldp = hidden_width(R)
+    # (p is far smaller than h while up is near 0)
+    f16 = 1 if dtype is calls["f16"] else 0
+    ldp = hidden_width(R) // 2 * (2 + f16)
     p = calls["empty"]((M, ldp), dtype=dtype, device=dev)
     if stream is None:
         stream = calls["stream"](di)
@@ -241,7 +246,7 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
         _stream(stream, dev, p, *[t for t, g in zip((dX, d_down, d_up), given) if g is None])
     # dX is the same product the other way round (a matrix's transpose is the same memory in
     # the other order), and leaves p as its hidden rows
-    a = Adapters(G, R, *upper[:3], 1 - upper[3], *lower[:3], 1 - lower[3], scales, at, ldp)
+    a = Adapters(G, R, *upper[:3], 1 - upper[3], *lower[:3], 1 - lower[3], scales, at, ldp, f16, wide)
     this, other, kept, mine = X.data_ptr(), dY.data_ptr(), hidden.data_ptr(), p.data_ptr()
     st = calls["run"](plan.handle, other, B.data_ptr(), dX.data_ptr(), M, K, N, lddy, ldb, lddx, 1 - layout,
                       calls["codes"][x_type], None, ctypes.byref(a), mine, ldp, stream)

@@ -6,7 +6,9 @@
 //
 // h and p are kept as a high and a low part of the plan's type, high = round(h) and
 // low = round(h - high): products with both, added in fp32, lose 2^-17 (bf16) of h,
-// where high alone would lose 2^-9, as much as the rounding of D.
+// where high alone would lose 2^-9, as much as the rounding of D.  fp16 has no low parts below
+// 2^-24; the gradients of the factors, whose sums over high and low parts are apart until they
+// are stored, can have them times 2^11 (a third part: the product adds both in one sum).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,6 +44,7 @@ struct RowArgs {
     const int32_t* index;
     const float* scale;
     int32_t count, rank, part;
+    uint32_t wide;                    // 1: low, high and low parts times 2^11, else high and low ones
     uint16_t* hidden;
     int64_t ldh;
     uint32_t bf16;
@@ -105,8 +108,10 @@ __global__ void __launch_bounds__(kRowThreads) hidden_rows_kernel(const RowArgs 
         h = mine && r < a.rank ? (a.scale ? a.scale[g] * h : h) : 0.f;
         uint16_t hi, lo;
         adapter_split(h, bf16, hi, lo);
-        a.hidden[i * a.ldh + r] = hi;
-        a.hidden[i * a.ldh + a.part + r] = lo;
+        uint16_t* out = a.hidden + i * a.ldh + r;
+        out[a.wide ? a.part : 0] = hi;
+        out[a.wide ? 0 : a.part] = lo;
+        if (a.wide) out[2 * a.part] = tcdt::adapter_rest(h, hi);
     }
 }
 
@@ -129,6 +134,7 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 bool layout_ok(gemm_layout_t l) { return l == GEMM_ROW_MAJOR || l == GEMM_COL_MAJOR; }
 
 int part_of(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+int64_t hidden_columns(const gemm_adapters_t& a, bool wide) { return (wide ? 3 : 2) * part_of(a.rank); }
 
 // Makes the plan's device current, and the previous one again at the end.
 struct OnDevice {
@@ -152,6 +158,7 @@ gemm_status_t check_adapters(const gemm_plan* plan, int64_t M, int64_t N, int64_
     if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || a->count > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED;
     if (M > 0 && !a->index) return GEMM_ERR_INVALID_ARG;
     if (!aligned(a->index, 4) || !aligned(a->scale, 4)) return GEMM_ERR_MISALIGNED;
+    if ((a->wide || a->wide_h) && plan->in_dtype != GEMM_F16) return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
 }
 
@@ -241,7 +248,7 @@ gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* 
     if (row && by_rows(M, part, K)) {
         const RowArgs r{static_cast<const uint16_t*>(X), ldx, K, static_cast<const uint16_t*>(a.down), a.down_ld,
                         a.down_stride, a.index, a.scale, static_cast<int32_t>(a.count), static_cast<int32_t>(a.rank), part,
-                        static_cast<uint16_t*>(hidden), ldh, bf16};
+                        a.wide ? 1u : 0u, static_cast<uint16_t*>(hidden), ldh, bf16};
         hidden_rows_kernel<<<dim3(part / kRowValues, static_cast<unsigned>(M)), kRowThreads, 0, s>>>(r);
         return launched(plan, cudaGetLastError());
     }
@@ -252,6 +259,7 @@ gemm_status_t run_hidden(gemm_plan* plan, const gemm_adapters_t& a, const void* 
     h.count = static_cast<int32_t>(a.count);
     h.rank = static_cast<int32_t>(a.rank);
     h.part = part;
+    h.wide = a.wide ? 1u : 0u;
     h.rr = (h.rank + 15) / 16 * 16;
     h.a_mn = row ? 0u : 1u;
     h.per_stage = row && h.rr <= 32 ? 64 / h.rr : 1;
@@ -303,7 +311,7 @@ gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void* X, const void* W, 
     if (K > 0) st = check_stack(a.count, a.down, down_row ? K : a.rank, a.down_ld, a.down_stride);
     if (st == GEMM_OK && N > 0) st = check_stack(a.count, a.up, up_row ? a.rank : N, a.up_ld, a.up_stride);
     if (st == GEMM_OK) st = check_matrix(X, M, K, ldx);
-    if (st == GEMM_OK) st = check_matrix(hidden, M, 2 * part_of(a.rank), ldh);
+    if (st == GEMM_OK) st = check_matrix(hidden, M, hidden_columns(a, a.wide), ldh);
     if (st != GEMM_OK) return st;
     if (!aligned(bias, 4)) return GEMM_ERR_MISALIGNED;
     if (M == 0) return GEMM_OK;
@@ -312,7 +320,7 @@ gemm_status_t gemm_run_adapters(gemm_plan_t plan, const void* X, const void* W, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0 || a.count == 0) {
         // no adapter adds anything
-        st = launched(plan, cudaMemset2DAsync(hidden, ldh * 2, 0, 4 * part_of(a.rank), M, s));
+        st = launched(plan, cudaMemset2DAsync(hidden, ldh * 2, 0, 2 * hidden_columns(a, a.wide), M, s));
         if (st != GEMM_OK || N == 0) return st;
         const gemm_epilogue_t ep{bias, nullptr, nullptr, GEMM_ACT_NONE};
         return gemm_run_ep(plan, X, W, nullptr, D, M, N, K, ldx, ldw, ldd, GEMM_ROW_MAJOR, layoutW, GEMM_F32, out_dtype,
@@ -341,12 +349,12 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     const int64_t ldp = a.ldp ? a.ldp : ldh;
     if (d_down) {
         st = check_matrix(X, M, K, ldx);
-        if (st == GEMM_OK) st = check_matrix(p, M, 2 * part, ldp);
+        if (st == GEMM_OK) st = check_matrix(p, M, hidden_columns(a, a.wide), ldp);
         if (st == GEMM_OK) st = check_gradient(a.count, a.rank, K, down_ld, down_stride);
     }
     if (d_up && st == GEMM_OK) {
         st = check_matrix(dD, M, N, lddd);
-        if (st == GEMM_OK) st = check_matrix(h, M, 2 * part, ldh);
+        if (st == GEMM_OK) st = check_matrix(h, M, hidden_columns(a, a.wide_h), ldh);
         if (st == GEMM_OK) st = check_gradient(a.count, N, a.rank, up_ld, up_stride);
     }
     if (st != GEMM_OK) return st;
@@ -361,12 +369,15 @@ gemm_status_t gemm_adapters_grad(gemm_plan_t plan, const void* X, const void* dD
     const OnDevice on(plan->device);
     if (!on.ok) return GEMM_ERR_CUDA;
     const void* left[2] = {X, dD};
-    const void* right[2] = {p, h};
+    // (the high parts and those times 2^11 of wide rows)
+    const bool wide[2] = {a.wide != 0, a.wide_h != 0};
+    const uint16_t* right[2] = {static_cast<const uint16_t*>(p), static_cast<const uint16_t*>(h)};
     const int64_t columns[2] = {K, N}, ld[2] = {ldx, lddd}, ld_right[2] = {ldp, ldh};
     for (int i = 0; i < 2 && M > 0; ++i) {
         if (f.f[i].blocks == 0) continue;
+        f.f[i].low = wide[i] ? tcdt::kRestScale : 1.0f;
         st = encode_map(plan, &f.f[i].tmX, left[i], columns[i], M, ld[i], 64, 64, plan->in_dtype);
-        if (st == GEMM_OK) st = encode_map(plan, &f.f[i].tmH, right[i], 2 * part, M, ld_right[i], 64, 64, plan->in_dtype);
+        if (st == GEMM_OK) st = encode_map(plan, &f.f[i].tmH, right[i] + (wide[i] ? part : 0), 2 * part, M, ld_right[i], 64, 64, plan->in_dtype);
         if (st != GEMM_OK) return st;
     }
     f.f[0].out = d_down, f.f[0].stride = down_stride, f.f[0].sr = down_ld, f.f[0].sc = 1;

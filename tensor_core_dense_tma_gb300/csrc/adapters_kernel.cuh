@@ -80,6 +80,14 @@ __device__ __forceinline__ void adapter_split(float h, bool bf16, uint16_t& high
     low = adapter_bits(isfinite(x) ? h - x : 0.0f, bf16);
 }
 
+// What the high part of an fp16 value lost, times 2^11: at most 16 times that, within the type's range.
+constexpr float kRestScale = 0x1p-11f;
+
+__device__ __forceinline__ uint16_t adapter_rest(float h, uint16_t high) {
+    const float x = adapter_value(high, false);
+    return adapter_bits(isfinite(x) ? (h - x) * (1.0f / kRestScale) : 0.0f, false);
+}
+
 // Stage and phase of a ring.
 struct RingAt {
     int stage = 0;
@@ -98,6 +106,7 @@ struct HiddenArgs {
     const int32_t* index;
     const float* scale;
     int32_t count, rank, part;
+    uint32_t wide;            // 1: hidden is wide (adapters.h)
     int32_t rr;               // the rank in whole 16s
     int32_t per_stage;        // adapters of a stage, whose columns lie side by side:
     int32_t pitch;            // columns from one to the next (rr, or 64 or 128)
@@ -378,8 +387,15 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
                 for (int e = 0; e < 4; ++e)
                     adapter_split(c[k] + e < a.rank ? v[e] * factor[row[k]] : 0.0f, bf16, hi[e], lo[e]);
                 uint16_t* out = a.hidden + (row0 + row[k]) * a.ldh + c[k];
-                *reinterpret_cast<uint2*>(out) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                *reinterpret_cast<uint2*>(out + a.part) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                *reinterpret_cast<uint2*>(out + (a.wide ? a.part : 0)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2*>(out + (a.wide ? 0 : a.part)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                if (a.wide) {
+                    uint32_t rest[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        rest[e] = adapter_rest(c[k] + e < a.rank ? v[e] * factor[row[k]] : 0.0f, hi[e]);
+                    *reinterpret_cast<uint2*>(out + 2 * a.part) = make_uint2(rest[0] | rest[1] << 16, rest[2] | rest[3] << 16);
+                }
             }
         }
     }
@@ -397,7 +413,8 @@ __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __gr
 // gradients of the factors: for an adapter g, sum over its rows of x[i] h[i]^T
 // ---------------------------------------------------------------------------
 struct FactorArgs {
-    CUtensorMap tmX, tmH;     // of each 64 x 64 boxes
+    CUtensorMap tmX, tmH;     // of each 64 x 64 boxes; tmH's columns are high and low parts
+    float low;                // what the low parts count: 1, or 2^-11 of those times 2^11
     void* out;                // element (g, r, c) at out[g * stride + r * sr + c * sc]
     int64_t stride, sr, sc;
     int32_t columns, blocks;  // blocks of 128 columns
@@ -619,7 +636,8 @@ __global__ void __launch_bounds__(kAdapterThreads) factor_grad_kernel(const __gr
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (r + i < a.rank)
-                        to[(r + i) * kFactorPitch] = used ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : 0.0f;
+                        to[(r + i) * kFactorPitch] =
+                            used ? fmaf(__uint_as_float(lo[i]), f.low, __uint_as_float(hi[i])) : 0.0f;
             }
             tc_fence_before_sync();
         }
