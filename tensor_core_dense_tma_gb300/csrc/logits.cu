@@ -1304,13 +1304,16 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(const Pairs a) {
             reward[side] *= a.beta;
             a.reward[2 * pair + side] = static_cast<float>(reward[side]);
         }
-        // -log sigma(m) = log1p(e^-|m|) + max(-m, 0), sigma from the same exponential
-        // (32 bits from here on: in 64 one thread took 4 us for them)
-        const float m = static_cast<float>(reward[0] - reward[1]), e = a.smoothing;
-        const float x = expf(-fabsf(m)), l = log1pf(x);
+        // -log sigma(m) = log1p(e^-|m|) + max(-m, 0), sigma from the same exponential.  |m| in two
+        // fp32 parts, far + near: rounded to 32 bits it would be off by 2^-24 |m|, and so would
+        // sigma, relatively.  (All of it in 64 bits took one thread 4 us.)
+        const double margin = reward[0] - reward[1];
+        const float m = static_cast<float>(margin), e = a.smoothing, far = fabsf(m);
+        const float near = isfinite(m) ? static_cast<float>(fabs(margin) - static_cast<double>(far)) : 0.f;
+        const float x0 = expf(-far), x = fmaf(-near, x0, x0), l = log1pf(x);
         const float less = x / (1.f + x), more = 1.f / (1.f + x);
-        const float right = e == 1.f ? 0.f : (1.f - e) * (l + (m < 0.f ? -m : 0.f));
-        const float wrong = e == 0.f ? 0.f : e * (l + (m > 0.f ? m : 0.f));
+        const float right = e == 1.f ? 0.f : (1.f - e) * (m < 0.f ? (l + near) + far : l);
+        const float wrong = e == 0.f ? 0.f : e * (m > 0.f ? (l + near) + far : l);
         a.loss[pair] = m != m ? m : right + wrong;
         if (a.w) {
             const float d = e * (m < 0.f ? less : more) - (1.f - e) * (m < 0.f ? more : less);
