@@ -506,16 +506,21 @@ __device__ __forceinline__ float teacher_value(const void* p, int type, int64_t 
 // KL term is e^d - 1 - d >= 0, from expm1: for small d it is d^2 / 2, of which
 // e^d in fp32 would keep nothing.  A NaN is not lost in the minimum.
 struct PolicyLoss {
-    float loss, kl, slope;
+    float loss, kl, slope, logprob;
 };
 
-__device__ __forceinline__ PolicyLoss policy_loss(const Args& a, int64_t r, float logprob) {
-    const float A = a.advantage[r], ratio = expf(logprob - a.old_logprob[r]);
-    const float free = ratio * A, bounded = fminf(fmaxf(ratio, a.lo), a.hi) * A;
-    PolicyLoss l{-bounded, 0.f, 0.f};
+__device__ __forceinline__ PolicyLoss policy_loss(const Args& a, float logprob, float A, float old, float ref) {
+    const float x = logprob - old, ratio = expf(x);
+    const float bounded = fminf(fmaxf(ratio, a.lo), a.hi) * A;
+    float free = ratio * A;
+    if (ratio == INFINITY && x != INFINITY) {      // beyond fp32, which the product need not be
+        const float half = expf(0.5f * x);
+        free = A == 0.f ? 0.f : half * A * half;
+    }
+    PolicyLoss l{-bounded, 0.f, 0.f, logprob};
     if (!(free > bounded)) l.loss = l.slope = -free;
     if (a.ref_logprob) {
-        const float d = a.ref_logprob[r] - logprob, e = expm1f(d);
+        const float d = ref - logprob, e = expm1f(d);
         l.kl = e == INFINITY ? e : e - d;
         if (a.kl_coef != 0.f) l.loss = fmaf(a.kl_coef, l.kl, l.loss), l.slope = fmaf(-a.kl_coef, e, l.slope);
     }
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Stats warp_stats[kWarps];
     __shared__ Exchange inbox[kMaxCluster], all;
-    __shared__ LogSum row_log;
+    __shared__ PolicyLoss row_policy;
     __shared__ bool heard;                               // of every CTA of the row
     __shared__ volatile int gave_up;                     // on a copy
     __shared__ __align__(8) uint64_t full_bar[kSlotsMost], empty_bar[kSlotsMost], inbox_bar;
@@ -1004,6 +1009,11 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         // The segments' statistics into every CTA's shared memory, lane i's
         // copy to CTA i, and the row's joined from them.
         if (warp == 0) {
+            float advantage = 0.f, old_logprob = 0.f, ref_logprob = 0.f;      // asked for before the others' statistics
+            if constexpr (OP == kPolicy) {
+                advantage = a.advantage[r], old_logprob = a.old_logprob[r];
+                if (a.ref_logprob) ref_logprob = a.ref_logprob[r];
+            }
             Exchange x{s, A, p};
             bool arrived = true;
             if (a.cluster > 1) {
@@ -1035,8 +1045,12 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
             __syncwarp();
             if (lane == 0) {
                 all = {s, l, sum_P};
-                // (for all threads of a policy loss: computed by each of them it took 2 % longer)
-                if constexpr (OP == kPolicy) row_log = log_sum(s.S, s.U, a.c_rest);
+                // (computed by every thread, a policy loss took 3 % longer)
+                if constexpr (OP == kPolicy) {
+                    const float logprob =
+                        s.S == 0.f ? -INFINITY : log_p(z_token, s.m, log_sum(s.S, s.U, a.c_rest), a.t, a.inv_t);
+                    row_policy = policy_loss(a, logprob, advantage, old_logprob, ref_logprob);
+                }
                 if constexpr (TOP) heard = arrived;
             }
         }
@@ -1046,24 +1060,18 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
         const bool nothing = s.S == 0.f;
         const float log2_S = lg2(s.S);
         const float entropy = nothing ? 0.f : kLn2 * (log2_S - s.U / s.S);
-        auto log_of_row = [&] { return OP == kPolicy ? row_log : log_sum(s.S, s.U, a.c_rest); };
-        PolicyLoss policy{};
-        if constexpr (OP == kPolicy) {
-            const float logprob = nothing ? -INFINITY : log_p(z_token, s.m, row_log, a.t, a.inv_t);
-            policy = policy_loss(a, r, logprob);
-            if (a.bonus != 0.f) policy.loss = fmaf(-a.bonus, entropy, policy.loss);
-        }
         if (rank == 0 && tid == 0) {
             if (a.lse) a.lse[r] = nothing ? -INFINITY : fmaf(s.m, a.inv_t, kLn2 * log2_S);
             if constexpr (OP != kDistill) {
                 if (a.logprob)
-                    a.logprob[r] = token < 0 ? 0.f
-                                   : nothing ? -INFINITY
-                                             : log_p(z_token, s.m, log_of_row(), a.t, a.inv_t);
+                    a.logprob[r] = token < 0       ? 0.f
+                                   : OP == kPolicy ? row_policy.logprob
+                                   : nothing       ? -INFINITY
+                                                   : log_p(z_token, s.m, log_sum(s.S, s.U, a.c_rest), a.t, a.inv_t);
                 if (a.entropy) a.entropy[r] = entropy;
                 if constexpr (OP == kPolicy) {
-                    a.loss[r] = policy.loss;
-                    if (a.kl) a.kl[r] = policy.kl;
+                    a.loss[r] = a.bonus != 0.f ? fmaf(-a.bonus, entropy, row_policy.loss) : row_policy.loss;
+                    if (a.kl) a.kl[r] = row_policy.kl;
                 }
                 if constexpr (OP == kScore)
                     if (a.state) a.state[r] = {s.m, nothing ? INFINITY : log2_S, 0.f, 0.f};
@@ -1079,7 +1087,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                 float g, h;
                 if constexpr (OP == kPolicy) {
                     const float w = a.w[r];
-                    g = w * policy.slope;
+                    g = w * row_policy.slope;
                     h = a.bonus != 0.f ? -a.bonus * w : 0.f;
                 } else {
                     g = token >= 0 && a.g ? a.g[r] : 0.f;
@@ -1216,7 +1224,7 @@ __global__ void __launch_bounds__(kBlock, ctas_of(GRAD)) rows_kernel(const Args 
                     sync_threads();
                     keys = top->cand;
                 }
-                const LogSum l = log_of_row();
+                const LogSum l = log_sum(s.S, s.U, a.c_rest);
                 for (int i = tid; i < lists * n; i += kThreads) {
                     const uint64_t k = keys[i];
                     if (!k) continue;
