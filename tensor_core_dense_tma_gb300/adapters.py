@@ -172,8 +172,8 @@ def linear(plan, X, B, down, up, index, scale, D, bias, hidden, out_dtype, strea
     calls = _calls or _lib()
     types = calls["types"]
     dtype, dev, di = types.get(plan.in_dtype), X.device, X.get_device()
-    if dtype is None or dtype is calls["f32"] or di < 0 or X.dim() != 2 or B.dim() != 2:
-        raise ValueError("adapters take 2-D device tensors and an f16 or bf16 plan")
+    if dtype is None or dtype is calls["f32"] or di != plan.device or X.dim() != 2 or B.dim() != 2:
+        raise ValueError("adapters take 2-D tensors on the plan's device and an f16 or bf16 plan")
     (M, K), (KB, N) = X.shape, B.shape
     ldx = _row_ld(X, "X", di, dtype)
     if KB != K:
@@ -216,8 +216,8 @@ def linear_grad(plan, dY, B, X, hidden, down, up, index, scale, dX, d_down, d_up
     """Plan.linear_adapters_grad."""
     calls = _calls or _lib()
     dtype, dev, di = calls["types"].get(plan.in_dtype), X.device, X.get_device()
-    if dtype is None or dtype is calls["f32"] or di < 0 or X.dim() != 2 or dY.dim() != 2 or B.dim() != 2:
-        raise ValueError("adapters take 2-D device tensors and an f16 or bf16 plan")
+    if dtype is None or dtype is calls["f32"] or di != plan.device or X.dim() != 2 or dY.dim() != 2 or B.dim() != 2:
+        raise ValueError("adapters take 2-D tensors on the plan's device and an f16 or bf16 plan")
     (M, K), (MY, N) = X.shape, dY.shape
     if MY != M or B.shape != (K, N):
         raise ValueError("dY must be M x N, B K x N")

@@ -135,3 +135,36 @@ def test_hidden_in_a_wide_buffer(plans, kind, R):      # noqa: F811
     torch.cuda.synchronize()
     assert torch.cuda.max_memory_allocated() - before <= 2 * hidden.numel() * hidden.element_size() + (2 << 20)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_plan_of_another_device(tc):      # noqa: F811
+    """Tensors that are not on the plan's device: its kernels cannot read them (a plan that says it is on another)."""
+    c = Case(40, 264, 520, 16, 3, "bf16", seed=46, index="mixed")
+    with tc.Plan("bf16", 0) as plan:
+        _, hidden = plan.linear_adapters(c.X, *c.args())
+        plan.device = 1
+        with pytest.raises(ValueError, match="device"):
+            plan.linear_adapters(c.X, *c.args())
+        with pytest.raises(ValueError, match="device"):
+            plan.linear_adapters_grad(c.dY, c.B, c.X, hidden, c.down, c.up, c.index, c.scale)
+        plan.device = 0
+        plan.linear_adapters(c.X, *c.args())
+        torch.cuda.synchronize()
+        assert plan.device_status() == 0
+
+
+@pytest.mark.parametrize("K,G", [(0, 2), (64, 0)])
+def test_far_hidden_without_adapters(plans, K, G):      # noqa: F811
+    """Rows of zeros 2^30 elements apart."""
+    plan = plans["bf16"]
+    far = 1 << 30
+    buf = torch.full((2 * far + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    hidden = torch.as_strided(buf, (3, 32), (far, 1), 8)
+    z = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")      # noqa: E731
+    bias = torch.arange(40, device="cuda").float()
+    D, _ = plan.linear_adapters(z(3, K), z(K, 40), z(G, 8, K), z(G, 40, 8), torch.zeros(3, dtype=torch.int32, device="cuda"),
+                                bias=bias, hidden=hidden)
+    torch.cuda.synchronize()
+    assert not hidden.any() and torch.equal(D, (bias + K).bfloat16().expand(3, 40))
+    for i in range(3):
+        assert bool((buf[i * far:i * far + 8] == 7).all()) and bool((buf[i * far + 40:i * far + 64] == 7).all())
