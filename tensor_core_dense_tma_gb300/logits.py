@@ -183,7 +183,8 @@ def _stream(stream, device, *own):
     current = torch._C._cuda_getCurrentRawStream(device.index)    # current_stream() takes 2 us to make an object
     if stream is None or stream == current:
         return current
-    other = torch.cuda.ExternalStream(stream, device=device)
+    # (torch has no stream of the handle cudaStreamLegacy, 1, which is 0's)
+    other = torch.cuda.ExternalStream(0 if stream == 1 else stream, device=device)
     for t in own:
         if t is not None:
             t.record_stream(other)

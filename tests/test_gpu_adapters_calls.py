@@ -168,3 +168,26 @@ def test_far_hidden_without_adapters(plans, K, G):      # noqa: F811
     assert not hidden.any() and torch.equal(D, (bias + K).bfloat16().expand(3, 40))
     for i in range(3):
         assert bool((buf[i * far:i * far + 8] == 7).all()) and bool((buf[i * far + 40:i * far + 64] == 7).all())
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2], ids=["default", "legacy", "per_thread"])
+def test_default_streams_by_handle(plans, tc, handle):      # noqa: F811
+    """The runtime's default streams, by the handles that stand for them, while torch's current stream is another."""
+    plan = plans["bf16"]
+    c = Case(40, 264, 520, 16, 3, "bf16", seed=47, index="mixed")
+    D, hidden = plan.linear_adapters(c.X, *c.args())
+    args = (c.dY, c.B, c.X, hidden, c.down, c.up, c.index, c.scale)
+    g = plan.linear_adapters_grad(*args)
+    z = torch.randn((20, 300), device="cuda")
+    t, at = torch.randint(0, 300, (20,), device="cuda"), torch.tensor([0, 9, 20], device="cuda")
+    w = torch.ones(1, device="cuda")
+    p = tc.preference_loss_grad(z, t, at, w)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = (*plan.linear_adapters(c.X, *c.args(), stream=handle), *plan.linear_adapters_grad(*args, stream=handle),
+                   *tc.preference_loss_grad(z, t, at, w, stream=handle))
+            torch.full((4096, 32), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, (D, hidden, *g, *p)))
+        del got
