@@ -24,7 +24,8 @@
  * from gemm_adapters_grad with h and p.  A row's results depend on that row,
  * W and its own adapter alone: infinities and NaN of other rows and
  * adapters do not reach it, nor those of other adapters' rows an
- * adapter's gradients.  Rows of an adapter need not be neighbours.
+ * adapter's gradients.  (Its own ones do, an infinity of U, X or dD as a NaN where the low
+ * part of h or p that it meets is 0.)  Rows of an adapter need not be neighbours.
  *
  * h and p are handed on as `hidden`: M rows of P = gemm_adapters_hidden_width(rank) / 2
  * high parts, the values rounded to the plan's type, and P low parts, what that

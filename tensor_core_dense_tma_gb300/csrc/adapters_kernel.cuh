@@ -141,7 +141,8 @@ __host__ __device__ constexpr int hidden_stage_bytes(int rr) {
 // other rows as they are.  (An MMA costs some 95 cycles to issue however narrow it is:
 // one for all adapters of a stage, not one each.)  8192 x 8192, rank 64, four
 // adapters: 30 us (134 MB, 20 at the copy rate); 2048 x 4096, rank 32: 9.5, of which 5
-// are start and end; 64 adapters of rank 16 in turn, K = 8192, 146 for 64 to 1024 rows.
+// are start and end; 64 adapters of rank 16 in turn, K = 8192, 145 for 512 to 1024 rows, of rank-contiguous
+// factors (one adapter a stage) 311 for 64 to 1024.
 __global__ void __launch_bounds__(kAdapterThreads) hidden_tile_kernel(const __grid_constant__ HiddenArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ AdapterPipe q;

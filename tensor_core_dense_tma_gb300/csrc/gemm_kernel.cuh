@@ -1335,8 +1335,8 @@ gemm_sm103_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         uint32_t off[kRows / 32];
                         int g;
                         if constexpr (kAdapterTokens) {
-                            // up to four adapters a step (one after another took 400 cycles each, 16 x
-                            // 8192 x 8192 with 16 of rank 16 3 us)
+                            // up to four adapters a step (one after another took 400 cycles each: 16 x 8192 x
+                            // 8192 with 16 of rank 16 takes 32.9 us so, with N-contiguous U one by one 36.4; rank 32 38.1)
                             bool more = ad.packed != 0;
                             while (ok && more) {
                                 int four[4], n = 0;

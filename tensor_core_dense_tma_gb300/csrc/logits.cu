@@ -499,7 +499,7 @@ __device__ __forceinline__ float teacher_value(const void* p, int type, int64_t 
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
 }
 
-// The policy operator (4096 x 131072 bf16 with gradient 390 us, 0.82 of the copy rate; 2048 x 65537
+// The policy operator (4096 x 131072 bf16 with gradient 388 us, 0.83 of the copy rate; 2048 x 65537
 // without entropy bonus, a quarter of the rows unread, 84, with the bonus's arithmetic 88).
 // Policy loss of a row without its entropy bonus, its KL term and the loss's
 // derivative with respect to the log-probability.  With d = ref - logprob the
