@@ -374,12 +374,14 @@ constexpr float kEx2Lacks = 5.0e-8f;
 
 // raise_max for a sum that is joined with others.  Every value goes through several exponentials on its
 // way into the row's sum, its own and those that scale it to the maximum of the warp, the block and the
-// cluster, all off to one side: what the factor lacks (and `more`) is put back, before the product is
-// rounded (afterwards, below half a unit of S, it would be lost).
+// cluster, all off to one side: what the factor lacks (and `more`) is put back, before the products are
+// rounded (afterwards, below half a unit, it would be lost); in U too, which the entropy divides by S.
 __device__ __forceinline__ void raise_joined(Stats& s, float m, float c, float more) {
-    const float S = s.S, d = max_nan((s.m - m) * c, -1e4f);
-    raise_max(s, m, c);
-    s.S = fmaf(S, ex2(d), s.S * fmaf(fminf(-d, 1.f), kEx2Lacks, more));
+    const float S = s.S, d = max_nan((s.m - m) * c, -1e4f), f = ex2(d);
+    const float U = fmaf(d, S, s.U), lacks = fmaf(fminf(-d, 1.f), kEx2Lacks, more);
+    s.U = fmaf(U, f, U * f * lacks);
+    s.S = fmaf(S, f, S * f * lacks);
+    s.m = m;
 }
 
 // Two floats in a register pair, and the packed arithmetic on them.

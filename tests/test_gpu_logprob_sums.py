@@ -111,3 +111,21 @@ def test_extremes(tc, kind):      # noqa: F811
     r = tc.token_logprobs(z, tokens, top=4)
     assert r.top_token[0].tolist() == [0, 1, 2, 4] and r.top_token[1].tolist() == [-1] * 4 and r.top_token[6].tolist() == [0, 1, 2, -1]
     assert bool((r.top_logprob[6, :3] == r.logprob[6]).all()) and r.top_logprob[6, 3].item() == -inf
+
+
+@pytest.mark.parametrize("V,T,size", [(4099, 16384, 2.0), (32768, 4096, 2.0), (32768, 4096, 0.5)])
+def test_mean_of_logits(tc, V, T, size):      # noqa: F811
+    """entropy - lse is minus the mean logit: both have the same logarithm of S, so what is left is the sum of u 2^u over S,
+    whose two sums lack the same.  Its mean error: the roundings of two numbers of 16 or less, as above, and 2^-25 of itself."""
+    z, _, _ = logits(T, V, "f32", 3, size)
+    want, least = [], []
+    for part in z.split(1024):
+        x = part.double()
+        want.append(-(torch.softmax(x, 1) * x).sum(1))
+        least.append(x.amax(1))
+    want = torch.cat(want)
+    one = torch.ones(T, device="cuda")
+    tokens = torch.zeros(T, dtype=torch.int64, device="cuda")
+    for r in (tc.token_logprobs(z), tc.token_logprobs(z, top=2), tc.token_logprobs_grad(z, tokens, one, one)):
+        e = r.entropy.double() - r.lse.double() - want
+        assert abs(e.mean().item()) <= 6 * 2.0 ** -20 / math.sqrt(T) + (torch.cat(least) + want).mean().item() * 2.0 ** -25
